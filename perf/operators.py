@@ -360,7 +360,7 @@ def _unit_views(cache):
 def _quantise(x):
     """FP32 rows [..., D] -> codes and their FP16 (scale, offset)."""
     lo, hi = x.amin(-1, keepdim=True), x.amax(-1, keepdim=True)
-    s = ((hi - lo) / 15.0).half().float()
+    s = ((hi - lo) * (1.0 / 15.0)).half().float()
     z = (lo + 8.0 * s).half().float()
     r = torch.where(s > 0, 1.0 / s, torch.zeros_like(s))
     q = (torch.round((x - z) * r) + 8.0).clamp(0.0, 15.0).to(torch.uint8)
