@@ -19,8 +19,8 @@ namespace {
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_cus[kMaxDevices];  // 0 = not yet queried
 
-// Compute units of the current device, cached per device.  Returns <= 0 on
-// failure.
+}  // namespace
+
 int current_cus(int* device_out) {
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return -1;
@@ -39,6 +39,8 @@ int current_cus(int* device_out) {
   g_cus[dev].store(cus, std::memory_order_relaxed);
   return cus;
 }
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

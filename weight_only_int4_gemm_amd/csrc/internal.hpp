@@ -53,6 +53,10 @@ struct WeightFormat {
   const uint8_t* zeros;
 };
 
+// Compute units of the current device, cached per device (api.hip); its
+// number goes to *device_out if that is not null.  Returns <= 0 on failure.
+int current_cus(int* device_out);
+
 Plan make_plan(int M, int K, int N, int group, int cus, int fmt = 0);
 
 // The streaming kernel with activations in LDS (gemm.hip): batches of at

@@ -1,0 +1,716 @@
+// Attention over the paged 4-bit cache (kv4_attention).
+//
+// Mathematics.  With key row k_j = (c_j - 8) s_j + z_j (codes c, scale s,
+// offset z) a score is  q . k_j = s_j (q . c_j - 8 sum q) + z_j sum q, and
+// with value row v_j likewise the output is
+//   sum_j p_j v_j = sum_j (p_j s_j)(c_j - 8) + sum_j p_j z_j,
+// so the codes go into the matrix instruction as they are and scales and
+// offsets touch one number per key or per probability instead of D.
+//
+// Codes as operands.  Four bits c in the mantissa of an FP16 whose other bits
+// are zero are the subnormal c 2^-24 (16 c 2^-24 when they sit one nibble
+// higher); the matrix instruction takes subnormals exactly.  One AND per two
+// codes is then the whole unpacking.
+//
+// Layout.  The keys are the first operand (rows = 16 tokens), the queries the
+// second (columns = 16 query rows), so lane l holds scores of column l % 16
+// for tokens 4 (l / 16) + i.  The product with the values wants exactly those
+// probabilities as its second operand (k = tokens), with values transposed as
+// the first: lane l reads, for the eight tokens it holds probabilities of, the
+// words of channels 8 (l % 16) .. + 7 and pairs tokens byte by byte.  Nothing
+// crosses lanes, and every load is 16 bytes per lane.
+//
+// Softmax.  A running reference m per column (base 2, with the value scales
+// in it): weights w = 2^(x - m) s stay below 2^15 for FP16, sums are FP32.  m
+// moves only when a weight or the sum would leave its range, so the usual
+// tile has no reduction across lanes and no rescaling.  The weights' rounding
+// to FP16 is the only one before the output; the -8 is applied to the sum of
+// the rounded weights (a product with a row of ones), so it cancels exactly.
+// For BF16 outputs that rounding is an eighth of the output's own.  For FP16
+// outputs it would be as large as it, so there the weights are two FP16
+// numbers, the rounded weight and its remainder, and the product with the
+// values runs twice.
+#include <cstdio>
+
+#include "../../include/w4a16_kv4.h"
+#include "coherent.hpp"
+#include "internal.hpp"
+#include "kv4.hpp"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kTile = 32;                   // tokens of one step: two units
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kNone = -1e30f;             // reference of a column that has seen no key
+constexpr float kMostWeight = 32768.0f;     // of a weight, before the reference moves
+constexpr float kTopWeight = 8.0f;          // log2 of the largest weight after it has
+constexpr float kMostSum = 0x1p60f;         // of a tile's probabilities, likewise
+constexpr float kSumHeadroom = 40.0f;       // log2 of a probability over the reference
+
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ float4v mfma(const uint4v& a, const uint4v& b, const float4v& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a),
+                                                __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float low_half(uint32_t w) {
+  return (float)__builtin_bit_cast(half2v, w)[0];
+}
+__device__ __forceinline__ float high_half(uint32_t w) {
+  return (float)__builtin_bit_cast(half2v, w)[1];
+}
+__device__ __forceinline__ uint32_t pack_halves(float a, float b) {
+  const half2v h = {(_Float16)a, (_Float16)b};  // round half to even
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+// Sum and maximum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ float groups_sum(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+__device__ __forceinline__ float groups_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+
+// What one lane loads of two units.
+template <int D>
+struct TileData {
+  static constexpr int KV = D / 32;                 // key words per unit
+  static constexpr int VV = D == 256 ? 2 : 1;       // value vectors per unit
+  uint32_t k[2][KV];
+  uint4v v[2][VV];
+  uint4v kp[2], vp[2];
+  bool valid[2];                                    // the unit's page exists
+};
+
+// The page ids of 64 pages from `first`, one per lane.
+struct PageIds {
+  const int32_t* row;
+  int max_pages, first, mine;
+  __device__ __forceinline__ void load(int page) {
+    first = page;
+    const int p = page + (int)(threadIdx.x & 63);
+    mine = p < max_pages ? row[p] : -1;
+  }
+  // `page` is the same in all lanes
+  __device__ __forceinline__ int at(int page) {
+    if (page - first >= 64) load(page);
+    return __builtin_amdgcn_readlane(mine, page - first);
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(TileData<D>& d, const KvAttentionArgs& a, int head,
+                                          int page_shift, PageIds& ids, int t) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int tu = t + kKvUnit * u;
+    const int id = ids.at(tu >> page_shift);
+    d.valid[u] = (unsigned)id < (unsigned)a.pages;
+    const uint8_t* unit = a.cache + kv_unit_offset<D>(d.valid[u] ? id : 0, a.H, head, a.page,
+                                                      tu & (a.page - 1));
+    const uint8_t* kp = unit + r * (D / 2) + g * (D / 8);
+    if constexpr (D == 64) {
+      const uint2v w = *reinterpret_cast<const uint2v*>(kp);
+      d.k[u][0] = w[0];
+      d.k[u][1] = w[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i) {
+        const uint4v w = reinterpret_cast<const uint4v*>(kp)[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d.k[u][4 * i + j] = w[j];
+      }
+    }
+    const uint8_t* vp = unit + KvUnit<D>::values + g * (2 * D);
+    const int word = D == 64 ? r >> 1 : r;
+#pragma unroll
+    for (int i = 0; i < TileData<D>::VV; ++i)
+      d.v[u][i] = reinterpret_cast<const uint4v*>(vp)[word + 16 * i];
+    d.kp[u] = reinterpret_cast<const uint4v*>(unit + KvUnit<D>::key_params)[g];
+    d.vp[u] = reinterpret_cast<const uint4v*>(unit + KvUnit<D>::value_params)[g];
+  }
+}
+
+// The sums of 16 * NB query rows over the tokens seen so far, for column
+// (row) lane % 16 of each block.
+template <int D, int NB>
+struct Sums {
+  float4v acc[NB][D / 16];  // sum of w c, in the operands' units
+  float4v w[NB];            // sum of w (every element the same)
+  float m[NB];              // reference
+  float l[NB], z[NB];       // this lane's part of sum p, sum p z
+};
+
+// A wave's query rows as operands, and what its columns need.
+template <int D, int NB>
+struct Queries {
+  uint4v even[NB][D / 64], odd[NB][D / 64];  // channels by parity of the nibble
+  float sum8[NB];    // -8 sum q, in the products' units
+  float unit[NB];    // product units to base-2 logits
+  float sum[NB];     // sum q in base-2 logits
+  int lo[NB], hi[NB];  // keys seen: lo <= j <= hi
+};
+
+template <int D, int NB, bool BF16>
+__device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB>& q,
+                                       Sums<D, NB>& s, int t, bool edge) {
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+
+  float4v even[NB][2], odd[NB][2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      even[nb][u] = float4v{q.sum8[nb], q.sum8[nb], q.sum8[nb], q.sum8[nb]};
+      odd[nb][u] = float4v{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p) {
+      const uint32_t w0 = d.k[u][2 * p], w1 = d.k[u][2 * p + 1];
+      const uint4v e = {w0 & kLow, w1 & kLow, (w0 >> 8) & kLow, (w1 >> 8) & kLow};
+      const uint4v o = {w0 & kHigh, w1 & kHigh, (w0 >> 8) & kHigh, (w1 >> 8) & kHigh};
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        even[nb][u] = mfma(e, q.even[nb][p], even[nb][u]);
+        odd[nb][u] = mfma(o, q.odd[nb][p], odd[nb][u]);
+      }
+    }
+  }
+
+  // FP16: the remainders of the weights' rounding as a second operand
+  constexpr int kParts = BF16 ? 1 : 2;
+  uint4v weights[NB][kParts];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    float x[8];
+    uint32_t vp[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int u = i >> 2;
+      const uint32_t kp = d.kp[u][i & 3];
+      vp[i] = d.vp[u][i & 3];
+      const float raw = (even[nb][u][i & 3] + 0.0625f * odd[nb][u][i & 3]) * q.unit[nb];
+      x[i] = low_half(kp) * raw + high_half(kp) * q.sum[nb];
+      if (edge) {
+        const int j = t + kKvUnit * u + 4 * g + (i & 3);
+        if (!(d.valid[u] && j >= q.lo[nb] && j <= q.hi[nb])) {
+          x[i] = -__builtin_inff();
+          vp[i] = 0;
+        }
+      }
+    }
+    float p[8], w[8], sum, most;
+    auto weigh = [&](float m) {
+      sum = 0.f;
+      most = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = exp2_hw(x[i] - m);
+        w[i] = p[i] * low_half(vp[i]);
+        sum += p[i];
+        most = fmaxf(most, w[i]);
+      }
+    };
+    weigh(s.m[nb]);
+    if (__any(most > kMostWeight || sum > kMostSum)) {
+      // Move the reference: the largest weight becomes 2^8, unless that lets
+      // a probability exceed 2^40 (values of scale 0).
+      float top = kNone;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        top = fmaxf(top, x[i] + __builtin_amdgcn_logf(low_half(vp[i])) - kTopWeight);
+        top = fmaxf(top, x[i] - kSumHeadroom);
+      }
+      const float m = fmaxf(s.m[nb], groups_max(top));
+      const float f = exp2_hw(s.m[nb] - m);
+      s.m[nb] = m;
+      s.l[nb] *= f;
+      s.z[nb] *= f;
+      s.w[nb] *= f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) s.acc[nb][c] *= f;
+      weigh(m);
+    }
+    s.l[nb] += sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s.z[nb] += p[i] * high_half(vp[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = pack_halves(w[2 * i], w[2 * i + 1]);
+      weights[nb][0][i] = h;
+      if constexpr (!BF16)
+        weights[nb][1][i] = pack_halves(w[2 * i] - low_half(h), w[2 * i + 1] - high_half(h));
+    }
+  }
+
+  const uint4v ones = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) s.w[nb] = mfma(ones, weights[nb][k], s.w[nb]);
+
+  // byte b of two tokens' words into the two halves of a register
+  const uint32_t half = D == 64 ? (lane & 1) * 0x00020002u : 0u;
+  constexpr int kBytes = D == 64 ? 2 : 4;
+#pragma unroll
+  for (int i = 0; i < TileData<D>::VV; ++i) {
+#pragma unroll
+    for (int b = 0; b < kBytes; ++b) {
+      const uint32_t sel = (0x0c040c00u + 0x00010001u * b) + half;
+      uint4v both, e, o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4v& v = d.v[k >> 1][i];
+        both[k] = __builtin_amdgcn_perm(v[2 * (k & 1) + 1], v[2 * (k & 1)], sel);
+        e[k] = both[k] & kLow;
+        o[k] = both[k] & kHigh;
+      }
+      const int c = 2 * (kBytes * i + b);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          s.acc[nb][c] = mfma(e, weights[nb][k], s.acc[nb][c]);
+          s.acc[nb][c + 1] = mfma(o, weights[nb][k], s.acc[nb][c + 1]);
+        }
+    }
+  }
+}
+
+// Query rows of a workgroup and the tokens they see.
+struct Span {
+  int len, nq, tok0;    // tokens held, queries, first query row of the request
+  int rows;             // query rows (query, head of the group) of the request
+  int begin, end;       // tokens any row of the tile sees: begin (multiple of
+                        // kTile) <= j < end
+};
+
+template <int D, int NB, bool BF16>
+__device__ __forceinline__ void load_queries(Queries<D, NB>& q, const KvAttentionArgs& a,
+                                             const Span& sp, int head, int group, int row0) {
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    // rows past the last repeat it; they are not stored
+    const int want = row0 + 16 * nb + (lane & 15);
+    const int row = want < sp.rows ? want : sp.rows - 1;
+    const int i = row / group;
+    const uint16_t* src = a.q.p + (int64_t)(sp.tok0 + i) * a.q.token +
+                          (int64_t)(head * group + row - i * group) * a.q.head;
+    uint4v raw[D / 64][2];
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p) {
+      const uint4v* w = reinterpret_cast<const uint4v*>(src + 8 * (g * (D / 32) + 2 * p));
+      raw[p][0] = w[0];
+      raw[p][1] = w[1];
+    }
+    // BF16 rows are brought near FP16's upper end by a power of two, which
+    // loses nothing down to 2^-38 of the largest element.
+    float up = 1.f, back = 1.f;
+    if constexpr (BF16) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int p = 0; p < D / 64; ++p)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x = raw[p][k][e] & 0x7fff7fffu;
+            top = max(top, max(x & 0xffffu, x >> 16));
+          }
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+      int e = (int)(top >> 7) - 127;                   // exponent of the largest
+      e = e < -100 ? -100 : e > 126 ? 126 : e;
+      up = __builtin_bit_cast(float, (uint32_t)(127 + 13 - e) << 23);
+      back = __builtin_bit_cast(float, (uint32_t)(127 - 13 + e) << 23);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p) {
+      _Float16 h[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint32_t w = raw[p][c >> 3][(c >> 1) & 3];
+        const uint32_t bits = c & 1 ? w >> 16 : w & 0xffffu;
+        if constexpr (BF16) h[c] = (_Float16)(__builtin_bit_cast(float, bits << 16) * up);
+        else h[c] = __builtin_bit_cast(_Float16, (uint16_t)bits);
+        sum += (float)h[c];
+      }
+      const half8 even = {h[0], h[4], h[8], h[12], h[2], h[6], h[10], h[14]};
+      const half8 odd = {h[1], h[5], h[9], h[13], h[3], h[7], h[11], h[15]};
+      q.even[nb][p] = __builtin_bit_cast(uint4v, even);
+      q.odd[nb][p] = __builtin_bit_cast(uint4v, odd);
+    }
+    sum = groups_sum(sum);
+    const float logits = a.scale * kLog2e * back;
+    q.sum8[nb] = sum * -0x1p-21f;
+    q.unit[nb] = logits * 0x1p24f;
+    q.sum[nb] = sum * logits;
+    const int pos = sp.len - sp.nq + i;
+    q.hi[nb] = pos;
+    q.lo[nb] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+  }
+}
+
+// The tokens of a row tile.
+__device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int group, int row0,
+                                        int row_tile) {
+  Span s;
+  const int64_t most = (int64_t)a.max_pages * a.page;
+  const int len = a.lens[b] > 0 ? a.lens[b] : 0;
+  s.len = len < most ? len : (int)most;
+  if (a.q_start) {
+    int lo = a.q_start[b], hi = a.q_start[b + 1];
+    lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+    hi = hi < lo ? lo : hi > a.T ? a.T : hi;
+    s.tok0 = lo;
+    s.nq = hi - lo;
+  } else {
+    s.tok0 = b;
+    s.nq = b < a.T;
+  }
+  // queries beyond max_q are not computed
+  const int nq = s.nq < a.max_q ? s.nq : a.max_q;
+  s.rows = nq * group;
+  const int last = row0 + row_tile < s.rows ? row0 + row_tile : s.rows;
+  const int first_pos = s.len - s.nq + row0 / group;
+  const int last_pos = s.len - s.nq + (last - 1) / group;
+  s.begin = a.window > 0 && first_pos >= a.window ? first_pos - a.window + 1 : 0;
+  s.begin &= ~(kTile - 1);
+  s.end = last_pos + 1 > s.begin ? last_pos + 1 : s.begin;
+  return s;
+}
+
+// Rows of D floats of a block in LDS, padded so that the 16 rows of a store
+// fall on different banks.
+template <int D>
+constexpr int kLdsRow = D + 4;
+
+template <int D, int NB, bool ROWS, bool BF16>
+__global__ __launch_bounds__(kThreads) void kv_attention_kernel(
+    KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
+    float* __restrict__ partials) {
+  constexpr int kRowTile = ROWS ? 16 * NB * kWaves : 16 * NB;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = a.Hq / a.H;
+  int id = blockIdx.x;
+  const int split = id % splits;
+  id /= splits;
+  const int work = id;               // (request, head, row tile)
+  const int tile = id % tiles;
+  id /= tiles;
+  const int head = id % a.H, b = id / a.H;
+  const int row0 = tile * kRowTile;
+  const Span sp = span_of(a, b, group, row0, kRowTile);
+  if (row0 >= sp.rows) return;
+
+  // This workgroup's tokens.
+  int per = chunk;
+  int parts = (sp.end - sp.begin + per - 1) / per;
+  if (parts > splits) {
+    per = ((sp.end - sp.begin + splits - 1) / splits + kTile - 1) / kTile * kTile;
+    parts = (sp.end - sp.begin + per - 1) / per;
+  }
+  if (parts < 1) parts = 1;
+  if (split >= parts) return;
+  int begin = sp.begin + split * per;
+  int end = begin + per < sp.end ? begin + per : sp.end;
+
+  int wave_row0 = row0;
+  if constexpr (ROWS) {
+    wave_row0 = row0 + 16 * NB * wave;
+  } else {
+    const int n = (end - begin + kTile - 1) / kTile;
+    const int each = (n + kWaves - 1) / kWaves;
+    begin += wave * each * kTile;
+    const int stop = begin + each * kTile;
+    end = stop < end ? stop : end;
+  }
+
+  Queries<D, NB> q;
+  load_queries<D, NB, BF16>(q, a, sp, head, group, wave_row0);
+  Sums<D, NB> s;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    s.m[nb] = kNone;
+    s.l[nb] = s.z[nb] = 0.f;
+    s.w[nb] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) s.acc[nb][c] = float4v{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // Inner tiles, which every row of the wave sees whole, need no mask.
+  int row_last = wave_row0 + 16 * NB < sp.rows ? wave_row0 + 16 * NB - 1 : sp.rows - 1;
+  const int row_first = wave_row0 < sp.rows ? wave_row0 : sp.rows - 1;
+  const int pos_first = sp.len - sp.nq + row_first / group;
+  const int pos_last = sp.len - sp.nq + row_last / group;
+  const int inner_end = pos_first + 1;  // exclusive
+  const int inner_begin = a.window > 0 && pos_last >= a.window ? pos_last - a.window + 1 : 0;
+
+  if constexpr (ROWS) {  // this wave's share of the tile's tokens; none past the last row
+    const int window_begin = a.window > 0 && pos_first >= a.window
+                                 ? (pos_first - a.window + 1) & ~(kTile - 1) : 0;
+    begin = begin > window_begin ? begin : window_begin;
+    end = wave_row0 >= sp.rows ? begin : end < pos_last + 1 ? end : pos_last + 1;
+  }
+
+  if (begin < end) {
+    const int page_shift = 31 - __builtin_clz((unsigned)a.page);
+    PageIds ids{a.table + (int64_t)b * a.max_pages, a.max_pages, 0, -1};
+    ids.load(begin >> page_shift);
+    TileData<D> cur, next;
+    load_tile<D>(cur, a, head, page_shift, ids, begin);
+    for (int t = begin; t < end; t += kTile) {
+      if (t + kTile < end) load_tile<D>(next, a, head, page_shift, ids, t + kTile);
+      const bool edge = t < inner_begin || t + kTile > inner_end || !cur.valid[0] || !cur.valid[1];
+      attend<D, NB, BF16>(cur, q, s, t, edge);
+      cur = next;
+    }
+  }
+
+  // Each lane's rows as true sums: O (unnormalised), sum p.
+  const int g = lane >> 4, n16 = lane & 15;
+  float total[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    total[nb] = groups_sum(s.l[nb]);
+    const float fixed = groups_sum(s.z[nb]) - 8.0f * s.w[nb][0];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s.acc[nb][c][i] = s.acc[nb][c][i] * (c & 1 ? 0x1p20f : 0x1p24f) + fixed;
+  }
+
+  constexpr int kCols = D == 64 ? 4 : 8;  // neighbouring channels of a lane
+  auto write_out = [&](int row, int ch, const float* x, float inv) {
+    const int i = row / group;
+    uint16_t* dst = a.o + (int64_t)(sp.tok0 + i) * a.o_token +
+                    (int64_t)(head * group + row - i * group) * a.o_head + ch;
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (BF16) {
+        const __bf16 lo = (__bf16)(x[2 * k] * inv), hi = (__bf16)(x[2 * k + 1] * inv);
+        w[k] = (uint32_t)__builtin_bit_cast(uint16_t, lo) |
+               (uint32_t)__builtin_bit_cast(uint16_t, hi) << 16;
+      } else {
+        w[k] = pack_halves(x[2 * k] * inv, x[2 * k + 1] * inv);
+      }
+    }
+    *reinterpret_cast<uint2v*>(dst) = uint2v{w[0], w[1]};
+  };
+  auto write_lse = [&](int row, float m, float l) {
+    if (!a.lse) return;
+    const int i = row / group;
+    a.lse[(int64_t)(sp.tok0 + i) * a.Hq + head * group + row - i * group] =
+        l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  };
+
+  if constexpr (ROWS) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = wave_row0 + 16 * nb + n16;
+      if (row >= sp.rows) continue;
+      const float inv = total[nb] == 0.f ? 0.f : 1.0f / total[nb];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 16; c += 4) {
+          const int ch = kCols * (4 * g + i) + c % kCols + c / kCols * 128;
+          const float x[4] = {s.acc[nb][c][i], s.acc[nb][c + 1][i], s.acc[nb][c + 2][i],
+                              s.acc[nb][c + 3][i]};
+          write_out(row, ch, x, inv);
+        }
+      if (g == 0) write_lse(row, s.m[nb], total[nb]);
+    }
+  } else {
+    // Join the waves, in wave order, through LDS.
+    __shared__ float red[16 * NB * kLdsRow<D>];
+    __shared__ float s_m[kWaves][16 * NB], s_l[kWaves][16 * NB];
+    __shared__ bool s_last;
+    if (g == 0) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        s_m[wave][16 * nb + n16] = s.m[nb];
+        s_l[wave][16 * nb + n16] = total[nb];
+      }
+    }
+    __syncthreads();
+    for (int w = 0; w < kWaves; ++w) {
+      if (wave == w) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int row = 16 * nb + n16;
+          float m = s_m[0][row];
+          for (int o = 1; o < kWaves; ++o) m = fmaxf(m, s_m[o][row]);
+          const float f = exp2_hw(s.m[nb] - m);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float* at = red + row * kLdsRow<D> + kCols * (4 * g + i) + c % kCols +
+                          c / kCols * 128;
+              const float x = s.acc[nb][c][i] * f;
+              *at = w == 0 ? x : *at + x;
+            }
+        }
+      }
+      __syncthreads();
+    }
+    const int rows = sp.rows - row0 < 16 * NB ? sp.rows - row0 : 16 * NB;
+    auto joined = [&](int row, float* m_out) {
+      float m = s_m[0][row], l = 0.f;
+      for (int o = 1; o < kWaves; ++o) m = fmaxf(m, s_m[o][row]);
+      for (int o = 0; o < kWaves; ++o) l += s_l[o][row] * exp2_hw(s_m[o][row] - m);
+      *m_out = m;
+      return l;
+    };
+    constexpr int kVecs = D / 4;
+    if (parts == 1) {
+      for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
+        const int row = v / kVecs, ch = v % kVecs * 4;
+        float m;
+        const float l = joined(row, &m);
+        write_out(row0 + row, ch, red + row * kLdsRow<D> + ch, l == 0.f ? 0.f : 1.0f / l);
+        if (ch == 0) write_lse(row0 + row, m, l);
+      }
+      return;
+    }
+    // Publish this workgroup's rows and (m, l), then count the arrival; the
+    // last workgroup of the row tile joins them in split order.
+    constexpr int kRowFloats = D + 4;
+    const int64_t part_floats = (int64_t)16 * NB * kRowFloats;
+    const float* tile_base = partials + (int64_t)work * splits * part_floats;
+    {
+      const __amdgpu_buffer_rsrc_t mine = coherent_rsrc(tile_base + split * part_floats);
+      for (int v = threadIdx.x; v < rows * (kVecs + 1); v += kThreads) {
+        const int row = v / (kVecs + 1), c = v % (kVecs + 1);
+        float4_t x;
+        if (c < kVecs) {
+          x = *reinterpret_cast<const float4_t*>(red + row * kLdsRow<D> + 4 * c);
+        } else {
+          float m;
+          const float l = joined(row, &m);
+          x = float4_t{m, l, 0.f, 0.f};
+        }
+        store_coherent(mine, v, x);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const unsigned prev = __hip_atomic_fetch_add(counters + work, 1u, __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_AGENT);
+      s_last = prev == (unsigned)(parts - 1);
+    }
+    __syncthreads();
+    if (!s_last) return;
+    for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
+      const int row = v / kVecs, c = v % kVecs;
+      float m = kNone, l = 0.f;
+      float4_t x = {0.f, 0.f, 0.f, 0.f};
+      for (int o = 0; o < parts; ++o) {
+        const __amdgpu_buffer_rsrc_t part = coherent_rsrc(tile_base + o * part_floats);
+        const float4_t ml = load_coherent(part, row * (kVecs + 1) + kVecs);
+        const float4_t y = load_coherent(part, row * (kVecs + 1) + c);
+        const float to = fmaxf(m, ml[0]);
+        const float f0 = exp2_hw(m - to), f1 = exp2_hw(ml[0] - to);
+        x = x * f0 + y * f1;
+        l = l * f0 + ml[1] * f1;
+        m = to;
+      }
+      const float out[4] = {x[0], x[1], x[2], x[3]};
+      write_out(row0 + row, 4 * c, out, l == 0.f ? 0.f : 1.0f / l);
+      if (c == 0) write_lse(row0 + row, m, l);
+    }
+    if (threadIdx.x == 0)  // ready for the next call
+      __hip_atomic_store(counters + work, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+
+template <int D, int NB, bool ROWS>
+hipError_t launch(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
+                  unsigned* counters, float* partials, hipStream_t stream) {
+  const dim3 grid((unsigned)((int64_t)a.B * a.H * p.tiles * p.splits));
+  if (dtype == W4A16_DTYPE_BF16)
+    hipLaunchKernelGGL((kv_attention_kernel<D, NB, ROWS, true>), grid, dim3(kThreads), 0, stream,
+                       a, p.tiles, p.splits, p.chunk, counters, partials);
+  else
+    hipLaunchKernelGGL((kv_attention_kernel<D, NB, ROWS, false>), grid, dim3(kThreads), 0, stream,
+                       a, p.tiles, p.splits, p.chunk, counters, partials);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_d(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
+                    unsigned* counters, float* partials, hipStream_t stream) {
+  constexpr int kWide = D == 256 ? 1 : 2;  // a second block of rows does not fit the registers
+  if (p.rows) return launch<D, kWide, true>(p, a, dtype, counters, partials, stream);
+  if (p.nb == 1) return launch<D, 1, false>(p, a, dtype, counters, partials, stream);
+  return launch<D, kWide, false>(p, a, dtype, counters, partials, stream);
+}
+
+}  // namespace
+
+KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, int max_len,
+                                       int window, int cus) {
+  KvAttentionPlan p{};
+  const int64_t rows = (int64_t)(Hq / H) * max_q;
+  p.waves = kWaves;
+  p.rows = rows > 64;
+  p.nb = D < 256 && rows > 16 ? 2 : 1;
+  const int tile_rows = 16 * p.nb * (p.rows ? kWaves : 1);
+  p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
+  p.splits = 1;
+  int64_t keys = max_len;
+  if (window > 0 && keys > (int64_t)window + max_q) keys = (int64_t)window + max_q;
+  keys = (keys + kTile - 1) / kTile * kTile + kTile;
+  p.chunk = (int)(keys < (1 << 30) ? keys : (1 << 30));
+  const int64_t work = (int64_t)B * H * p.tiles;
+  if (!p.rows && work <= kMaxSplitTiles) {
+    // two workgroups per compute unit; a wave has at least two tiles
+    const int64_t want = (2 * (int64_t)cus + work - 1) / work;
+    const int64_t most = keys / (2 * kWaves * kTile);
+    int64_t n = want < most ? want : most;
+    if (n > 1) {
+      p.chunk = (int)((keys + n - 1) / n + kTile - 1) / kTile * kTile;
+      p.splits = (int)((keys + p.chunk - 1) / p.chunk);
+    }
+  }
+  if (p.splits > 1)
+    p.workspace_bytes = kCounterHeaderBytes + (size_t)work * p.splits * 16 * p.nb *
+                                                  (D + 4) * sizeof(float);
+  return p;
+}
+
+hipError_t launch_kv_attention(const KvAttentionPlan& p, const KvAttentionArgs& a, int D,
+                               int dtype, void* workspace, hipStream_t stream) {
+  unsigned* counters = static_cast<unsigned*>(workspace);
+  float* partials =
+      reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterHeaderBytes);
+  switch (D) {
+    case 64: return launch_d<64>(p, a, dtype, counters, partials, stream);
+    case 128: return launch_d<128>(p, a, dtype, counters, partials, stream);
+    default: return launch_d<256>(p, a, dtype, counters, partials, stream);
+  }
+}
+
+}  // namespace w4a16

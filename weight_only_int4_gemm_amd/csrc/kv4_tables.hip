@@ -1,0 +1,211 @@
+// Page tables, slots and positions from request lengths (kv4_tables).
+//
+// Three exclusive prefix sums over the requests (new tokens, pages taken,
+// pages given back) place everything; the rest is independent per token and
+// per page.  Free pages wait in a ring, taken at its head and given back at
+// its tail, so what a call reads of it (head .. head + count) and what it
+// writes (from head + count on) never meet, and workgroups need not wait for
+// each other.  Every workgroup therefore makes the (small) prefix sums for
+// itself in LDS and then takes its share of the tokens and pages.  lens_out
+// and state_out may be lens and state: the last workgroup to finish, counted
+// in state_out[3], writes them.
+//
+// What bounds it: the launch and three dependent trips to memory.
+#include "../../include/w4a16_kv4.h"
+#include "kv4.hpp"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kItemsPerGroup = 1024;  // tokens and pages of one workgroup
+constexpr int kMaxGroups = 256;
+
+// Addition of non-negative numbers that stops at `most`: associative, so a
+// scan of it does not depend on its shape, and no length overflows it.
+__device__ __forceinline__ int add_up_to(int a, int b, int most) {
+  const unsigned s = (unsigned)a + (unsigned)b;
+  return s < (unsigned)most ? (int)s : most;
+}
+
+struct Request {
+  int len, want, old_pages, new_pages;
+  bool over;
+};
+
+__device__ __forceinline__ Request request(const KvTablesArgs& a, int b) {
+  Request r;
+  const int64_t most = (int64_t)a.max_pages * a.page;
+  const int len = a.lens[b] > 0 ? a.lens[b] : 0;
+  r.len = len < most ? len : (int)most;
+  r.want = a.want[b] > 0 ? a.want[b] : 0;
+  r.old_pages = (int)(((int64_t)r.len + a.page - 1) / a.page);
+  r.new_pages = (int)(((int64_t)r.want + a.page - 1) / a.page);
+  r.over = r.new_pages > a.max_pages;
+  return r;
+}
+
+// The last index b with sums[b] <= x, for x < sums[n].
+__device__ __forceinline__ int owner(const int* sums, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Served requests are those whose pages are there: cumulative need within
+// the free pages (requests that take none are always served).
+__device__ __forceinline__ bool served(const Request& r, int taken_before, int taken_upto,
+                                       int count) {
+  return !r.over && (taken_upto == taken_before || taken_upto <= count);
+}
+
+__global__ __launch_bounds__(kThreads) void kv_tables_kernel(KvTablesArgs a) {
+  // exclusive sums, [B + 1] each: new tokens, pages wanted, pages returned
+  extern __shared__ int lds[];
+  int* const tok = lds;
+  int* const need = tok + a.B + 1;
+  int* const back = need + a.B + 1;
+  __shared__ int wave_sum[3][kThreads / 64];
+  __shared__ int s_refused, s_taken, s_last;
+  constexpr int kMost = 0x7fffffff;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int b0 = tid * per < a.B ? tid * per : a.B;
+  const int b1 = b0 + per < a.B ? b0 + per : a.B;
+  if (tid == 0) s_refused = s_taken = 0;
+
+  const unsigned P = a.pages;
+  const unsigned head = (unsigned)a.state[0] % P;
+  int count = a.state[1];
+  count = count < 0 ? 0 : count > a.pages ? a.pages : count;
+
+  int sum[3] = {0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    const Request r = request(a, b);
+    const int grown = r.want > r.len ? r.want - r.len : 0;
+    const int diff = r.over ? 0 : r.new_pages - r.old_pages;
+    // kept per request; made exclusive below
+    tok[b + 1] = grown;
+    need[b + 1] = diff > 0 ? diff : 0;
+    back[b + 1] = diff < 0 ? -diff : 0;
+    sum[0] = add_up_to(sum[0], grown, a.capacity);
+    sum[1] = add_up_to(sum[1], need[b + 1], kMost);
+    sum[2] = add_up_to(sum[2], back[b + 1], kMost);
+  }
+  const int most[3] = {a.capacity, kMost, kMost};
+  int before[3];
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    int x = sum[s];
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int y = __shfl_up(x, d);
+      if (lane >= d) x = add_up_to(x, y, most[s]);
+    }
+    before[s] = __shfl_up(x, 1);
+    if (lane == 0) before[s] = 0;
+    if (lane == 63) wave_sum[s][wave] = x;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    int base = 0;
+    for (int w = 0; w < wave; ++w) base = add_up_to(base, wave_sum[s][w], most[s]);
+    int x = add_up_to(base, before[s], most[s]);
+    int* const sums = s == 0 ? tok : s == 1 ? need : back;
+    for (int b = b0; b < b1; ++b) {
+      x = add_up_to(x, sums[b + 1], most[s]);
+      sums[b + 1] = x;
+    }
+    if (tid == 0) sums[0] = 0;
+  }
+  __syncthreads();
+
+  const int tokens = tok[a.B], wanted = need[a.B], returned = back[a.B];
+  const int stride = gridDim.x * kThreads;
+  const int first = blockIdx.x * kThreads + tid;
+
+  // pages taken: request b's j-th new page is the ring's (need[b] + j)-th
+  const int take = wanted < count ? wanted : count;
+  for (int i = first; i < take; i += stride) {
+    const int b = owner(need, a.B, i);
+    const Request r = request(a, b);
+    if (!served(r, need[b], need[b + 1], count)) continue;
+    const int col = r.old_pages + i - need[b];
+    a.table[(int64_t)b * a.max_pages + col] = a.ring[(head + (unsigned)i) % P];
+  }
+  // pages given back, to the tail
+  for (int i = first; i < returned; i += stride) {
+    const int b = owner(back, a.B, i);
+    const Request r = request(a, b);
+    const int col = r.new_pages + i - back[b];
+    a.ring[(head + (unsigned)count + (unsigned)i) % P] =
+        a.table[(int64_t)b * a.max_pages + col];
+  }
+  for (int t = first; t < a.capacity; t += stride) {
+    int slot = -1, pos = 0;
+    if (t < tokens) {
+      const int b = owner(tok, a.B, t);
+      const Request r = request(a, b);
+      pos = r.len + t - tok[b];
+      if (served(r, need[b], need[b + 1], count)) {
+        const int col = pos / a.page;
+        // a page of this call comes from the ring: the table's entry may
+        // not be written yet
+        const unsigned id = col >= r.old_pages
+                                ? a.ring[(head + (unsigned)(need[b] + col - r.old_pages)) % P]
+                                : a.table[(int64_t)b * a.max_pages + col];
+        if (id < P) slot = (int)id * a.page + pos % a.page;
+      }
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+  }
+  for (int b = first; b <= a.B; b += stride) a.q_start[b] = tok[b];
+
+  // The last workgroup writes what others may still have been reading.
+  if (gridDim.x > 1) {
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (tid == 0)
+      s_last = __hip_atomic_fetch_add(reinterpret_cast<unsigned*>(a.state_out) + 3, 1u,
+                                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+  }
+  for (int b = tid; b < a.B; b += kThreads) {
+    const Request r = request(a, b);
+    const bool ok = served(r, need[b], need[b + 1], count);
+    a.lens_out[b] = ok ? r.want : r.len;
+    if (!ok) atomicAdd(&s_refused, 1);
+    else if (need[b + 1] > need[b]) atomicMax(&s_taken, need[b + 1]);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    const int64_t left = (int64_t)count - s_taken + returned;
+    a.state_out[0] = (int)((head + (unsigned)s_taken) % P);
+    a.state_out[1] = left < a.pages ? (int)left : a.pages;
+    a.state_out[2] = s_refused;
+    a.state_out[3] = 0;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_tables(const KvTablesArgs& a, hipStream_t stream) {
+  // One workgroup covers the requests' own work; tokens beyond that are
+  // shared out.  Pages are at most as many as tokens, or released ones,
+  // which are few.
+  int64_t groups = ((int64_t)a.capacity + kItemsPerGroup - 1) / kItemsPerGroup;
+  if (groups < 1) groups = 1;
+  if (groups > kMaxGroups) groups = kMaxGroups;
+  const size_t lds = 3 * (size_t)(a.B + 1) * sizeof(int);
+  hipLaunchKernelGGL(kv_tables_kernel, dim3((unsigned)groups), dim3(kThreads), lds, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace w4a16
