@@ -484,6 +484,31 @@ def test_attention_never_sees_masked_places():
             assert torch.equal(O, O2) and torch.equal(L, L2), hex(fill)
 
 
+def test_a_stored_nan_reaches_the_queries_that_see_it_only():
+    """A token stored with an infinite key or a NaN value: queries before it,
+    and those whose window has passed it, are as without it."""
+    torch = _torch()
+    rng = np.random.default_rng(29)
+    for D, n, window, bad_key in ((128, 150, 0, False), (64, 150, 40, True), (128, 90, 20, False)):
+        H, Hq, page, pages = 1, 4, 16, 12
+        C = _filled(rng, pages, H, page, D)
+        table = _requests(rng, [n], pages, page)
+        Q, q = to16(rng.standard_normal((n, Hq, D)), "float16")
+        O, L = _attend(Q, C, table, [n], [0, n], Hq, 0.1, window, n, n)
+        at = 45
+        slot = int(table[0, at // page]) * page + at % page
+        kv = torch.randn((2, 1, H, D), device="cuda").half()
+        kv[0 if bad_key else 1, 0, 0, 5] = float("inf" if bad_key else "nan")
+        w4.kv4_append(kv[0], kv[1], cuda(np.array([slot], np.int32)), C)
+        O2, L2 = _attend(Q, C, table, [n], [0, n], Hq, 0.1, window, n, n)
+        sees = np.arange(n) >= at
+        if window:
+            sees &= np.arange(n) < at + window
+        sees = torch.from_numpy(sees)
+        assert torch.equal(O[~sees], O2[~sees]) and torch.equal(L[~sees], L2[~sees])
+        assert bool(O2[sees].isnan().all())
+
+
 def test_attention_treats_bad_pages_as_not_there():
     rng = np.random.default_rng(22)
     page, H, Hq, D, pages = 16, 1, 4, 128, 14

@@ -42,6 +42,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
+constexpr int kWaitLoads = 0x0f70;          // s_waitcnt: all vector loads, nothing else
 constexpr int kTile = 32;                   // tokens of one step: two units
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -75,6 +76,34 @@ __device__ __forceinline__ uint32_t pack_halves(float a, float b) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
+// x times or less a half of w, in one instruction (written out, the compiler
+// converts first and multiplies or subtracts then).
+__device__ __forceinline__ float times_low_half(float x, uint32_t w) {
+  float y;
+  asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel_hi:[0,1,0]" : "=v"(y) : "v"(x), "v"(w));
+  return y;
+}
+__device__ __forceinline__ float less_low_half(float x, uint32_t w) {
+  float y;
+  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(y) : "v"(w), "v"(x));
+  return y;
+}
+__device__ __forceinline__ float less_high_half(float x, uint32_t w) {
+  float y;
+  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
+      : "=v"(y) : "v"(w), "v"(x));
+  return y;
+}
+
+// Keeps the compiler from doing a rare branch's work always, with selects,
+// and from sharing its conversions with the usual path, where they cost
+// nothing as operands of a mixed-precision instruction.
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+__device__ __forceinline__ uint32_t apart(uint32_t w) {
+  asm volatile("" : "+v"(w));
+  return w;
+}
+
 // Sum and maximum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_sum(float x) {
   x += __shfl_xor(x, 16);
@@ -104,6 +133,9 @@ struct PageIds {
     first = page;
     const int p = page + (int)(threadIdx.x & 63);
     mine = p < max_pages ? row[p] : -1;
+    // Wait here, where it is rare: left to the first use, the wait would
+    // stand after the branch and hold up the tiles in flight every time.
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
   }
   // `page` is the same in all lanes
   __device__ __forceinline__ int at(int page) {
@@ -112,37 +144,58 @@ struct PageIds {
   }
 };
 
+// Where a head's units lie: page id `p` of it starts at
+// cache + head offset + p * page stride.
+struct Pages {
+  const uint8_t* head;
+  uint64_t stride;  // bytes of a page over all heads
+  int shift, count; // log2 of a page's tokens, pages of the cache
+};
+
 template <int D>
-__device__ __forceinline__ void load_tile(TileData<D>& d, const KvAttentionArgs& a, int head,
-                                          int page_shift, PageIds& ids, int t) {
+__device__ __forceinline__ void load_tile(TileData<D>& d, const Pages& pages, PageIds& ids,
+                                          int t) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const uint8_t* base = nullptr;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int tu = t + kKvUnit * u;
-    const int id = ids.at(tu >> page_shift);
-    d.valid[u] = (unsigned)id < (unsigned)a.pages;
-    const uint8_t* unit = a.cache + kv_unit_offset<D>(d.valid[u] ? id : 0, a.H, head, a.page,
-                                                      tu & (a.page - 1));
-    const uint8_t* kp = unit + r * (D / 2) + g * (D / 8);
+    if (u == 0 || pages.shift == 4) {
+      const int tu = t + kKvUnit * u;
+      const int id = ids.at(tu >> pages.shift);
+      d.valid[u] = (unsigned)id < (unsigned)pages.count;
+      base = pages.head + (uint64_t)(uint32_t)(d.valid[u] ? id : 0) * pages.stride +
+             (uint32_t)((tu & ((1 << pages.shift) - 1)) / kKvUnit * KvUnit<D>::bytes);
+    } else {  // a larger page holds both units side by side
+      d.valid[u] = d.valid[0];
+      base += KvUnit<D>::bytes;
+    }
+    // one address for the wave, 32-bit offsets for the lanes
+    const __amdgpu_buffer_rsrc_t unit = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(base), (short)0, KvUnit<D>::bytes, 0x00020000);
+    auto load16 = [&](int at, int plus) {
+      return __builtin_bit_cast(uint4v,
+                                __builtin_amdgcn_raw_buffer_load_b128(unit, at + plus, 0, 0));
+    };
+    const int key = r * (D / 2) + g * (D / 8);
     if constexpr (D == 64) {
-      const uint2v w = *reinterpret_cast<const uint2v*>(kp);
+      const uint2v w =
+          __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(unit, key, 0, 0));
       d.k[u][0] = w[0];
       d.k[u][1] = w[1];
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
-        const uint4v w = reinterpret_cast<const uint4v*>(kp)[i];
+        const uint4v w = load16(key, 16 * i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) d.k[u][4 * i + j] = w[j];
       }
     }
-    const uint8_t* vp = unit + KvUnit<D>::values + g * (2 * D);
-    const int word = D == 64 ? r >> 1 : r;
+    const int value = g * (2 * D) + 16 * (D == 64 ? r >> 1 : r);
 #pragma unroll
     for (int i = 0; i < TileData<D>::VV; ++i)
-      d.v[u][i] = reinterpret_cast<const uint4v*>(vp)[word + 16 * i];
-    d.kp[u] = reinterpret_cast<const uint4v*>(unit + KvUnit<D>::key_params)[g];
-    d.vp[u] = reinterpret_cast<const uint4v*>(unit + KvUnit<D>::value_params)[g];
+      d.v[u][i] = load16(value, KvUnit<D>::values + 256 * i);
+    d.kp[u] = load16(16 * g, KvUnit<D>::key_params);
+    d.vp[u] = load16(16 * g, KvUnit<D>::value_params);
   }
 }
 
@@ -159,27 +212,30 @@ struct Sums {
 // A wave's query rows as operands, and what its columns need.
 template <int D, int NB>
 struct Queries {
-  uint4v even[NB][D / 64], odd[NB][D / 64];  // channels by parity of the nibble
+  // channels by parity of the nibble; the odd ones, which meet codes of 16
+  // times the size, are divided by 16
+  uint4v even[NB][D / 64], odd[NB][D / 64];
   float sum8[NB];    // -8 sum q, in the products' units
-  float unit[NB];    // product units to base-2 logits
+  float unit;        // product units to base-2 logits
   float sum[NB];     // sum q in base-2 logits
   int lo[NB], hi[NB];  // keys seen: lo <= j <= hi
 };
 
+// One tile.  `edge`: some of its tokens are not seen by some row.  What the
+// cache holds for those may be anything (NaN included), so they are taken out
+// of the probabilities and the weights, never multiplied by zero.
 template <int D, int NB, bool BF16>
 __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB>& q,
                                        Sums<D, NB>& s, int t, bool edge) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
-  float4v even[NB][2], odd[NB][2];
+  float4v raw[NB][2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      even[nb][u] = float4v{q.sum8[nb], q.sum8[nb], q.sum8[nb], q.sum8[nb]};
-      odd[nb][u] = float4v{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int nb = 0; nb < NB; ++nb)
+      raw[nb][u] = float4v{q.sum8[nb], q.sum8[nb], q.sum8[nb], q.sum8[nb]};
 #pragma unroll
     for (int p = 0; p < D / 64; ++p) {
       const uint32_t w0 = d.k[u][2 * p], w1 = d.k[u][2 * p + 1];
@@ -187,45 +243,53 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
       const uint4v o = {w0 & kHigh, w1 & kHigh, (w0 >> 8) & kHigh, (w1 >> 8) & kHigh};
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        even[nb][u] = mfma(e, q.even[nb][p], even[nb][u]);
-        odd[nb][u] = mfma(o, q.odd[nb][p], odd[nb][u]);
+        raw[nb][u] = mfma(e, q.even[nb][p], raw[nb][u]);
+        raw[nb][u] = mfma(o, q.odd[nb][p], raw[nb][u]);
       }
     }
   }
+
+  auto key_params = [&](int i) { return d.kp[i >> 2][i & 3]; };
+  auto value_params = [&](int i) { return d.vp[i >> 2][i & 3]; };
+  float scale[8];  // of the keys, times the logits' unit
+#pragma unroll
+  for (int i = 0; i < 8; ++i) scale[i] = times_low_half(q.unit, key_params(i));
 
   // FP16: the remainders of the weights' rounding as a second operand
   constexpr int kParts = BF16 ? 1 : 2;
   uint4v weights[NB][kParts];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    float x[8];
-    uint32_t vp[8];
+    float p[8], w[8], sum, most;
+    auto seen = [&](int i) {
+      const int j = (int)apart(t + 4 * g) + kKvUnit * (i >> 2) + (i & 3);
+      return d.valid[i >> 2] && j >= q.lo[nb] && j <= q.hi[nb];
+    };
+    // the logit less m: scale (q . c) + (offset sum q - m)
+    auto logit = [&](int i, float m) {
+      return __builtin_fmaf(scale[i], raw[nb][i >> 2][i & 3],
+                            __builtin_fmaf(high_half(key_params(i)), q.sum[nb], -m));
+    };
+    auto weigh = [&](float m) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int u = i >> 2;
-      const uint32_t kp = d.kp[u][i & 3];
-      vp[i] = d.vp[u][i & 3];
-      const float raw = (even[nb][u][i & 3] + 0.0625f * odd[nb][u][i & 3]) * q.unit[nb];
-      x[i] = low_half(kp) * raw + high_half(kp) * q.sum[nb];
+      for (int i = 0; i < 8; ++i) {
+        p[i] = exp2_hw(logit(i, m));
+        w[i] = times_low_half(p[i], value_params(i));
+      }
       if (edge) {
-        const int j = t + kKvUnit * u + 4 * g + (i & 3);
-        if (!(d.valid[u] && j >= q.lo[nb] && j <= q.hi[nb])) {
-          x[i] = -__builtin_inff();
-          vp[i] = 0;
+        keep_branch();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[i] = seen(i) ? p[i] : 0.f;
+          w[i] = seen(i) ? w[i] : 0.f;
         }
       }
-    }
-    float p[8], w[8], sum, most;
-    auto weigh = [&](float m) {
       sum = 0.f;
       most = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = exp2_hw(x[i] - m);
-        w[i] = p[i] * low_half(vp[i]);
-        sum += p[i];
-        most = fmaxf(most, w[i]);
-      }
+      for (int i = 0; i < 8; ++i) sum += p[i];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) most = fmaxf(fmaxf(most, w[i]), w[i + 1]);
     };
     weigh(s.m[nb]);
     if (__any(most > kMostWeight || sum > kMostSum)) {
@@ -234,8 +298,11 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
       float top = kNone;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        top = fmaxf(top, x[i] + __builtin_amdgcn_logf(low_half(vp[i])) - kTopWeight);
-        top = fmaxf(top, x[i] - kSumHeadroom);
+        const float offset = high_half(apart(key_params(i)));
+        float x = scale[i] * raw[nb][i >> 2][i & 3] + offset * q.sum[nb];
+        if (edge) x = seen(i) ? x : -__builtin_inff();
+        top = fmaxf(top, x + __builtin_amdgcn_logf(low_half(apart(value_params(i)))) - kTopWeight);
+        top = fmaxf(top, x - kSumHeadroom);
       }
       const float m = fmaxf(s.m[nb], groups_max(top));
       const float f = exp2_hw(s.m[nb] - m);
@@ -248,14 +315,21 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
       weigh(m);
     }
     s.l[nb] += sum;
+    if (edge) {
+      keep_branch();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s.z[nb] += p[i] * high_half(vp[i]);
+      for (int i = 0; i < 8; ++i) s.z[nb] += seen(i) ? p[i] * high_half(apart(value_params(i))) : 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s.z[nb] += p[i] * high_half(value_params(i));
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t h = pack_halves(w[2 * i], w[2 * i + 1]);
+      if constexpr (!BF16) {
+        weights[nb][1][i] = pack_halves(less_low_half(w[2 * i], h), less_high_half(w[2 * i + 1], h));
+      }
       weights[nb][0][i] = h;
-      if constexpr (!BF16)
-        weights[nb][1][i] = pack_halves(w[2 * i] - low_half(h), w[2 * i + 1] - high_half(h));
     }
   }
 
@@ -305,6 +379,14 @@ template <int D, int NB, bool BF16>
 __device__ __forceinline__ void load_queries(Queries<D, NB>& q, const KvAttentionArgs& a,
                                              const Span& sp, int head, int group, int row0) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
+  uint4v raw[NB][D / 64][2];
+  auto element = [&](int nb, int p, int c) {
+    const uint32_t w = raw[nb][p][c >> 3][(c >> 1) & 3];
+    const uint32_t bits = c & 1 ? w >> 16 : w & 0xffffu;
+    if constexpr (BF16) return __builtin_bit_cast(float, bits << 16);
+    else return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  };
+  float top = 0.f;  // the largest magnitude of the rows that are finite
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     // rows past the last repeat it; they are not stored
@@ -313,45 +395,45 @@ __device__ __forceinline__ void load_queries(Queries<D, NB>& q, const KvAttentio
     const int i = row / group;
     const uint16_t* src = a.q.p + (int64_t)(sp.tok0 + i) * a.q.token +
                           (int64_t)(head * group + row - i * group) * a.q.head;
-    uint4v raw[D / 64][2];
+    uint32_t most = 0;
 #pragma unroll
     for (int p = 0; p < D / 64; ++p) {
       const uint4v* w = reinterpret_cast<const uint4v*>(src + 8 * (g * (D / 32) + 2 * p));
-      raw[p][0] = w[0];
-      raw[p][1] = w[1];
+      raw[nb][p][0] = w[0];
+      raw[nb][p][1] = w[1];
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        most = max(most, __builtin_bit_cast(uint32_t, element(nb, p, c)) & 0x7fffffffu);
     }
-    // BF16 rows are brought near FP16's upper end by a power of two, which
-    // loses nothing down to 2^-38 of the largest element.
-    float up = 1.f, back = 1.f;
-    if constexpr (BF16) {
-      uint32_t top = 0;
+    most = max(most, (uint32_t)__shfl_xor((int)most, 16));
+    most = max(most, (uint32_t)__shfl_xor((int)most, 32));
+    if (most < 0x7f800000u) top = fmaxf(top, __builtin_bit_cast(float, most));
+    const int pos = sp.len - sp.nq + i;
+    q.hi[nb] = pos;
+    q.lo[nb] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+  }
 #pragma unroll
-      for (int p = 0; p < D / 64; ++p)
+  for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+  // The wave's rows are brought near FP16's upper end by one power of two:
+  // every score keeps 2^-30 of the largest one among them, however small the
+  // queries (the odd channels are divided by 16, which FP16's smallest step
+  // would otherwise cut into).
+  int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
+  e = e < -100 ? -100 : e;
+  const float up = __builtin_bit_cast(float, (uint32_t)(127 + 13 - e) << 23);
+  const float back = __builtin_bit_cast(float, (uint32_t)(127 - 13 + e) << 23);
+  const float logits = a.scale * kLog2e * back;
+  q.unit = logits * 0x1p24f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t x = raw[p][k][e] & 0x7fff7fffu;
-            top = max(top, max(x & 0xffffu, x >> 16));
-          }
-      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-      int e = (int)(top >> 7) - 127;                   // exponent of the largest
-      e = e < -100 ? -100 : e > 126 ? 126 : e;
-      up = __builtin_bit_cast(float, (uint32_t)(127 + 13 - e) << 23);
-      back = __builtin_bit_cast(float, (uint32_t)(127 - 13 + e) << 23);
-    }
+  for (int nb = 0; nb < NB; ++nb) {
     float sum = 0.f;
 #pragma unroll
     for (int p = 0; p < D / 64; ++p) {
       _Float16 h[16];
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        const uint32_t w = raw[p][c >> 3][(c >> 1) & 3];
-        const uint32_t bits = c & 1 ? w >> 16 : w & 0xffffu;
-        if constexpr (BF16) h[c] = (_Float16)(__builtin_bit_cast(float, bits << 16) * up);
-        else h[c] = __builtin_bit_cast(_Float16, (uint16_t)bits);
-        sum += (float)h[c];
+        h[c] = (_Float16)(element(nb, p, c) * (c & 1 ? 0.0625f * up : up));
+        sum += (float)h[c] * (c & 1 ? 16.0f : 1.0f);
       }
       const half8 even = {h[0], h[4], h[8], h[12], h[2], h[6], h[10], h[14]};
       const half8 odd = {h[1], h[5], h[9], h[13], h[3], h[7], h[11], h[15]};
@@ -359,13 +441,8 @@ __device__ __forceinline__ void load_queries(Queries<D, NB>& q, const KvAttentio
       q.odd[nb][p] = __builtin_bit_cast(uint4v, odd);
     }
     sum = groups_sum(sum);
-    const float logits = a.scale * kLog2e * back;
     q.sum8[nb] = sum * -0x1p-21f;
-    q.unit[nb] = logits * 0x1p24f;
     q.sum[nb] = sum * logits;
-    const int pos = sp.len - sp.nq + i;
-    q.hi[nb] = pos;
-    q.lo[nb] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
   }
 }
 
@@ -403,8 +480,12 @@ __device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int gro
 template <int D>
 constexpr int kLdsRow = D + 4;
 
+// Waves per SIMD the registers are divided for.
+template <int D, int NB>
+constexpr int kResident = D * NB <= 128 ? 2 : 1;
+
 template <int D, int NB, bool ROWS, bool BF16>
-__global__ __launch_bounds__(kThreads) void kv_attention_kernel(
+__global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_attention_kernel(
     KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
     float* __restrict__ partials) {
   constexpr int kRowTile = ROWS ? 16 * NB * kWaves : 16 * NB;
@@ -472,16 +553,37 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(
   }
 
   if (begin < end) {
-    const int page_shift = 31 - __builtin_clz((unsigned)a.page);
+    Pages pages;
+    pages.shift = 31 - __builtin_clz((unsigned)a.page);
+    pages.count = a.pages;
+    const uint64_t page_bytes = (uint64_t)(a.page / kKvUnit) * KvUnit<D>::bytes;
+    pages.stride = page_bytes * a.H;
+    pages.head = a.cache + page_bytes * head;
     PageIds ids{a.table + (int64_t)b * a.max_pages, a.max_pages, 0, -1};
-    ids.load(begin >> page_shift);
-    TileData<D> cur, next;
-    load_tile<D>(cur, a, head, page_shift, ids, begin);
-    for (int t = begin; t < end; t += kTile) {
-      if (t + kTile < end) load_tile<D>(next, a, head, page_shift, ids, t + kTile);
-      const bool edge = t < inner_begin || t + kTile > inner_end || !cur.valid[0] || !cur.valid[1];
-      attend<D, NB, BF16>(cur, q, s, t, edge);
-      cur = next;
+    ids.load(begin >> pages.shift);
+    // A ring of tiles in registers: the loads of a tile are issued kAhead
+    // tiles before it is used.  They are issued whatever is left (the last
+    // tile again, at the end): where a branch could skip them, the wait for a
+    // tile would have to allow for both sides and so wait for the next one.
+    constexpr int kAhead = 1;
+    TileData<D> ring[kAhead + 1];
+    const int last = begin + (end - begin - 1) / kTile * kTile;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int t = begin + k * kTile;
+      load_tile<D>(ring[k], pages, ids, t < last ? t : last);
+    }
+    for (int t0 = begin; t0 < end; t0 += (kAhead + 1) * kTile) {
+#pragma unroll
+      for (int k = 0; k <= kAhead; ++k) {
+        const int t = t0 + k * kTile, then = t + kAhead * kTile;
+        if (t >= end) break;
+        load_tile<D>(ring[(k + kAhead) % (kAhead + 1)], pages, ids, then < last ? then : last);
+        const TileData<D>& cur = ring[k];
+        const bool edge =
+            t < inner_begin || t + kTile > inner_end || !cur.valid[0] || !cur.valid[1];
+        attend<D, NB, BF16>(cur, q, s, t, edge);
+      }
     }
   }
 
@@ -542,76 +644,72 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(
       if (g == 0) write_lse(row, s.m[nb], total[nb]);
     }
   } else {
-    // Join the waves, in wave order, through LDS.
-    __shared__ float red[16 * NB * kLdsRow<D>];
+    // Join the waves, in wave order, through LDS: each leaves its rows and
+    // their (m, l), and the threads add them up per element.
+    constexpr int kSlab = 16 * NB * kLdsRow<D>;
+    __shared__ float red[kWaves * kSlab];
     __shared__ float s_m[kWaves][16 * NB], s_l[kWaves][16 * NB];
     __shared__ bool s_last;
-    if (g == 0) {
+    const int rows = sp.rows - row0 < 16 * NB ? sp.rows - row0 : 16 * NB;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        s_m[wave][16 * nb + n16] = s.m[nb];
-        s_l[wave][16 * nb + n16] = total[nb];
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = 16 * nb + n16;
+      if (row >= rows) continue;
+      if (g == 0) {
+        s_m[wave][row] = s.m[nb];
+        s_l[wave][row] = total[nb];
       }
+      float* at = red + wave * kSlab + row * kLdsRow<D> + kCols * 4 * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 16; c += 4)
+          *reinterpret_cast<float4v*>(at + kCols * i + c % kCols + c / kCols * 128) =
+              float4v{s.acc[nb][c][i], s.acc[nb][c + 1][i], s.acc[nb][c + 2][i],
+                      s.acc[nb][c + 3][i]};
     }
     __syncthreads();
-    for (int w = 0; w < kWaves; ++w) {
-      if (wave == w) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int row = 16 * nb + n16;
-          float m = s_m[0][row];
-          for (int o = 1; o < kWaves; ++o) m = fmaxf(m, s_m[o][row]);
-          const float f = exp2_hw(s.m[nb] - m);
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float* at = red + row * kLdsRow<D> + kCols * (4 * g + i) + c % kCols +
-                          c / kCols * 128;
-              const float x = s.acc[nb][c][i] * f;
-              *at = w == 0 ? x : *at + x;
-            }
-        }
-      }
-      __syncthreads();
-    }
-    const int rows = sp.rows - row0 < 16 * NB ? sp.rows - row0 : 16 * NB;
-    auto joined = [&](int row, float* m_out) {
+    // Four neighbouring channels of a row over all waves, and its (m, l).
+    auto joined = [&](int row, int ch, float* m_out, float* l_out) {
       float m = s_m[0][row], l = 0.f;
+#pragma unroll
       for (int o = 1; o < kWaves; ++o) m = fmaxf(m, s_m[o][row]);
-      for (int o = 0; o < kWaves; ++o) l += s_l[o][row] * exp2_hw(s_m[o][row] - m);
+      float4_t x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int o = 0; o < kWaves; ++o) {
+        const float f = exp2_hw(s_m[o][row] - m);
+        l += s_l[o][row] * f;
+        x += *reinterpret_cast<const float4_t*>(red + o * kSlab + row * kLdsRow<D> + ch) * f;
+      }
       *m_out = m;
-      return l;
+      *l_out = l;
+      return x;
     };
     constexpr int kVecs = D / 4;
     if (parts == 1) {
       for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
         const int row = v / kVecs, ch = v % kVecs * 4;
-        float m;
-        const float l = joined(row, &m);
-        write_out(row0 + row, ch, red + row * kLdsRow<D> + ch, l == 0.f ? 0.f : 1.0f / l);
+        float m, l;
+        const float4_t x = joined(row, ch, &m, &l);
+        const float out[4] = {x[0], x[1], x[2], x[3]};
+        write_out(row0 + row, ch, out, l == 0.f ? 0.f : 1.0f / l);
         if (ch == 0) write_lse(row0 + row, m, l);
       }
       return;
     }
-    // Publish this workgroup's rows and (m, l), then count the arrival; the
-    // last workgroup of the row tile joins them in split order.
+    // Publish this workgroup's rows, each as D channels and (m, l), then
+    // count the arrival; the last workgroup of the row tile joins them in
+    // split order.
     constexpr int kRowFloats = D + 4;
     const int64_t part_floats = (int64_t)16 * NB * kRowFloats;
     const float* tile_base = partials + (int64_t)work * splits * part_floats;
     {
       const __amdgpu_buffer_rsrc_t mine = coherent_rsrc(tile_base + split * part_floats);
-      for (int v = threadIdx.x; v < rows * (kVecs + 1); v += kThreads) {
-        const int row = v / (kVecs + 1), c = v % (kVecs + 1);
-        float4_t x;
-        if (c < kVecs) {
-          x = *reinterpret_cast<const float4_t*>(red + row * kLdsRow<D> + 4 * c);
-        } else {
-          float m;
-          const float l = joined(row, &m);
-          x = float4_t{m, l, 0.f, 0.f};
-        }
-        store_coherent(mine, v, x);
+      for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
+        const int row = v / kVecs, c = v % kVecs;
+        float m, l;
+        store_coherent(mine, row * (kVecs + 1) + c, joined(row, 4 * c, &m, &l));
+        if (c == 0) store_coherent(mine, row * (kVecs + 1) + kVecs, float4_t{m, l, 0.f, 0.f});
       }
     }
     __builtin_amdgcn_s_waitcnt(0);
@@ -623,19 +721,37 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(
     }
     __syncthreads();
     if (!s_last) return;
+    // One resource over all parts: its offsets stay below 2 GiB (the
+    // workspace is far smaller).
+    const __amdgpu_buffer_rsrc_t all = coherent_rsrc(tile_base);
+    const int part_vecs = (int)(part_floats / 4);
     for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
       const int row = v / kVecs, c = v % kVecs;
+      const int at = row * (kVecs + 1) + c, stat = row * (kVecs + 1) + kVecs;
       float m = kNone, l = 0.f;
       float4_t x = {0.f, 0.f, 0.f, 0.f};
-      for (int o = 0; o < parts; ++o) {
-        const __amdgpu_buffer_rsrc_t part = coherent_rsrc(tile_base + o * part_floats);
-        const float4_t ml = load_coherent(part, row * (kVecs + 1) + kVecs);
-        const float4_t y = load_coherent(part, row * (kVecs + 1) + c);
-        const float to = fmaxf(m, ml[0]);
-        const float f0 = exp2_hw(m - to), f1 = exp2_hw(ml[0] - to);
-        x = x * f0 + y * f1;
-        l = l * f0 + ml[1] * f1;
+      constexpr int kBatch = 16;  // parts whose loads are in flight together
+      for (int o0 = 0; o0 < parts; o0 += kBatch) {
+        float4_t ml[kBatch], y[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int o = o0 + k < parts ? o0 + k : parts - 1;
+          ml[k] = load_coherent(all, o * part_vecs + stat);
+          y[k] = load_coherent(all, o * part_vecs + at);
+        }
+        float to = m;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) to = fmaxf(to, ml[k][0]);
+        const float f = exp2_hw(m - to);
+        x *= f;
+        l *= f;
         m = to;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const float w = o0 + k < parts ? exp2_hw(ml[k][0] - to) : 0.f;
+          x += y[k] * w;
+          l += ml[k][1] * w;
+        }
       }
       const float out[4] = {x[0], x[1], x[2], x[3]};
       write_out(row0 + row, 4 * c, out, l == 0.f ? 0.f : 1.0f / l);
@@ -686,10 +802,24 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
   p.chunk = (int)(keys < (1 << 30) ? keys : (1 << 30));
   const int64_t work = (int64_t)B * H * p.tiles;
   if (!p.rows && work <= kMaxSplitTiles) {
-    // two workgroups per compute unit; a wave has at least two tiles
-    const int64_t want = (2 * (int64_t)cus + work - 1) / work;
-    const int64_t most = keys / (2 * kWaves * kTile);
-    int64_t n = want < most ? want : most;
+    // Token ranges: rounds of resident workgroups times the steps of a wave
+    // in one, of which starting, joining the waves and joining the ranges
+    // are worth about kStart, kJoin steps.
+    constexpr int64_t kStart = 5, kJoin = 3;
+    const int64_t slots = (int64_t)cus * (D * p.nb <= 128 ? 2 : 1);
+    const int64_t steps = keys / kTile;
+    int64_t most = 8 * slots / work + 1;
+    if (most > (steps + kWaves - 1) / kWaves) most = (steps + kWaves - 1) / kWaves;
+    int64_t best = 0, n = 1;
+    for (int64_t i = 1; i <= most; ++i) {
+      const int64_t rounds = (work * i + slots - 1) / slots;
+      const int64_t each = ((steps + i - 1) / i + kWaves - 1) / kWaves;
+      const int64_t cost = rounds * (each + kStart) + (i > 1 ? kJoin : 0);
+      if (i == 1 || cost < best) {
+        best = cost;
+        n = i;
+      }
+    }
     if (n > 1) {
       p.chunk = (int)((keys + n - 1) / n + kTile - 1) / kTile * kTile;
       p.splits = (int)((keys + p.chunk - 1) / p.chunk);
