@@ -23,7 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libw4a16.so")
 PROBES_LIB = os.path.join(PKG, "libw4a16_probes.so")
 SOURCES = ["api.hip", "gemm.hip", "gemm_lds.hip", "gemm_sk.hip", "gemm_sk_fmt.hip", "repack.hip", "dequant.hip",
-           "kv4_api.hip", "kv4_tables.hip", "kv4_append.hip", "kv4_attention.hip"]
+           "kv4_api.hip", "kv4_tables.hip", "kv4_append.hip", "kv4_attention.hip",
+           "kv4_prefill.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

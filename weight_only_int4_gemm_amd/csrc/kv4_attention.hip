@@ -30,12 +30,7 @@
 // outputs it would be as large as it, so there the weights are two FP16
 // numbers, the rounded weight and its remainder, and the product with the
 // values runs twice.
-#include <cstdio>
-
-#include "../../include/w4a16_kv4.h"
-#include "coherent.hpp"
-#include "internal.hpp"
-#include "kv4.hpp"
+#include "kv4_attention.hpp"
 
 namespace w4a16 {
 namespace {
@@ -43,66 +38,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kWaitLoads = 0x0f70;          // s_waitcnt: all vector loads, nothing else
-constexpr int kTile = 32;                   // tokens of one step: two units
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kNone = -1e30f;             // reference of a column that has seen no key
-constexpr float kMostWeight = 32768.0f;     // of a weight, before the reference moves
-constexpr float kTopWeight = 8.0f;          // log2 of the largest weight after it has
-constexpr float kMostSum = 0x1p60f;         // of a tile's probabilities, likewise
-constexpr float kSumHeadroom = 40.0f;       // log2 of a probability over the reference
-
-typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
-typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-typedef float float4v __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
-
-__device__ __forceinline__ float4v mfma(const uint4v& a, const uint4v& b, const float4v& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a),
-                                                __builtin_bit_cast(half8, b), c, 0, 0, 0);
-}
-
-__device__ __forceinline__ float low_half(uint32_t w) {
-  return (float)__builtin_bit_cast(half2v, w)[0];
-}
-__device__ __forceinline__ float high_half(uint32_t w) {
-  return (float)__builtin_bit_cast(half2v, w)[1];
-}
-__device__ __forceinline__ uint32_t pack_halves(float a, float b) {
-  const half2v h = {(_Float16)a, (_Float16)b};  // round half to even
-  return __builtin_bit_cast(uint32_t, h);
-}
-
-// x times or less a half of w, in one instruction (written out, the compiler
-// converts first and multiplies or subtracts then).
-__device__ __forceinline__ float times_low_half(float x, uint32_t w) {
-  float y;
-  asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel_hi:[0,1,0]" : "=v"(y) : "v"(x), "v"(w));
-  return y;
-}
-__device__ __forceinline__ float less_low_half(float x, uint32_t w) {
-  float y;
-  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(y) : "v"(w), "v"(x));
-  return y;
-}
-__device__ __forceinline__ float less_high_half(float x, uint32_t w) {
-  float y;
-  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
-      : "=v"(y) : "v"(w), "v"(x));
-  return y;
-}
-
-// Keeps the compiler from doing a rare branch's work always, with selects,
-// and from sharing its conversions with the usual path, where they cost
-// nothing as operands of a mixed-precision instruction.
-__device__ __forceinline__ void keep_branch() { asm volatile(""); }
-__device__ __forceinline__ uint32_t apart(uint32_t w) {
-  asm volatile("" : "+v"(w));
-  return w;
-}
 
 // Sum and maximum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_sum(float x) {
@@ -367,14 +302,6 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
   }
 }
 
-// Query rows of a workgroup and the tokens they see.
-struct Span {
-  int len, nq, tok0;    // tokens held, queries, first query row of the request
-  int rows;             // query rows (query, head of the group) of the request
-  int begin, end;       // tokens any row of the tile sees: begin (multiple of
-                        // kTile) <= j < end
-};
-
 template <int D, int NB, bool BF16>
 __device__ __forceinline__ void load_queries(Queries<D, NB>& q, const KvAttentionArgs& a,
                                              const Span& sp, int head, int group, int row0) {
@@ -446,35 +373,6 @@ __device__ __forceinline__ void load_queries(Queries<D, NB>& q, const KvAttentio
   }
 }
 
-// The tokens of a row tile.
-__device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int group, int row0,
-                                        int row_tile) {
-  Span s;
-  const int64_t most = (int64_t)a.max_pages * a.page;
-  const int len = a.lens[b] > 0 ? a.lens[b] : 0;
-  s.len = len < most ? len : (int)most;
-  if (a.q_start) {
-    int lo = a.q_start[b], hi = a.q_start[b + 1];
-    lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
-    hi = hi < lo ? lo : hi > a.T ? a.T : hi;
-    s.tok0 = lo;
-    s.nq = hi - lo;
-  } else {
-    s.tok0 = b;
-    s.nq = b < a.T;
-  }
-  // queries beyond max_q are not computed
-  const int nq = s.nq < a.max_q ? s.nq : a.max_q;
-  s.rows = nq * group;
-  const int last = row0 + row_tile < s.rows ? row0 + row_tile : s.rows;
-  const int first_pos = s.len - s.nq + row0 / group;
-  const int last_pos = s.len - s.nq + (last - 1) / group;
-  s.begin = a.window > 0 && first_pos >= a.window ? first_pos - a.window + 1 : 0;
-  s.begin &= ~(kTile - 1);
-  s.end = last_pos + 1 > s.begin ? last_pos + 1 : s.begin;
-  return s;
-}
-
 // Rows of D floats of a block in LDS, padded so that the 16 rows of a store
 // fall on different banks.
 template <int D>
@@ -484,11 +382,11 @@ constexpr int kLdsRow = D + 4;
 template <int D, int NB>
 constexpr int kResident = D * NB <= 128 ? 2 : 1;
 
-template <int D, int NB, bool ROWS, bool BF16>
-__global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_attention_kernel(
+template <int D, int NB, bool BF16>
+__global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel(
     KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
     float* __restrict__ partials) {
-  constexpr int kRowTile = ROWS ? 16 * NB * kWaves : 16 * NB;
+  constexpr int kRowTile = 16 * NB;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.Hq / a.H;
   int id = blockIdx.x;
@@ -501,32 +399,15 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_attention_ker
   const int row0 = tile * kRowTile;
   const Span sp = span_of(a, b, group, row0, kRowTile);
   if (row0 >= sp.rows) return;
-
-  // This workgroup's tokens.
-  int per = chunk;
-  int parts = (sp.end - sp.begin + per - 1) / per;
-  if (parts > splits) {
-    per = ((sp.end - sp.begin + splits - 1) / splits + kTile - 1) / kTile * kTile;
-    parts = (sp.end - sp.begin + per - 1) / per;
-  }
-  if (parts < 1) parts = 1;
-  if (split >= parts) return;
-  int begin = sp.begin + split * per;
-  int end = begin + per < sp.end ? begin + per : sp.end;
-
-  int wave_row0 = row0;
-  if constexpr (ROWS) {
-    wave_row0 = row0 + 16 * NB * wave;
-  } else {
-    const int n = (end - begin + kTile - 1) / kTile;
-    const int each = (n + kWaves - 1) / kWaves;
-    begin += wave * each * kTile;
-    const int stop = begin + each * kTile;
-    end = stop < end ? stop : end;
-  }
+  const Range range = range_of(sp, split, splits, chunk);
+  if (split >= range.parts) return;
+  // the waves divide the range
+  const int each = ((range.end - range.begin + kTile - 1) / kTile + kWaves - 1) / kWaves * kTile;
+  const int begin = range.begin + wave * each;
+  const int end = begin + each < range.end ? begin + each : range.end;
 
   Queries<D, NB> q;
-  load_queries<D, NB, BF16>(q, a, sp, head, group, wave_row0);
+  load_queries<D, NB, BF16>(q, a, sp, head, group, row0);
   Sums<D, NB> s;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
@@ -537,20 +418,12 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_attention_ker
     for (int c = 0; c < D / 16; ++c) s.acc[nb][c] = float4v{0.f, 0.f, 0.f, 0.f};
   }
 
-  // Inner tiles, which every row of the wave sees whole, need no mask.
-  int row_last = wave_row0 + 16 * NB < sp.rows ? wave_row0 + 16 * NB - 1 : sp.rows - 1;
-  const int row_first = wave_row0 < sp.rows ? wave_row0 : sp.rows - 1;
-  const int pos_first = sp.len - sp.nq + row_first / group;
+  // Inner tiles, which every row sees whole, need no mask.
+  const int row_last = row0 + kRowTile < sp.rows ? row0 + kRowTile - 1 : sp.rows - 1;
+  const int pos_first = sp.len - sp.nq + row0 / group;
   const int pos_last = sp.len - sp.nq + row_last / group;
   const int inner_end = pos_first + 1;  // exclusive
   const int inner_begin = a.window > 0 && pos_last >= a.window ? pos_last - a.window + 1 : 0;
-
-  if constexpr (ROWS) {  // this wave's share of the tile's tokens; none past the last row
-    const int window_begin = a.window > 0 && pos_first >= a.window
-                                 ? (pos_first - a.window + 1) & ~(kTile - 1) : 0;
-    begin = begin > window_begin ? begin : window_begin;
-    end = wave_row0 >= sp.rows ? begin : end < pos_last + 1 ? end : pos_last + 1;
-  }
 
   if (begin < end) {
     Pages pages;
@@ -602,198 +475,119 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_attention_ker
   }
 
   constexpr int kCols = D == 64 ? 4 : 8;  // neighbouring channels of a lane
-  auto write_out = [&](int row, int ch, const float* x, float inv) {
-    const int i = row / group;
-    uint16_t* dst = a.o + (int64_t)(sp.tok0 + i) * a.o_token +
-                    (int64_t)(head * group + row - i * group) * a.o_head + ch;
-    uint32_t w[2];
+  // Join the waves, in wave order, through LDS: each leaves its rows and
+  // their (m, l), and the threads add them up per element.
+  constexpr int kSlab = 16 * NB * kLdsRow<D>;
+  __shared__ float red[kWaves * kSlab];
+  __shared__ float s_m[kWaves][16 * NB], s_l[kWaves][16 * NB];
+  __shared__ bool s_last;
+  const int rows = sp.rows - row0 < 16 * NB ? sp.rows - row0 : 16 * NB;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if constexpr (BF16) {
-        const __bf16 lo = (__bf16)(x[2 * k] * inv), hi = (__bf16)(x[2 * k + 1] * inv);
-        w[k] = (uint32_t)__builtin_bit_cast(uint16_t, lo) |
-               (uint32_t)__builtin_bit_cast(uint16_t, hi) << 16;
-      } else {
-        w[k] = pack_halves(x[2 * k] * inv, x[2 * k + 1] * inv);
-      }
+  for (int nb = 0; nb < NB; ++nb) {
+    const int row = 16 * nb + n16;
+    if (row >= rows) continue;
+    if (g == 0) {
+      s_m[wave][row] = s.m[nb];
+      s_l[wave][row] = total[nb];
     }
-    *reinterpret_cast<uint2v*>(dst) = uint2v{w[0], w[1]};
+    float* at = red + wave * kSlab + row * kLdsRow<D> + kCols * 4 * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < D / 16; c += 4)
+        *reinterpret_cast<float4v*>(at + kCols * i + c % kCols + c / kCols * 128) =
+            float4v{s.acc[nb][c][i], s.acc[nb][c + 1][i], s.acc[nb][c + 2][i],
+                    s.acc[nb][c + 3][i]};
+  }
+  __syncthreads();
+  // Four neighbouring channels of a row over all waves, and its (m, l).
+  auto joined = [&](int row, int ch, float* m_out, float* l_out) {
+    float m = s_m[0][row], l = 0.f;
+#pragma unroll
+    for (int o = 1; o < kWaves; ++o) m = fmaxf(m, s_m[o][row]);
+    float4_t x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int o = 0; o < kWaves; ++o) {
+      const float f = exp2_hw(s_m[o][row] - m);
+      l += s_l[o][row] * f;
+      x += *reinterpret_cast<const float4_t*>(red + o * kSlab + row * kLdsRow<D> + ch) * f;
+    }
+    *m_out = m;
+    *l_out = l;
+    return x;
   };
-  auto write_lse = [&](int row, float m, float l) {
-    if (!a.lse) return;
-    const int i = row / group;
-    a.lse[(int64_t)(sp.tok0 + i) * a.Hq + head * group + row - i * group] =
-        l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
-  };
-
-  if constexpr (ROWS) {
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int row = wave_row0 + 16 * nb + n16;
-      if (row >= sp.rows) continue;
-      const float inv = total[nb] == 0.f ? 0.f : 1.0f / total[nb];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < D / 16; c += 4) {
-          const int ch = kCols * (4 * g + i) + c % kCols + c / kCols * 128;
-          const float x[4] = {s.acc[nb][c][i], s.acc[nb][c + 1][i], s.acc[nb][c + 2][i],
-                              s.acc[nb][c + 3][i]};
-          write_out(row, ch, x, inv);
-        }
-      if (g == 0) write_lse(row, s.m[nb], total[nb]);
+  constexpr int kVecs = D / 4;
+  const Output out(a, sp, head, group);
+  if (range.parts == 1) {
+    for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
+      const int row = v / kVecs, ch = v % kVecs * 4;
+      float m, l;
+      const float4_t x = joined(row, ch, &m, &l);
+      const float y[4] = {x[0], x[1], x[2], x[3]};
+      out.store<BF16, 4>(row0 + row, ch, y, l == 0.f ? 0.f : 1.0f / l);
+      if (ch == 0) out.store_lse(row0 + row, m, l);
     }
-  } else {
-    // Join the waves, in wave order, through LDS: each leaves its rows and
-    // their (m, l), and the threads add them up per element.
-    constexpr int kSlab = 16 * NB * kLdsRow<D>;
-    __shared__ float red[kWaves * kSlab];
-    __shared__ float s_m[kWaves][16 * NB], s_l[kWaves][16 * NB];
-    __shared__ bool s_last;
-    const int rows = sp.rows - row0 < 16 * NB ? sp.rows - row0 : 16 * NB;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int row = 16 * nb + n16;
-      if (row >= rows) continue;
-      if (g == 0) {
-        s_m[wave][row] = s.m[nb];
-        s_l[wave][row] = total[nb];
-      }
-      float* at = red + wave * kSlab + row * kLdsRow<D> + kCols * 4 * g;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < D / 16; c += 4)
-          *reinterpret_cast<float4v*>(at + kCols * i + c % kCols + c / kCols * 128) =
-              float4v{s.acc[nb][c][i], s.acc[nb][c + 1][i], s.acc[nb][c + 2][i],
-                      s.acc[nb][c + 3][i]};
-    }
-    __syncthreads();
-    // Four neighbouring channels of a row over all waves, and its (m, l).
-    auto joined = [&](int row, int ch, float* m_out, float* l_out) {
-      float m = s_m[0][row], l = 0.f;
-#pragma unroll
-      for (int o = 1; o < kWaves; ++o) m = fmaxf(m, s_m[o][row]);
-      float4_t x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int o = 0; o < kWaves; ++o) {
-        const float f = exp2_hw(s_m[o][row] - m);
-        l += s_l[o][row] * f;
-        x += *reinterpret_cast<const float4_t*>(red + o * kSlab + row * kLdsRow<D> + ch) * f;
-      }
-      *m_out = m;
-      *l_out = l;
-      return x;
-    };
-    constexpr int kVecs = D / 4;
-    if (parts == 1) {
-      for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
-        const int row = v / kVecs, ch = v % kVecs * 4;
-        float m, l;
-        const float4_t x = joined(row, ch, &m, &l);
-        const float out[4] = {x[0], x[1], x[2], x[3]};
-        write_out(row0 + row, ch, out, l == 0.f ? 0.f : 1.0f / l);
-        if (ch == 0) write_lse(row0 + row, m, l);
-      }
-      return;
-    }
-    // Publish this workgroup's rows, each as D channels and (m, l), then
-    // count the arrival; the last workgroup of the row tile joins them in
-    // split order.
-    constexpr int kRowFloats = D + 4;
-    const int64_t part_floats = (int64_t)16 * NB * kRowFloats;
-    const float* tile_base = partials + (int64_t)work * splits * part_floats;
-    {
-      const __amdgpu_buffer_rsrc_t mine = coherent_rsrc(tile_base + split * part_floats);
-      for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
-        const int row = v / kVecs, c = v % kVecs;
-        float m, l;
-        store_coherent(mine, row * (kVecs + 1) + c, joined(row, 4 * c, &m, &l));
-        if (c == 0) store_coherent(mine, row * (kVecs + 1) + kVecs, float4_t{m, l, 0.f, 0.f});
-      }
-    }
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const unsigned prev = __hip_atomic_fetch_add(counters + work, 1u, __ATOMIC_RELAXED,
-                                                   __HIP_MEMORY_SCOPE_AGENT);
-      s_last = prev == (unsigned)(parts - 1);
-    }
-    __syncthreads();
-    if (!s_last) return;
-    // One resource over all parts: its offsets stay below 2 GiB (the
-    // workspace is far smaller).
-    const __amdgpu_buffer_rsrc_t all = coherent_rsrc(tile_base);
-    const int part_vecs = (int)(part_floats / 4);
+    return;
+  }
+  // Publish this workgroup's rows, then count the arrival; the last
+  // workgroup of the row tile joins them in range order.
+  constexpr int kVecsOfPart = kRowTile * kPartVecs<D>;
+  const float* tile_base = partials + (int64_t)work * splits * kVecsOfPart * 4;
+  {
+    const __amdgpu_buffer_rsrc_t mine = coherent_rsrc(tile_base + split * kVecsOfPart * 4);
     for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
       const int row = v / kVecs, c = v % kVecs;
-      const int at = row * (kVecs + 1) + c, stat = row * (kVecs + 1) + kVecs;
-      float m = kNone, l = 0.f;
-      float4_t x = {0.f, 0.f, 0.f, 0.f};
-      constexpr int kBatch = 16;  // parts whose loads are in flight together
-      for (int o0 = 0; o0 < parts; o0 += kBatch) {
-        float4_t ml[kBatch], y[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int o = o0 + k < parts ? o0 + k : parts - 1;
-          ml[k] = load_coherent(all, o * part_vecs + stat);
-          y[k] = load_coherent(all, o * part_vecs + at);
-        }
-        float to = m;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) to = fmaxf(to, ml[k][0]);
-        const float f = exp2_hw(m - to);
-        x *= f;
-        l *= f;
-        m = to;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const float w = o0 + k < parts ? exp2_hw(ml[k][0] - to) : 0.f;
-          x += y[k] * w;
-          l += ml[k][1] * w;
-        }
-      }
-      const float out[4] = {x[0], x[1], x[2], x[3]};
-      write_out(row0 + row, 4 * c, out, l == 0.f ? 0.f : 1.0f / l);
-      if (c == 0) write_lse(row0 + row, m, l);
+      float m, l;
+      store_coherent(mine, row * kPartVecs<D> + c, joined(row, 4 * c, &m, &l));
+      if (c == 0) store_coherent(mine, row * kPartVecs<D> + kVecs, float4_t{m, l, 0.f, 0.f});
     }
-    if (threadIdx.x == 0)  // ready for the next call
-      __hip_atomic_store(counters + work, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  if (last_to_arrive(counters + work, range.parts, &s_last))
+    join_parts<D, BF16, kThreads>(tile_base, kVecsOfPart, range.parts, rows, row0, out,
+                                  counters + work);
 }
 
-template <int D, int NB, bool ROWS>
+template <int D, int NB>
 hipError_t launch(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
                   unsigned* counters, float* partials, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)a.B * a.H * p.tiles * p.splits));
   if (dtype == W4A16_DTYPE_BF16)
-    hipLaunchKernelGGL((kv_attention_kernel<D, NB, ROWS, true>), grid, dim3(kThreads), 0, stream,
-                       a, p.tiles, p.splits, p.chunk, counters, partials);
+    hipLaunchKernelGGL((kv_tokens_kernel<D, NB, true>), grid, dim3(kThreads), 0, stream, a,
+                       p.tiles, p.splits, p.chunk, counters, partials);
   else
-    hipLaunchKernelGGL((kv_attention_kernel<D, NB, ROWS, false>), grid, dim3(kThreads), 0, stream,
-                       a, p.tiles, p.splits, p.chunk, counters, partials);
+    hipLaunchKernelGGL((kv_tokens_kernel<D, NB, false>), grid, dim3(kThreads), 0, stream, a,
+                       p.tiles, p.splits, p.chunk, counters, partials);
   return hipGetLastError();
 }
 
+// A second block of 256-channel rows does not fit the registers.
 template <int D>
 hipError_t launch_d(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
                     unsigned* counters, float* partials, hipStream_t stream) {
-  constexpr int kWide = D == 256 ? 1 : 2;  // a second block of rows does not fit the registers
-  if (p.rows) return launch<D, kWide, true>(p, a, dtype, counters, partials, stream);
-  if (p.nb == 1) return launch<D, 1, false>(p, a, dtype, counters, partials, stream);
-  return launch<D, kWide, false>(p, a, dtype, counters, partials, stream);
+  if (p.nb == 1) return launch<D, 1>(p, a, dtype, counters, partials, stream);
+  return launch<D, D == 256 ? 1 : 2>(p, a, dtype, counters, partials, stream);
 }
 
 }  // namespace
+
+hipError_t launch_kv_tokens(const KvAttentionPlan& p, const KvAttentionArgs& a, int D, int dtype,
+                            unsigned* counters, float* partials, hipStream_t stream) {
+  switch (D) {
+    case 64: return launch_d<64>(p, a, dtype, counters, partials, stream);
+    case 128: return launch_d<128>(p, a, dtype, counters, partials, stream);
+    default: return launch_d<256>(p, a, dtype, counters, partials, stream);
+  }
+}
 
 KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, int max_len,
                                        int window, int cus) {
   KvAttentionPlan p{};
   const int64_t rows = (int64_t)(Hq / H) * max_q;
-  p.waves = kWaves;
+  // Many rows: the waves of a workgroup take 32 each and share the tokens.
   p.rows = rows > 64;
-  p.nb = D < 256 && rows > 16 ? 2 : 1;
-  const int tile_rows = 16 * p.nb * (p.rows ? kWaves : 1);
+  p.nb = p.rows ? 2 : D < 256 && rows > 16 ? 2 : 1;
+  p.waves = !p.rows ? kWaves : D == 256 ? 4 : 8;
+  const int tile_rows = 16 * p.nb * (p.rows ? p.waves : 1);
   p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
   p.splits = 1;
   int64_t keys = max_len;
@@ -801,19 +595,20 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
   keys = (keys + kTile - 1) / kTile * kTile + kTile;
   p.chunk = (int)(keys < (1 << 30) ? keys : (1 << 30));
   const int64_t work = (int64_t)B * H * p.tiles;
-  if (!p.rows && work <= kMaxSplitTiles) {
+  if (work <= kMaxSplitTiles) {
     // Token ranges: rounds of resident workgroups times the steps of a wave
     // in one, of which starting, joining the waves and joining the ranges
     // are worth about kStart, kJoin steps.
     constexpr int64_t kStart = 5, kJoin = 3;
-    const int64_t slots = (int64_t)cus * (D * p.nb <= 128 ? 2 : 1);
+    const int64_t slots = (int64_t)cus * (!p.rows && D * p.nb <= 128 ? 2 : 1);
+    const int64_t sharing = p.rows ? 1 : kWaves;  // waves that divide the tokens
     const int64_t steps = keys / kTile;
     int64_t most = 8 * slots / work + 1;
-    if (most > (steps + kWaves - 1) / kWaves) most = (steps + kWaves - 1) / kWaves;
+    if (most > (steps + sharing - 1) / sharing) most = (steps + sharing - 1) / sharing;
     int64_t best = 0, n = 1;
     for (int64_t i = 1; i <= most; ++i) {
       const int64_t rounds = (work * i + slots - 1) / slots;
-      const int64_t each = ((steps + i - 1) / i + kWaves - 1) / kWaves;
+      const int64_t each = ((steps + i - 1) / i + sharing - 1) / sharing;
       const int64_t cost = rounds * (each + kStart) + (i > 1 ? kJoin : 0);
       if (i == 1 || cost < best) {
         best = cost;
@@ -826,8 +621,8 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
     }
   }
   if (p.splits > 1)
-    p.workspace_bytes = kCounterHeaderBytes + (size_t)work * p.splits * 16 * p.nb *
-                                                  (D + 4) * sizeof(float);
+    p.workspace_bytes = kCounterHeaderBytes + (size_t)work * p.splits * tile_rows * (D + 4) *
+                                                  sizeof(float);
   return p;
 }
 
@@ -836,11 +631,8 @@ hipError_t launch_kv_attention(const KvAttentionPlan& p, const KvAttentionArgs& 
   unsigned* counters = static_cast<unsigned*>(workspace);
   float* partials =
       reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterHeaderBytes);
-  switch (D) {
-    case 64: return launch_d<64>(p, a, dtype, counters, partials, stream);
-    case 128: return launch_d<128>(p, a, dtype, counters, partials, stream);
-    default: return launch_d<256>(p, a, dtype, counters, partials, stream);
-  }
+  return p.rows ? launch_kv_rows(p, a, D, dtype, counters, partials, stream)
+                : launch_kv_tokens(p, a, D, dtype, counters, partials, stream);
 }
 
 }  // namespace w4a16

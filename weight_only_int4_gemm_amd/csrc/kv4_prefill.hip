@@ -1,0 +1,499 @@
+// kv4_attention for many query rows: chunks of prompts, long drafts.
+//
+// The mathematics of kv4_attention.hip, arranged for rows.  A workgroup of
+// WAVES waves takes 32 * WAVES query rows, 32 per wave, and walks their
+// tokens 64 at a time.  Each step's codes are unpacked once per workgroup,
+// into LDS, as the exact FP16 integers c - 8 and in the order in which the
+// 32x32x16 matrix instruction takes its first operand, so a wave spends its
+// vector instructions on the softmax alone and reads every operand with one
+// conflict-free 16-byte LDS read.  The codes of the step after next are
+// loaded, and those of the next one unpacked, around the products of the
+// current one: one barrier per step, two stages of LDS.
+//
+// Operands.  Scores: keys first (rows = 32 tokens), queries second (columns =
+// 32 query rows); lane l has column l % 32 and, for i in 0..15, token
+// 8 (i / 4) + 4 (l / 32) + i % 4.  Values: transposed values first (rows =
+// 32 channels), weights second (k = 16 tokens): half h = l / 32 supplies the
+// tokens 4 h + j and 8 + 4 h + j of a unit, the ones it has scores of.  Row r
+// of channel block b stands for channel 8 (r % W) + M b + r / W, where
+// W = D / 8 words and M = 32 / W, so that a producer lane's word fills 16
+// bytes at neighbouring places and a lane ends up with eight neighbouring
+// channels.
+#include "kv4_attention.hpp"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kStep = 64;  // tokens of a step: two tiles, four units
+
+typedef float float16v __attribute__((ext_vector_type(16)));
+
+template <int D>
+constexpr int kRowWaves = D == 256 ? 4 : 8;
+
+template <int D>
+struct Stage {
+  static constexpr int F = D / 16, CB = D / 32;
+  uint4v k[2][F][64];      // [tile][16 channels][lane]
+  uint4v v[2][2][CB][64];  // [tile][unit][channel block][lane]
+  float ks[kStep];         // key scale in the logits' unit
+  float kz[kStep];         // key offset
+  uint32_t vp[kStep];      // value (scale, offset)
+  uint64_t there;          // tokens whose page exists
+};
+
+__device__ __forceinline__ float16v mfma32(const uint4v& a, const uint4v& b, const float16v& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a),
+                                                __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+
+// The codes in bits 0..3 (low) or 4..7 (high) of both halves, less 8: the
+// bits of 1024 + c or 64 + c, less 1032 or 72.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
+  const half2v h = __builtin_bit_cast(half2v, (w & 0x000f000fu) | 0x64006400u);
+  return __builtin_bit_cast(uint32_t, h - half2v{(_Float16)1032.f, (_Float16)1032.f});
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
+  const half2v h = __builtin_bit_cast(half2v, (w & 0x00f000f0u) | 0x54005400u);
+  return __builtin_bit_cast(uint32_t, h - half2v{(_Float16)72.f, (_Float16)72.f});
+}
+
+// What a wave unpacks of a step.  The step is divided into wave jobs: key job
+// q takes words 4 q .. + 3 of all 64 tokens (one per lane); a value job takes,
+// per lane, half of the channels of one word for the eight tokens of one unit
+// that one lane half multiplies.
+template <int D>
+struct Producer {
+  static constexpr int W = D / 8;
+  static constexpr int kKeyJobs = D / 32, kValueJobs = W * 16 / 64;
+  static constexpr int kJobs = kKeyJobs + kValueJobs;
+  static constexpr int kMine = (kJobs + kRowWaves<D> - 1) / kRowWaves<D>;
+
+  const uint8_t* head;   // the head's first page
+  uint64_t stride;       // bytes of a page over all heads
+  const int32_t* row;    // the request's page ids
+  int shift, max_pages, pages, wave;
+  int id[kMine];         // page of the next step's codes
+  uint4v a[kMine], b[kMine];
+  uint32_t params;
+  bool valid;
+
+  // the token of the step that lane and job look at
+  __device__ __forceinline__ int token_of(int job) const {
+    const int lane = threadIdx.x & 63;
+    return job < kKeyJobs ? lane : ((job - kKeyJobs) * 64 + lane) / (4 * W) * kKvUnit;
+  }
+  __device__ __forceinline__ void find(int t) {  // page ids of step t
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int job = wave + m * kRowWaves<D>;
+      const int page = (t + token_of(job)) >> shift;
+      id[m] = job < kJobs && page < max_pages ? row[page] : -1;
+    }
+  }
+  __device__ __forceinline__ void load(int t) {  // codes of step t, whose ids are found
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int job = wave + m * kRowWaves<D>;
+      if (job >= kJobs) break;
+      const bool there = (unsigned)id[m] < (unsigned)pages;
+      const int pos = t + token_of(job);
+      const uint8_t* unit = head + (uint64_t)(uint32_t)(there ? id[m] : 0) * stride +
+                            (uint32_t)((pos & ((1 << shift) - 1)) / kKvUnit * KvUnit<D>::bytes);
+      if (job < kKeyJobs) {
+        const uint32_t r = lane % kKvUnit;
+        a[m] = *reinterpret_cast<const uint4v*>(unit + r * (D / 2) + 16 * job);
+        // the first two key jobs bring the parameters, too
+        if (job < 2)
+          params = *reinterpret_cast<const uint32_t*>(
+              unit + (job == 0 ? KvUnit<D>::key_params : KvUnit<D>::value_params) + 4 * r);
+        valid = there;
+      } else {
+        const int x = (job - kKeyJobs) * 64 + lane;
+        const uint32_t w = x % W, h = x / W % 2;
+        const uint8_t* v = unit + KvUnit<D>::values + 16 * (h * W + w);
+        a[m] = *reinterpret_cast<const uint4v*>(v);
+        b[m] = *reinterpret_cast<const uint4v*>(v + 32 * W);
+      }
+    }
+  }
+  __device__ __forceinline__ void unpack(Stage<D>& st, float unit_of_logits) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int job = wave + m * kRowWaves<D>;
+      if (job >= kJobs) break;
+      if (job < kKeyJobs) {
+        const int tile = lane / 32, r = lane % 32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = a[m][i], w8 = w >> 8;
+          const int word = 4 * job + i;
+          st.k[tile][word / 2][32 * (word % 2) + r] =
+              uint4v{low_codes(w), high_codes(w), low_codes(w8), high_codes(w8)};
+        }
+        if (job == 0) {
+          st.ks[lane] = low_half(params) * unit_of_logits;
+          st.kz[lane] = high_half(params);
+          const uint64_t there = __ballot(valid);
+          if (lane == 0) st.there = there;
+        }
+        if (job == 1) st.vp[lane] = params;
+      } else {
+        constexpr int M = 32 / W;
+        const int x = (job - kKeyJobs) * 64 + lane;
+        const int w = x % W, h = x / W % 2, part = x / (2 * W) % 2, unit = x / (4 * W);
+        const uint4v* src[2] = {&a[m], &b[m]};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t sel = 0x0c040c00u + 0x00010001u * (2 * part + k);
+          uint4v even, odd;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4v& s = *src[i / 2];
+            const uint32_t both = __builtin_amdgcn_perm(s[2 * (i % 2) + 1], s[2 * (i % 2)], sel);
+            even[i] = low_codes(both);
+            odd[i] = high_codes(both);
+          }
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const int c = 4 * part + 2 * k + o;  // channel of the word
+            st.v[unit / 2][unit % 2][c / M][32 * h + w + W * (c % M)] = o ? odd : even;
+          }
+        }
+      }
+    }
+  }
+};
+
+// One tile of 32 tokens for a wave's 32 rows.
+template <int D>
+struct RowSums {
+  float16v acc[D / 32];  // sum of w (c - 8)
+  float m, l, z;         // reference; this lane's part of sum p, sum p z
+};
+
+// The probabilities of a tile under reference m: packed weights, and their
+// sums.  Parameters are read as they are used, four tokens at a time.  EDGE:
+// some token is not seen by some row; what the cache holds for it may be
+// anything, so it is taken out, not multiplied by zero.
+template <bool BF16>
+struct Weights {
+  uint4v w[2];                   // [unit]
+  uint4v rest[BF16 ? 1 : 2];     // FP16: the remainders of their rounding
+  float sum, z, most;
+};
+
+template <int D, bool BF16, bool EDGE>
+__device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int tile,
+                                      const float16v& raw, float sum_q, float m, uint32_t there,
+                                      int t, int lo, int hi) {
+  const int h = (threadIdx.x & 63) >> 5;
+  o.sum = o.z = o.most = 0.f;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int at = 8 * a + 4 * h;
+    const float4v ks = *reinterpret_cast<const float4v*>(&st.ks[32 * tile + at]);
+    const float4v kz = *reinterpret_cast<const float4v*>(&st.kz[32 * tile + at]);
+    const uint4v vp = *reinterpret_cast<const uint4v*>(&st.vp[32 * tile + at]);
+    float w[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float p = exp2_hw(
+          __builtin_fmaf(ks[r], raw[4 * a + r], __builtin_fmaf(kz[r], sum_q, -m)));
+      w[r] = times_low_half(p, vp[r]);
+      float z = high_half(vp[r]);
+      if constexpr (EDGE) {
+        const int j = t + at + r;
+        const bool seen = (there >> (at + r) & 1) && j >= lo && j <= hi;
+        p = seen ? p : 0.f;
+        w[r] = seen ? w[r] : 0.f;
+        z = seen ? z : 0.f;
+      }
+      o.sum += p;
+      o.z = __builtin_fmaf(p, z, o.z);
+    }
+    o.most = fmaxf(fmaxf(fmaxf(fmaxf(o.most, w[0]), w[1]), w[2]), w[3]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t x = pack_halves(w[2 * k], w[2 * k + 1]);
+      o.w[a / 2][2 * (a % 2) + k] = x;
+      if constexpr (!BF16)
+        o.rest[a / 2][2 * (a % 2) + k] =
+            pack_halves(less_low_half(w[2 * k], x), less_high_half(w[2 * k + 1], x));
+    }
+  }
+}
+
+template <int D, bool BF16>
+__device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const uint4v* q,
+                                            float sum_q, RowSums<D>& s, uint32_t there, int t,
+                                            bool edge, int lo, int hi) {
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  float16v raw;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) raw[i] = 0.f;
+#pragma unroll
+  for (int f = 0; f < D / 16; ++f) raw = mfma32(st.k[tile][f][lane], q[f], raw);
+
+  Weights<BF16> o;
+  if (edge)
+    weigh<D, BF16, true>(o, st, tile, raw, sum_q, s.m, there, t, lo, hi);
+  else
+    weigh<D, BF16, false>(o, st, tile, raw, sum_q, s.m, there, t, lo, hi);
+  if (__any(o.most > kMostWeight || o.sum > kMostSum)) {
+    // Move the reference, as the other kernel does.
+    keep_branch();
+    float top = kNone;
+#pragma unroll 1
+    for (int a = 0; a < 4; ++a) {
+      const int at = 8 * a + 4 * h;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = t + at + r, i = 32 * tile + at + r;
+        const float got = a == 0 ? raw[r] : a == 1 ? raw[4 + r] : a == 2 ? raw[8 + r] : raw[12 + r];
+        const float x = st.ks[i] * got + st.kz[i] * sum_q;
+        const bool seen = (there >> (at + r) & 1) && j >= lo && j <= hi;
+        const float y = fmaxf(x + __builtin_amdgcn_logf(low_half(st.vp[i])) - kTopWeight,
+                              x - kSumHeadroom);
+        top = seen ? fmaxf(top, y) : top;
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float m = fmaxf(s.m, top);
+    const float f = exp2_hw(s.m - m);
+    s.m = m;
+    s.l *= f;
+    s.z *= f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) s.acc[c] *= f;
+    weigh<D, BF16, true>(o, st, tile, raw, sum_q, s.m, there, t, lo, hi);
+  }
+  s.l += o.sum;
+  s.z += o.z;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const uint4v v = st.v[tile][u][c][lane];
+      s.acc[c] = mfma32(v, o.w[u], s.acc[c]);
+      if constexpr (!BF16) s.acc[c] = mfma32(v, o.rest[u], s.acc[c]);
+    }
+}
+
+template <int D, bool BF16>
+__global__ __launch_bounds__(64 * kRowWaves<D>, (kRowWaves<D> / 4)) void kv_rows_kernel(
+    KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
+    float* __restrict__ partials) {
+  constexpr int kWaves = kRowWaves<D>, kThreads = 64 * kWaves, kRowTile = 32 * kWaves;
+  constexpr int F = D / 16, CB = D / 32, W = D / 8, M = 32 / W;
+  __shared__ Stage<D> stage[2];
+  __shared__ float s_top[kWaves];
+  __shared__ bool s_last;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5;
+  const int group = a.Hq / a.H;
+  // Row tiles with the most tokens first: the last rows of every request.
+  int id = blockIdx.x;
+  const int split = id % splits;
+  id /= splits;
+  const int head = id % a.H;
+  id /= a.H;
+  const int b = id % a.B, tile = tiles - 1 - id / a.B;
+  const int work = (b * a.H + head) * tiles + tile;
+  const int row0 = tile * kRowTile;
+  const Span sp = span_of(a, b, group, row0, kRowTile);
+  if (row0 >= sp.rows) return;
+  const Range range = range_of(sp, split, splits, chunk);
+  if (split >= range.parts) return;
+
+  // This wave's rows; rows past the last repeat it and are not stored.
+  const int wave_row0 = row0 + 32 * wave;
+  const bool idle = wave_row0 >= sp.rows;
+  const int want = wave_row0 + (lane & 31);
+  const int row = want < sp.rows ? want : sp.rows - 1;
+  const int qi = row / group;
+  const uint16_t* src = a.q.p + (int64_t)(sp.tok0 + qi) * a.q.token +
+                        (int64_t)(head * group + row - qi * group) * a.q.head;
+  const int pos = sp.len - sp.nq + qi;
+  const int lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+  const int pos_first = __shfl(pos, 0), pos_last = __shfl(pos, 31);
+  const int lo_first = __shfl(lo, 0), lo_last = __shfl(lo, 31);
+
+  Producer<D> pr;
+  const uint64_t page_bytes = (uint64_t)(a.page / kKvUnit) * KvUnit<D>::bytes;
+  pr.head = a.cache + page_bytes * head;
+  pr.stride = page_bytes * a.H;
+  pr.row = a.table + (int64_t)b * a.max_pages;
+  pr.shift = 31 - __builtin_clz((unsigned)a.page);
+  pr.max_pages = a.max_pages;
+  pr.pages = a.pages;
+  pr.wave = wave;
+  const int begin = range.begin;
+  const int steps = (range.end - begin + kStep - 1) / kStep;
+  if (steps > 0) {
+    pr.find(begin);
+    pr.load(begin);
+    pr.find(begin + kStep);
+  }
+
+  // Queries as operands: 16-bit floats times one power of two that brings the
+  // workgroup's largest finite row near FP16's upper end (as the other
+  // kernel's, per workgroup: the keys' scales are stored in logits).
+  uint4v q[F];
+  float sum_q = 0.f, unit;
+  {
+    uint4v raw[F];
+    uint32_t most = 0;
+    auto element = [&](int f, int c) {
+      const uint32_t w = raw[f][c >> 1];
+      const uint32_t bits = c & 1 ? w >> 16 : w & 0xffffu;
+      if constexpr (BF16) return __builtin_bit_cast(float, bits << 16);
+      else return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+    };
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      raw[f] = *reinterpret_cast<const uint4v*>(src + 16 * f + 8 * h);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        most = max(most, __builtin_bit_cast(uint32_t, element(f, c)) & 0x7fffffffu);
+    }
+    most = max(most, (uint32_t)__shfl_xor((int)most, 32));
+    float top = most < 0x7f800000u ? __builtin_bit_cast(float, most) : 0.f;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    if (lane == 0) s_top[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_top[w]);
+    int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
+    e = e < -100 ? -100 : e;
+    const float up = __builtin_bit_cast(float, (uint32_t)(127 + 13 - e) << 23);
+    unit = a.scale * kLog2e * __builtin_bit_cast(float, (uint32_t)(127 - 13 + e) << 23);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      _Float16 x[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        x[c] = (_Float16)(element(f, c) * up);
+        sum_q += (float)x[c];
+      }
+      // the order in which a word's codes are unpacked
+      const half8 v = {x[0], x[4], x[1], x[5], x[2], x[6], x[3], x[7]};
+      q[f] = __builtin_bit_cast(uint4v, v);
+    }
+    sum_q += __shfl_xor(sum_q, 32);
+    sum_q *= unit;
+  }
+
+  RowSums<D> s;
+  s.m = kNone;
+  s.l = s.z = 0.f;
+#pragma unroll
+  for (int c = 0; c < CB; ++c)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s.acc[c][i] = 0.f;
+
+  if (steps > 0) {
+    pr.unpack(stage[0], unit);
+    if (steps > 1) {
+      pr.load(begin + kStep);
+      pr.find(begin + 2 * kStep);
+    }
+    __syncthreads();
+    for (int n = 0; n < steps; ++n) {
+      const Stage<D>& st = stage[n & 1];
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        const int t = begin + n * kStep + k * kTile;
+        // tokens beyond the range belong to the next workgroup, or to none
+        if (idle || t >= range.end || t > pos_last || t + kTile <= lo_first) continue;
+        const uint32_t there = (uint32_t)(st.there >> (32 * k));
+        const bool edge = t < lo_last || t + kTile > pos_first + 1 || there != 0xffffffffu;
+        attend_rows<D, BF16>(st, k, q, sum_q, s, there, t, edge, lo, pos);
+      }
+      if (n + 1 < steps) {
+        pr.unpack(stage[(n + 1) & 1], unit);
+        if (n + 2 < steps) {
+          pr.load(begin + (n + 2) * kStep);
+          pr.find(begin + (n + 3) * kStep);
+        }
+      }
+      __syncthreads();
+    }
+  }
+
+  const Output out(a, sp, head, group);
+  const float total = s.l + __shfl_xor(s.l, 32);
+  const float fixed = s.z + __shfl_xor(s.z, 32);
+  // Eight neighbouring channels of word 8 k + 4 h + r of this lane's row.
+  auto channels = [&](int k, int r, float* x) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = s.acc[c / M][4 * (k + W / 8 * (c % M)) + r] + fixed;
+  };
+  if (range.parts == 1) {
+    if (want < sp.rows) {
+      const float inv = total == 0.f ? 0.f : 1.0f / total;
+#pragma unroll
+      for (int k = 0; k < W / 8; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x[8];
+          channels(k, r, x);
+          out.store<BF16, 8>(row, 8 * (8 * k + 4 * h + r), x, inv);
+        }
+      if (h == 0) out.store_lse(row, s.m, total);
+    }
+    return;
+  }
+  const int rows = sp.rows - row0 < kRowTile ? sp.rows - row0 : kRowTile;
+  constexpr int kVecsOfPart = kRowTile * kPartVecs<D>;
+  const float* tile_base = partials + (int64_t)work * splits * kVecsOfPart * 4;
+  if (want < sp.rows) {
+    const __amdgpu_buffer_rsrc_t mine =
+        coherent_rsrc(tile_base + (int64_t)split * kVecsOfPart * 4);
+    const int base = (want - row0) * kPartVecs<D>;
+#pragma unroll
+    for (int k = 0; k < W / 8; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float x[8];
+        channels(k, r, x);
+        const int at = base + 2 * (8 * k + 4 * h + r);
+        store_coherent(mine, at, float4_t{x[0], x[1], x[2], x[3]});
+        store_coherent(mine, at + 1, float4_t{x[4], x[5], x[6], x[7]});
+      }
+    if (h == 0) store_coherent(mine, base + D / 4, float4_t{s.m, total, 0.f, 0.f});
+  }
+  if (last_to_arrive(counters + work, range.parts, &s_last))
+    join_parts<D, BF16, kThreads>(tile_base, kVecsOfPart, range.parts, rows, row0, out,
+                                  counters + work);
+}
+
+template <int D>
+hipError_t launch(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
+                  unsigned* counters, float* partials, hipStream_t stream) {
+  const dim3 grid((unsigned)((int64_t)a.B * a.H * p.tiles * p.splits));
+  const dim3 block(64 * kRowWaves<D>);
+  if (dtype == W4A16_DTYPE_BF16)
+    hipLaunchKernelGGL((kv_rows_kernel<D, true>), grid, block, 0, stream, a, p.tiles, p.splits,
+                       p.chunk, counters, partials);
+  else
+    hipLaunchKernelGGL((kv_rows_kernel<D, false>), grid, block, 0, stream, a, p.tiles, p.splits,
+                       p.chunk, counters, partials);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_rows(const KvAttentionPlan& p, const KvAttentionArgs& a, int D, int dtype,
+                          unsigned* counters, float* partials, hipStream_t stream) {
+  switch (D) {
+    case 64: return launch<64>(p, a, dtype, counters, partials, stream);
+    case 128: return launch<128>(p, a, dtype, counters, partials, stream);
+    default: return launch<256>(p, a, dtype, counters, partials, stream);
+  }
+}
+
+}  // namespace w4a16
