@@ -37,8 +37,6 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kWaitLoads = 0x0f70;          // s_waitcnt: all vector loads, nothing else
-
 // Sum and maximum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_sum(float x) {
   x += __shfl_xor(x, 16);
@@ -58,25 +56,6 @@ struct TileData {
   uint4v v[2][VV];
   uint4v kp[2], vp[2];
   bool valid[2];                                    // the unit's page exists
-};
-
-// The page ids of 64 pages from `first`, one per lane.
-struct PageIds {
-  const int32_t* row;
-  int max_pages, first, mine;
-  __device__ __forceinline__ void load(int page) {
-    first = page;
-    const int p = page + (int)(threadIdx.x & 63);
-    mine = p < max_pages ? row[p] : -1;
-    // Wait here, where it is rare: left to the first use, the wait would
-    // stand after the branch and hold up the tiles in flight every time.
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
-  }
-  // `page` is the same in all lanes
-  __device__ __forceinline__ int at(int page) {
-    if (page - first >= 64) load(page);
-    return __builtin_amdgcn_readlane(mine, page - first);
-  }
 };
 
 // Where a head's units lie: page id `p` of it starts at
@@ -586,7 +565,7 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
   // Many rows: the waves of a workgroup take 32 each and share the tokens.
   p.rows = rows > 64;
   p.nb = p.rows ? 2 : D < 256 && rows > 16 ? 2 : 1;
-  p.waves = !p.rows ? kWaves : D == 256 ? 4 : 8;
+  p.waves = kWaves;
   const int tile_rows = 16 * p.nb * (p.rows ? p.waves : 1);
   p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
   p.splits = 1;
@@ -600,7 +579,7 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
     // in one, of which starting, joining the waves and joining the ranges
     // are worth about kStart, kJoin steps.
     constexpr int64_t kStart = 5, kJoin = 3;
-    const int64_t slots = (int64_t)cus * (!p.rows && D * p.nb <= 128 ? 2 : 1);
+    const int64_t slots = (int64_t)cus * (D * (p.rows ? 1 : p.nb) <= 128 ? 2 : 1);
     const int64_t sharing = p.rows ? 1 : kWaves;  // waves that divide the tokens
     const int64_t steps = keys / kTile;
     int64_t most = 8 * slots / work + 1;

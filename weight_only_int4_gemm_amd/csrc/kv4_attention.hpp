@@ -10,6 +10,7 @@
 namespace w4a16 {
 
 constexpr int kTile = 32;                   // tokens of one step: two units
+constexpr int kWaitLoads = 0x0f70;          // s_waitcnt: all vector loads, nothing else
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNone = -1e30f;             // reference of a column that has seen no key
@@ -104,6 +105,25 @@ __device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int gro
   s.end = last_pos + 1 > s.begin ? last_pos + 1 : s.begin;
   return s;
 }
+
+// The page ids of 64 pages from `first`, one per lane.
+struct PageIds {
+  const int32_t* row;
+  int max_pages, first, mine;
+  __device__ __forceinline__ void load(int page) {
+    first = page;
+    const int p = page + (int)(threadIdx.x & 63);
+    mine = p < max_pages ? row[p] : -1;
+    // Wait here, where it is rare: left to the first use, the wait would
+    // stand after the branch and hold up the tiles in flight every time.
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+  }
+  // `page` is the same in all lanes
+  __device__ __forceinline__ int at(int page) {
+    if (page - first >= 64) load(page);
+    return __builtin_amdgcn_readlane(mine, page - first);
+  }
+};
 
 // This workgroup's token range of a row tile: `split` of `splits`, each of
 // `chunk` tokens, longer where the request is longer than planned.

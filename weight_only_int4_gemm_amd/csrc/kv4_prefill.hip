@@ -1,8 +1,8 @@
 // kv4_attention for many query rows: chunks of prompts, long drafts.
 //
 // The mathematics of kv4_attention.hip, arranged for rows.  A workgroup of
-// WAVES waves takes 32 * WAVES query rows, 32 per wave, and walks their
-// tokens 64 at a time.  Each step's codes are unpacked once per workgroup,
+// four waves takes 128 query rows, 32 per wave, and walks their tokens 64 at
+// a time.  Each step's codes are unpacked once per workgroup,
 // into LDS, as the exact FP16 integers c - 8 and in the order in which the
 // 32x32x16 matrix instruction takes its first operand, so a wave spends its
 // vector instructions on the softmax alone and reads every operand with one
@@ -28,18 +28,17 @@ constexpr int kStep = 64;  // tokens of a step: two tiles, four units
 
 typedef float float16v __attribute__((ext_vector_type(16)));
 
-template <int D>
-constexpr int kRowWaves = D == 256 ? 4 : 8;
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kRowTile = 32 * kWaves;
 
 template <int D>
 struct Stage {
   static constexpr int F = D / 16, CB = D / 32;
   uint4v k[2][F][64];      // [tile][16 channels][lane]
   uint4v v[2][2][CB][64];  // [tile][unit][channel block][lane]
-  float ks[kStep];         // key scale in the logits' unit
-  float kz[kStep];         // key offset
+  float ks[kStep];         // key scale, product units to base-2 logits
+  float kz[kStep];         // key offset - 8 scales
   uint32_t vp[kStep];      // value (scale, offset)
-  uint64_t there;          // tokens whose page exists
+  uint16_t there[4];       // per unit: all ones if its page exists
 };
 
 __device__ __forceinline__ float16v mfma32(const uint4v& a, const uint4v& b, const float16v& c) {
@@ -48,102 +47,110 @@ __device__ __forceinline__ float16v mfma32(const uint4v& a, const uint4v& b, con
 }
 
 // The codes in bits 0..3 (low) or 4..7 (high) of both halves, less 8: the
-// bits of 1024 + c or 64 + c, less 1032 or 72.
-__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
-  const half2v h = __builtin_bit_cast(half2v, (w & 0x000f000fu) | 0x64006400u);
+// bits of 1024 + c or 64 + c, less 1032 or 72.  The masks are values in
+// vector registers, for one instruction that ANDs and ORs.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t mask) {
+  const half2v h = __builtin_bit_cast(half2v, (w & mask) | 0x64006400u);
   return __builtin_bit_cast(uint32_t, h - half2v{(_Float16)1032.f, (_Float16)1032.f});
 }
-__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
-  const half2v h = __builtin_bit_cast(half2v, (w & 0x00f000f0u) | 0x54005400u);
+__device__ __forceinline__ uint32_t high_codes(uint32_t w, uint32_t mask) {
+  const half2v h = __builtin_bit_cast(half2v, (w & mask) | 0x54005400u);
   return __builtin_bit_cast(uint32_t, h - half2v{(_Float16)72.f, (_Float16)72.f});
 }
 
-// What a wave unpacks of a step.  The step is divided into wave jobs: key job
-// q takes words 4 q .. + 3 of all 64 tokens (one per lane); a value job takes,
-// per lane, half of the channels of one word for the eight tokens of one unit
-// that one lane half multiplies.
+// What a wave unpacks of a step, as jobs of 64 lanes.  A key job: 64 / J
+// tokens, J = D / 32 lanes with four words each.  A value job: the eight
+// tokens of a unit that one lane half multiplies, half of the channels of one
+// word per lane.  With D >= 128 a job lies in one unit, so its page is the
+// same for all lanes; with D = 64 it covers two.
 template <int D>
 struct Producer {
-  static constexpr int W = D / 8;
-  static constexpr int kKeyJobs = D / 32, kValueJobs = W * 16 / 64;
-  static constexpr int kJobs = kKeyJobs + kValueJobs;
-  static constexpr int kMine = (kJobs + kRowWaves<D> - 1) / kRowWaves<D>;
+  static constexpr int W = D / 8, J = D / 32;
+  static constexpr int kJobs = J;                // of each kind, in a step
+  static constexpr int kUnits = 4;               // of a step
+  static constexpr int kMine = (2 * kJobs + kWaves - 1) / kWaves;
+  static constexpr int kUnitsOfJob = D == 64 ? 2 : 1;
 
   const uint8_t* head;   // the head's first page
   uint64_t stride;       // bytes of a page over all heads
-  const int32_t* row;    // the request's page ids
-  int shift, max_pages, pages, wave;
-  int id[kMine];         // page of the next step's codes
+  PageIds ids;           // the request's pages
+  int shift, pages, wave;
   uint4v a[kMine], b[kMine];
-  uint32_t params;
+  uint32_t kp, vp;
   bool valid;
 
-  // the token of the step that lane and job look at
-  __device__ __forceinline__ int token_of(int job) const {
-    const int lane = threadIdx.x & 63;
-    return job < kKeyJobs ? lane : ((job - kKeyJobs) * 64 + lane) / (4 * W) * kKvUnit;
+  // Job m of this wave: its kind, and its first unit.  D = 64: waves 0, 1
+  // keys, 2, 3 values; D = 128: a unit's keys and values; D = 256: a unit's
+  // two key jobs and two value jobs.
+  __device__ __forceinline__ bool keys(int m) const {
+    return D == 64 ? wave < 2 : m < kMine / 2;
   }
-  __device__ __forceinline__ void find(int t) {  // page ids of step t
+  __device__ __forceinline__ int unit_of(int m) const { return D == 64 ? 2 * (wave & 1) : wave; }
+  // which of the unit's jobs of its kind
+  __device__ __forceinline__ int part_of(int m) const { return D == 256 ? m & 1 : 0; }
+
+  __device__ __forceinline__ const uint8_t* unit_at(int t, bool* there) {
+    const int id = ids.at(t >> shift);
+    *there = (unsigned)id < (unsigned)pages;
+    return head + (uint64_t)(uint32_t)(*there ? id : 0) * stride +
+           (uint32_t)((t & ((1 << shift) - 1)) / kKvUnit * KvUnit<D>::bytes);
+  }
+
+  __device__ __forceinline__ void load(int t) {  // codes of the step at t
+    const uint32_t lane = threadIdx.x & 63;
+    bool there0, there1 = true;
+    const uint8_t* base0 = unit_at(t + kKvUnit * unit_of(0), &there0);
+    const uint8_t* base1 = base0;
+    if constexpr (kUnitsOfJob == 2) base1 = unit_at(t + kKvUnit * (unit_of(0) + 1), &there1);
+    const uint8_t* unit = base0;
+    if constexpr (kUnitsOfJob == 2) unit = lane < 32 ? base0 : base1;
+    valid = kUnitsOfJob == 2 && lane >= 32 ? there1 : there0;
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
-      const int job = wave + m * kRowWaves<D>;
-      const int page = (t + token_of(job)) >> shift;
-      id[m] = job < kJobs && page < max_pages ? row[page] : -1;
-    }
-  }
-  __device__ __forceinline__ void load(int t) {  // codes of step t, whose ids are found
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int m = 0; m < kMine; ++m) {
-      const int job = wave + m * kRowWaves<D>;
-      if (job >= kJobs) break;
-      const bool there = (unsigned)id[m] < (unsigned)pages;
-      const int pos = t + token_of(job);
-      const uint8_t* unit = head + (uint64_t)(uint32_t)(there ? id[m] : 0) * stride +
-                            (uint32_t)((pos & ((1 << shift) - 1)) / kKvUnit * KvUnit<D>::bytes);
-      if (job < kKeyJobs) {
-        const uint32_t r = lane % kKvUnit;
-        a[m] = *reinterpret_cast<const uint4v*>(unit + r * (D / 2) + 16 * job);
-        // the first two key jobs bring the parameters, too
-        if (job < 2)
-          params = *reinterpret_cast<const uint32_t*>(
-              unit + (job == 0 ? KvUnit<D>::key_params : KvUnit<D>::value_params) + 4 * r);
-        valid = there;
+      if (keys(m)) {
+        const uint32_t x = lane + 64 * part_of(m), r = x % 16;
+        const uint32_t q = x / 16 % J;
+        a[m] = *reinterpret_cast<const uint4v*>(unit + r * (D / 2) + 16 * q);
+        if (m == 0) {
+          kp = *reinterpret_cast<const uint32_t*>(unit + KvUnit<D>::key_params + 4 * r);
+          vp = *reinterpret_cast<const uint32_t*>(unit + KvUnit<D>::value_params + 4 * r);
+        }
       } else {
-        const int x = (job - kKeyJobs) * 64 + lane;
-        const uint32_t w = x % W, h = x / W % 2;
-        const uint8_t* v = unit + KvUnit<D>::values + 16 * (h * W + w);
-        a[m] = *reinterpret_cast<const uint4v*>(v);
-        b[m] = *reinterpret_cast<const uint4v*>(v + 32 * W);
+        const uint32_t w = lane % W, h = lane / W % 2;
+        const uint32_t at = KvUnit<D>::values + 16 * (h * W + w);
+        a[m] = *reinterpret_cast<const uint4v*>(unit + at);
+        b[m] = *reinterpret_cast<const uint4v*>(unit + at + 32 * W);
       }
     }
   }
+
   __device__ __forceinline__ void unpack(Stage<D>& st, float unit_of_logits) {
     const int lane = threadIdx.x & 63;
+    constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+    const uint32_t low = apart(kLow), high = apart(kHigh);
+    const int unit = unit_of(0) + (kUnitsOfJob == 2 ? lane / 32 : 0);
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
-      const int job = wave + m * kRowWaves<D>;
-      if (job >= kJobs) break;
-      if (job < kKeyJobs) {
-        const int tile = lane / 32, r = lane % 32;
+      if (keys(m)) {
+        const int x = lane + 64 * part_of(m), r = 16 * (unit % 2) + x % 16, q = x / 16 % J;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = a[m][i], w8 = w >> 8;
-          const int word = 4 * job + i;
-          st.k[tile][word / 2][32 * (word % 2) + r] =
-              uint4v{low_codes(w), high_codes(w), low_codes(w8), high_codes(w8)};
+          // word 4 q + i; subnormals c 2^-24 and 16 c 2^-24, as in the other kernel
+          st.k[unit / 2][2 * q + i / 2][32 * (i % 2) + r] =
+              uint4v{w & kLow, w & kHigh, w8 & kLow, w8 & kHigh};
         }
-        if (job == 0) {
-          st.ks[lane] = low_half(params) * unit_of_logits;
-          st.kz[lane] = high_half(params);
-          const uint64_t there = __ballot(valid);
-          if (lane == 0) st.there = there;
+        if (m == 0 && q == 0) {
+          const int token = 16 * unit + lane % 16;
+          st.ks[token] = low_half(kp) * unit_of_logits * 0x1p24f;
+          st.kz[token] = high_half(kp) - 8.f * low_half(kp);
+          st.vp[token] = vp;
+          if (lane % 16 == 0) st.there[unit] = valid ? 0xffffu : 0u;
         }
-        if (job == 1) st.vp[lane] = params;
       } else {
         constexpr int M = 32 / W;
-        const int x = (job - kKeyJobs) * 64 + lane;
-        const int w = x % W, h = x / W % 2, part = x / (2 * W) % 2, unit = x / (4 * W);
+        const int w = lane % W, h = lane / W % 2;
+        const int part = D == 256 ? part_of(m) : lane / (2 * W) % 2;
         const uint4v* src[2] = {&a[m], &b[m]};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -153,8 +160,8 @@ struct Producer {
           for (int i = 0; i < 4; ++i) {
             const uint4v& s = *src[i / 2];
             const uint32_t both = __builtin_amdgcn_perm(s[2 * (i % 2) + 1], s[2 * (i % 2)], sel);
-            even[i] = low_codes(both);
-            odd[i] = high_codes(both);
+            even[i] = low_codes(both, low);
+            odd[i] = high_codes(both, high);
           }
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
@@ -174,6 +181,17 @@ struct RowSums {
   float m, l, z;         // reference; this lane's part of sum p, sum p z
 };
 
+template <int D>
+__device__ __forceinline__ float16v scores(const Stage<D>& st, int tile, const uint4v* q) {
+  const int lane = threadIdx.x & 63;
+  float16v raw;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) raw[i] = 0.f;
+#pragma unroll
+  for (int f = 0; f < D / 16; ++f) raw = mfma32(st.k[tile][f][lane], q[f], raw);
+  return raw;
+}
+
 // The probabilities of a tile under reference m: packed weights, and their
 // sums.  Parameters are read as they are used, four tokens at a time.  EDGE:
 // some token is not seen by some row; what the cache holds for it may be
@@ -182,7 +200,8 @@ template <bool BF16>
 struct Weights {
   uint4v w[2];                   // [unit]
   uint4v rest[BF16 ? 1 : 2];     // FP16: the remainders of their rounding
-  float sum, z, most;
+  float sum, z;
+  bool over;                     // out of the reference's range
 };
 
 template <int D, bool BF16, bool EDGE>
@@ -190,7 +209,9 @@ __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int 
                                       const float16v& raw, float sum_q, float m, uint32_t there,
                                       int t, int lo, int hi) {
   const int h = (threadIdx.x & 63) >> 5;
-  o.sum = o.z = o.most = 0.f;
+  const _Float16 kMostHalf = (_Float16)kMostWeight;  // what is larger rounds to it, or to infinity
+  half2v most;
+  o.sum = o.z = 0.f;
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
     const int at = 8 * a + 4 * h;
@@ -214,16 +235,18 @@ __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int 
       o.sum += p;
       o.z = __builtin_fmaf(p, z, o.z);
     }
-    o.most = fmaxf(fmaxf(fmaxf(fmaxf(o.most, w[0]), w[1]), w[2]), w[3]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const uint32_t x = pack_halves(w[2 * k], w[2 * k + 1]);
       o.w[a / 2][2 * (a % 2) + k] = x;
+      most = a == 0 && k == 0 ? __builtin_bit_cast(half2v, x)
+                              : __builtin_elementwise_max(most, __builtin_bit_cast(half2v, x));
       if constexpr (!BF16)
         o.rest[a / 2][2 * (a % 2) + k] =
             pack_halves(less_low_half(w[2 * k], x), less_high_half(w[2 * k + 1], x));
     }
   }
+  o.over = most[0] > kMostHalf || most[1] > kMostHalf || o.sum > kMostSum;
 }
 
 template <int D, bool BF16>
@@ -231,18 +254,13 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
                                             float sum_q, RowSums<D>& s, uint32_t there, int t,
                                             bool edge, int lo, int hi) {
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  float16v raw;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) raw[i] = 0.f;
-#pragma unroll
-  for (int f = 0; f < D / 16; ++f) raw = mfma32(st.k[tile][f][lane], q[f], raw);
-
+  const float16v raw = scores<D>(st, tile, q);
   Weights<BF16> o;
   if (edge)
     weigh<D, BF16, true>(o, st, tile, raw, sum_q, s.m, there, t, lo, hi);
   else
     weigh<D, BF16, false>(o, st, tile, raw, sum_q, s.m, there, t, lo, hi);
-  if (__any(o.most > kMostWeight || o.sum > kMostSum)) {
+  if (__any(o.over)) {
     // Move the reference, as the other kernel does.
     keep_branch();
     float top = kNone;
@@ -282,11 +300,12 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
     }
 }
 
+// Two workgroups per compute unit, which drift apart, so that one's softmax
+// fills the vector units while the other's products fill the matrix units.
 template <int D, bool BF16>
-__global__ __launch_bounds__(64 * kRowWaves<D>, (kRowWaves<D> / 4)) void kv_rows_kernel(
+__global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
     KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
     float* __restrict__ partials) {
-  constexpr int kWaves = kRowWaves<D>, kThreads = 64 * kWaves, kRowTile = 32 * kWaves;
   constexpr int F = D / 16, CB = D / 32, W = D / 8, M = 32 / W;
   __shared__ Stage<D> stage[2];
   __shared__ float s_top[kWaves];
@@ -294,13 +313,17 @@ __global__ __launch_bounds__(64 * kRowWaves<D>, (kRowWaves<D> / 4)) void kv_rows
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5;
   const int group = a.Hq / a.H;
-  // Row tiles with the most tokens first: the last rows of every request.
+  // Heads next to each other (they go to unlike XCDs), then the row tiles of
+  // a request, the last, which see the most tokens, first.  Neighbours in this
+  // order are about equally long: the shader engines take workgroups in turn,
+  // so requests of unlike lengths side by side would load them unevenly
+  // (two requests, one three times as long: 1209 against 8xx us).
   int id = blockIdx.x;
   const int split = id % splits;
   id /= splits;
   const int head = id % a.H;
   id /= a.H;
-  const int b = id % a.B, tile = tiles - 1 - id / a.B;
+  const int tile = tiles - 1 - id % tiles, b = id / tiles;
   const int work = (b * a.H + head) * tiles + tile;
   const int row0 = tile * kRowTile;
   const Span sp = span_of(a, b, group, row0, kRowTile);
@@ -325,17 +348,15 @@ __global__ __launch_bounds__(64 * kRowWaves<D>, (kRowWaves<D> / 4)) void kv_rows
   const uint64_t page_bytes = (uint64_t)(a.page / kKvUnit) * KvUnit<D>::bytes;
   pr.head = a.cache + page_bytes * head;
   pr.stride = page_bytes * a.H;
-  pr.row = a.table + (int64_t)b * a.max_pages;
   pr.shift = 31 - __builtin_clz((unsigned)a.page);
-  pr.max_pages = a.max_pages;
+  pr.ids = PageIds{a.table + (int64_t)b * a.max_pages, a.max_pages, 0, -1};
   pr.pages = a.pages;
   pr.wave = wave;
   const int begin = range.begin;
   const int steps = (range.end - begin + kStep - 1) / kStep;
   if (steps > 0) {
-    pr.find(begin);
+    pr.ids.load(begin >> pr.shift);
     pr.load(begin);
-    pr.find(begin + kStep);
   }
 
   // Queries as operands: 16-bit floats times one power of two that brings the
@@ -376,8 +397,9 @@ __global__ __launch_bounds__(64 * kRowWaves<D>, (kRowWaves<D> / 4)) void kv_rows
       _Float16 x[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        x[c] = (_Float16)(element(f, c) * up);
-        sum_q += (float)x[c];
+        // odd channels meet codes of 16 times the size
+        x[c] = (_Float16)(element(f, c) * (c & 1 ? 0.0625f * up : up));
+        sum_q += (float)x[c] * (c & 1 ? 16.f : 1.f);
       }
       // the order in which a word's codes are unpacked
       const half8 v = {x[0], x[4], x[1], x[5], x[2], x[6], x[3], x[7]};
@@ -397,28 +419,22 @@ __global__ __launch_bounds__(64 * kRowWaves<D>, (kRowWaves<D> / 4)) void kv_rows
 
   if (steps > 0) {
     pr.unpack(stage[0], unit);
-    if (steps > 1) {
-      pr.load(begin + kStep);
-      pr.find(begin + 2 * kStep);
-    }
+    if (steps > 1) pr.load(begin + kStep);
     __syncthreads();
     for (int n = 0; n < steps; ++n) {
       const Stage<D>& st = stage[n & 1];
 #pragma unroll 1
       for (int k = 0; k < 2; ++k) {
         const int t = begin + n * kStep + k * kTile;
-        // tokens beyond the range belong to the next workgroup, or to none
+        // tiles beyond the range belong to the next workgroup, or to none
         if (idle || t >= range.end || t > pos_last || t + kTile <= lo_first) continue;
-        const uint32_t there = (uint32_t)(st.there >> (32 * k));
+        const uint32_t there = st.there[2 * k] | (uint32_t)st.there[2 * k + 1] << 16;
         const bool edge = t < lo_last || t + kTile > pos_first + 1 || there != 0xffffffffu;
         attend_rows<D, BF16>(st, k, q, sum_q, s, there, t, edge, lo, pos);
       }
       if (n + 1 < steps) {
         pr.unpack(stage[(n + 1) & 1], unit);
-        if (n + 2 < steps) {
-          pr.load(begin + (n + 2) * kStep);
-          pr.find(begin + (n + 3) * kStep);
-        }
+        if (n + 2 < steps) pr.load(begin + (n + 2) * kStep);
       }
       __syncthreads();
     }
@@ -475,7 +491,7 @@ template <int D>
 hipError_t launch(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
                   unsigned* counters, float* partials, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)a.B * a.H * p.tiles * p.splits));
-  const dim3 block(64 * kRowWaves<D>);
+  const dim3 block(kThreads);
   if (dtype == W4A16_DTYPE_BF16)
     hipLaunchKernelGGL((kv_rows_kernel<D, true>), grid, block, 0, stream, a, p.tiles, p.splits,
                        p.chunk, counters, partials);
