@@ -558,6 +558,9 @@ hipError_t launch_kv_tokens(const KvAttentionPlan& p, const KvAttentionArgs& a, 
   }
 }
 
+// What partial results may take of a workspace.
+constexpr int64_t kMostPartBytes = ((int64_t)192 << 20) - (int64_t)kCounterHeaderBytes;
+
 KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, int max_len,
                                        int window, int cus) {
   KvAttentionPlan p{};
@@ -582,8 +585,10 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
     const int64_t slots = (int64_t)cus * (D * (p.rows ? 1 : p.nb) <= 128 ? 2 : 1);
     const int64_t sharing = p.rows ? 1 : kWaves;  // waves that divide the tokens
     const int64_t steps = keys / kTile;
+    const int64_t part = (int64_t)tile_rows * (D + 4) * (int64_t)sizeof(float);
     int64_t most = 8 * slots / work + 1;
     if (most > (steps + sharing - 1) / sharing) most = (steps + sharing - 1) / sharing;
+    if (most > kMostPartBytes / (work * part)) most = kMostPartBytes / (work * part);
     int64_t best = 0, n = 1;
     for (int64_t i = 1; i <= most; ++i) {
       const int64_t rounds = (work * i + slots - 1) / slots;
