@@ -2,13 +2,26 @@
 //
 // The mathematics of kv4_attention.hip, arranged for rows.  A workgroup of
 // four waves takes 128 query rows, 32 per wave, and walks their tokens 64 at
-// a time.  Each step's codes are unpacked once per workgroup,
-// into LDS, as the exact FP16 integers c - 8 and in the order in which the
-// 32x32x16 matrix instruction takes its first operand, so a wave spends its
-// vector instructions on the softmax alone and reads every operand with one
-// conflict-free 16-byte LDS read.  The codes of the step after next are
-// loaded, and those of the next one unpacked, around the products of the
-// current one: one barrier per step, two stages of LDS.
+// a time.  Each step's codes are unpacked once per workgroup, into LDS, as
+// FP16 and in the order in which the 32x32x16 matrix instruction takes its
+// first operand, so a wave spends its vector instructions on the softmax and
+// reads every operand with one conflict-free 16-byte LDS read.  The codes of
+// the step after next are loaded, and those of the next one unpacked, around
+// the products of the current one: one barrier per step, two stages of LDS,
+// two workgroups per compute unit.
+//
+// What bounds it: the issue of vector and matrix instructions.  Measured with
+// loops of both, matrix instructions of one wave and vector instructions of
+// another hardly overlap on a SIMD (16 products and 120 vector instructions
+// take 0.34 us per wave together, 0.22 and 0.17 alone), so a tile of 32 x 32
+// scores costs their sum, 512 + about 880 cycles with D = 128, and the kernel
+// runs at 0.92 of that: 2 x 2048 queries over up to 8192 keys, 64 heads of
+// 128, BF16: 0.83 ms, 690 TFLOP/s (the library's 16384^3 product: 1364).  For
+// the same reason these did not help: two groups of waves that change places
+// between softmax and products at barriers (0.91), eight waves per workgroup
+// (0.85), the next tile's products between the softmax's instructions (0.87
+// of the time before the masks left the usual path, spills), steps of 32
+// tokens (0.93), wave priorities around the products (0.85).
 //
 // Operands.  Scores: keys first (rows = 32 tokens), queries second (columns =
 // 32 query rows); lane l has column l % 32 and, for i in 0..15, token
@@ -209,6 +222,11 @@ __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int 
                                       const float16v& raw, float sum_q, float m, uint32_t there,
                                       int t, int lo, int hi) {
   const int h = (threadIdx.x & 63) >> 5;
+  // known here only: the usual path must not compute any of the masks
+  if constexpr (EDGE) {
+    t = (int)apart(t);
+    there = apart(there);
+  }
   const _Float16 kMostHalf = (_Float16)kMostWeight;  // what is larger rounds to it, or to infinity
   half2v most;
   o.sum = o.z = 0.f;
@@ -262,17 +280,18 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
     weigh<D, BF16, false>(o, st, tile, raw, sum_q, s.m, there, t, lo, hi);
   if (__any(o.over)) {
     // Move the reference, as the other kernel does.
-    keep_branch();
     float top = kNone;
+    const int t1 = (int)apart(t);
+    const uint32_t there1 = apart(there);
 #pragma unroll 1
     for (int a = 0; a < 4; ++a) {
       const int at = 8 * a + 4 * h;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int j = t + at + r, i = 32 * tile + at + r;
+        const int j = t1 + at + r, i = 32 * tile + at + r;
         const float got = a == 0 ? raw[r] : a == 1 ? raw[4 + r] : a == 2 ? raw[8 + r] : raw[12 + r];
         const float x = st.ks[i] * got + st.kz[i] * sum_q;
-        const bool seen = (there >> (at + r) & 1) && j >= lo && j <= hi;
+        const bool seen = (there1 >> (at + r) & 1) && j >= lo && j <= hi;
         const float y = fmaxf(x + __builtin_amdgcn_logf(low_half(st.vp[i])) - kTopWeight,
                               x - kSumHeadroom);
         top = seen ? fmaxf(top, y) : top;
@@ -300,8 +319,6 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
     }
 }
 
-// Two workgroups per compute unit, which drift apart, so that one's softmax
-// fills the vector units while the other's products fill the matrix units.
 template <int D, bool BF16>
 __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
     KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
@@ -317,7 +334,7 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
   // a request, the last, which see the most tokens, first.  Neighbours in this
   // order are about equally long: the shader engines take workgroups in turn,
   // so requests of unlike lengths side by side would load them unevenly
-  // (two requests, one three times as long: 1209 against 8xx us).
+  // (two requests, one three times as long: 1.21 against 0.87 ms).
   int id = blockIdx.x;
   const int split = id % splits;
   id /= splits;
