@@ -23,7 +23,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;     // tokens of a workgroup
+constexpr int kMaxTokensLog = 2, kMaxTokens = 1 << kMaxTokensLog;  // of a workgroup
 constexpr float kFifteenth = 1.0f / 15.0f;
 constexpr float kMaxHalf = 65504.0f;
 
@@ -110,16 +110,17 @@ __device__ __forceinline__ void rotate8(const RopeArgs& r, const float2* cs, int
   const bool low = j < half8;
   const int lane = threadIdx.x & 63;
   const int partner = j >= rot8 ? lane : low ? lane + half8 : lane - half8;
+  // x1 cos - x2 sin and x2 cos + x1 sin: the first's partner changes sign
+  const uint32_t sign = low ? 0x80008000u : 0u;
   uint4v other;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) other[i] = (uint32_t)__shfl((int)w[i], partner);
+  for (int i = 0; i < 4; ++i) other[i] = (uint32_t)__shfl((int)w[i], partner) ^ sign;
   if (j < rot8) {
     float y[8];
     unpack8<BF16>(other, y);
     const float2* a = cs + 8 * (low ? j : j - half8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = low ? x[i] * a[i].x - y[i] * a[i].y : x[i] * a[i].x + y[i] * a[i].y;
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * a[i].x + y[i] * a[i].y;
   }
 }
 
@@ -127,98 +128,135 @@ struct Quantised {
   uint32_t codes, params;
 };
 
+template <int CTRL>
+__device__ __forceinline__ float other_lane(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+
+// Reduction over a row's LANES lanes, all of which get the result.  Once
+// lanes hold what their neighbours of a group of four hold, a mirrored lane
+// is as good as an exchanged one.
+template <int LANES, typename Op>
+__device__ __forceinline__ float over_row(float x, Op op) {
+  x = op(x, other_lane<0xb1>(x));   // quad_perm 1 0 3 2
+  x = op(x, other_lane<0x4e>(x));   // quad_perm 2 3 0 1
+  x = op(x, other_lane<0x141>(x));  // row_half_mirror: 8 lanes
+  if constexpr (LANES >= 16) x = op(x, other_lane<0x140>(x));  // row_mirror: 16
+  if constexpr (LANES >= 32) x = op(x, __shfl_xor(x, 16));
+  return x;
+}
+
 // The stored form of a row, of which this lane holds eight channels.
 template <int LANES>
 __device__ __forceinline__ Quantised quantise8(const float* x) {
 #pragma clang fp contract(off)
+  // (these pass a NaN on, so that the row's ends tell of every channel)
+  auto smaller = [](float a, float b) { return __builtin_elementwise_minimum(a, b); };
+  auto larger = [](float a, float b) { return __builtin_elementwise_maximum(a, b); };
   float lo = x[0], hi = x[0];
-  bool bad = !finite(x[0]);
 #pragma unroll
   for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    bad |= !finite(x[i]);
+    lo = smaller(lo, x[i]);
+    hi = larger(hi, x[i]);
   }
-#pragma unroll
-  for (int d = 1; d < LANES; d *= 2) {
-    lo = fminf(lo, __shfl_xor(lo, d));
-    hi = fmaxf(hi, __shfl_xor(hi, d));
-  }
-  const uint64_t row = (LANES == 64 ? ~0ull : (1ull << (LANES & 63)) - 1)
-                       << ((threadIdx.x & 63) / LANES * LANES);
-  if (__ballot(bad) & row) return {0x88888888u, 0x7e007e00u};  // code 8, NaN
+  lo = over_row<LANES>(lo, smaller);
+  hi = over_row<LANES>(hi, larger);
+  if (!finite(lo) || !finite(hi)) return {0x88888888u, 0x7e007e00u};  // code 8, NaN
   const _Float16 sh = (_Float16)fminf((hi - lo) * kFifteenth, kMaxHalf);
   const float s = (float)sh;
   const _Float16 zh = (_Float16)fminf(fmaxf(lo + 8.0f * s, -kMaxHalf), kMaxHalf);
   const float z = (float)zh;
   const float inv = s > 0.f ? 1.0f / s : 0.f;
-  uint32_t codes = 0;
+  // Adding 1.5 2^23 rounds to an integer (half to even: the added number is
+  // even, and so is 8) and leaves it in the low bits; what that number's own
+  // bits add to the codes is one constant.
+  constexpr float kRound = 12582912.0f + 8.0f;
+  constexpr uint32_t kRoundBits = 0x4b400000u;
+  uint32_t codes = 0u - kRoundBits * 0x11111111u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf(rintf((x[i] - z) * inv) + 8.0f, 0.f), 15.f);
-    codes |= (uint32_t)q << (4 * i);
+    const float q = __builtin_amdgcn_fmed3f((x[i] - z) * inv + kRound, kRound - 8.0f,
+                                            kRound + 7.0f);
+    codes += __builtin_bit_cast(uint32_t, q) << (4 * i);
   }
   return {codes, (uint32_t)__builtin_bit_cast(uint16_t, sh) |
                      (uint32_t)__builtin_bit_cast(uint16_t, zh) << 16};
 }
 
-// Grid: x = groups of `tokens` tokens, y = shares of the Hq + 2 H rows of a
-// token.
+// Grid: x = groups of 1 << tokens_log tokens, y = shares of the Hq + 2 H rows
+// of a token.
 template <int D, bool BF16>
-__global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a, int tokens) {
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a, int tokens_log,
+                                                             int page_log) {
   constexpr int LANES = D / 8, ROWS = kThreads / LANES;
   __shared__ float2 cs[kMaxTokens][D / 2];
-  const int t0 = blockIdx.x * tokens;
-  const int nt = a.T - t0 < tokens ? a.T - t0 : tokens;
+  const int t0 = blockIdx.x << tokens_log;
+  const int nt = a.T - t0 < 1 << tokens_log ? a.T - t0 : 1 << tokens_log;
   const int half = a.rope.half;
+  const int j = threadIdx.x % LANES;
+  // Rows in (head, token) order, so that neighbouring tokens of a head, whose
+  // words lie side by side in the cache, are stored together.  Whole waves
+  // leave the loop together and read a clamped row where there is none: the
+  // lane exchanges need every lane.
+  const int rows = (a.Hq + 2 * a.H) << tokens_log;
+  struct Row {
+    int head, tt, slot;
+    uint4v w;
+  };
+  auto load = [&](int base) {
+    Row r;
+    int row = base + (int)threadIdx.x / LANES;
+    row = row < rows ? row : rows - 1;
+    r.head = row >> tokens_log;
+    r.tt = row & ((1 << tokens_log) - 1);
+    const int t = t0 + (r.tt < nt ? r.tt : nt - 1);
+    const bool is_q = r.head < a.Hq, is_k = r.head < a.Hq + a.H;
+    const Rows& src = is_q ? a.q : is_k ? a.k : a.v;
+    const int h = r.head - (is_q ? 0 : is_k ? a.Hq : a.Hq + a.H);
+    r.w = *reinterpret_cast<const uint4v*>(src.p + t * src.token + h * src.head + 8 * j);
+    r.slot = is_q ? -1 : a.slots[t];
+    return r;
+  };
+  int base = blockIdx.y * ROWS;
+  if (base >= rows) return;
+  Row next = load(base);  // under way while the angles are computed
   if (half) {
     for (int i = threadIdx.x; i < nt * half; i += kThreads)
       cs[i / half][i % half] = rope_angle(a.rope, i % half, t0 + i / half);
     __syncthreads();
   }
-  const int heads = a.Hq + 2 * a.H;
-  const int j = threadIdx.x % LANES;
-  // Rows in (head, token) order, so that neighbouring tokens of a head, whose
-  // words lie side by side in the cache, are stored together.  Whole waves
-  // leave the loop together or hold a clamped row: the lane exchanges need
-  // every lane.
-  const int rows = heads * nt;
-  for (int base = blockIdx.y * ROWS; base < rows; base += gridDim.y * ROWS) {
-    const int mine = base + threadIdx.x / LANES;
-    const bool live = mine < rows;
-    const int row = live ? mine : rows - 1;
-    const int head = row / nt, tt = row - head * nt, t = t0 + tt;
-    const bool is_q = head < a.Hq, is_k = !is_q && head < a.Hq + a.H;
-    const int h = is_q ? head : is_k ? head - a.Hq : head - a.Hq - a.H;
-    const Rows& src = is_q ? a.q : is_k ? a.k : a.v;
-    const uint4v w = *reinterpret_cast<const uint4v*>(src.p + t * src.token + h * src.head + 8 * j);
+  for (; base < rows; base += gridDim.y * ROWS) {
+    const Row r = next;
+    next = load(base + gridDim.y * ROWS);
+    const bool live = base + (int)threadIdx.x / LANES < rows && r.tt < nt;
+    const bool is_q = r.head < a.Hq, is_k = !is_q && r.head < a.Hq + a.H;
     float x[8];
-    unpack8<BF16>(w, x);
-    if (half) {
+    unpack8<BF16>(r.w, x);
+    if (half && __any(is_q || is_k)) {
       float turned[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) turned[i] = x[i];
-      rotate8<BF16>(a.rope, cs[tt], j, w, turned);
+      rotate8<BF16>(a.rope, cs[r.tt < nt ? r.tt : nt - 1], j, r.w, turned);
       if (is_q || is_k) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = turned[i];
       }
     }
+    if (live && is_q)
+      *reinterpret_cast<uint4v*>(a.qo + (t0 + r.tt) * a.qo_token + r.head * a.qo_head + 8 * j) =
+          pack8<BF16>(x);
+    if (!__any(!is_q)) continue;
     const Quantised c = quantise8<LANES>(x);
-    if (!live) continue;
-    if (is_q) {
-      *reinterpret_cast<uint4v*>(a.qo + t * a.qo_token + h * a.qo_head + 8 * j) = pack8<BF16>(x);
-      continue;
-    }
-    const int slot = a.slots[t];
-    if (slot < 0 || slot >= a.pages * a.page) continue;
-    const int at = slot % a.page, r = at % kKvUnit;
-    uint8_t* unit = a.cache + kv_unit_offset<D>(slot / a.page, a.H, h, a.page, at);
+    if (!live || is_q || r.slot < 0 || r.slot >= a.pages << page_log) continue;
+    const int h = r.head - (is_k ? a.Hq : a.Hq + a.H);
+    const int at = r.slot & (a.page - 1), u = at % kKvUnit;
+    uint8_t* unit = a.cache + kv_unit_offset<D>(r.slot >> page_log, a.H, h, a.page, at);
     uint32_t* codes = reinterpret_cast<uint32_t*>(unit + (is_k ? 0 : KvUnit<D>::values));
-    codes[is_k ? r * LANES + j : (r / 4 * LANES + j) * 4 + r % 4] = c.codes;
+    codes[is_k ? u * LANES + j : (u / 4 * LANES + j) * 4 + u % 4] = c.codes;
     if (j == 0)
       reinterpret_cast<uint32_t*>(
-          unit + (is_k ? KvUnit<D>::key_params : KvUnit<D>::value_params))[r] = c.params;
+          unit + (is_k ? KvUnit<D>::key_params : KvUnit<D>::value_params))[u] = c.params;
   }
 }
 
@@ -258,15 +296,16 @@ hipError_t append(const KvAppendArgs& a, hipStream_t stream) {
   // Few tokens: one per workgroup, its rows shared out, so that every row
   // is under way at once; many: four per workgroup, which share no angles
   // but fill the threads that compute them.
-  const int tokens = a.T >= 1024 ? kMaxTokens : 1;
-  const int groups = (a.T + tokens - 1) / tokens;
-  const int rows = (a.Hq + 2 * a.H) * tokens;
+  const int tokens_log = a.T >= 1024 ? kMaxTokensLog : 0;
+  const int page_log = a.page > 0 ? 31 - __builtin_clz((unsigned)a.page) : 0;
+  const int groups = (a.T + (1 << tokens_log) - 1) >> tokens_log;
+  const int rows = (a.Hq + 2 * a.H) << tokens_log;
   int shares = (rows + ROWS - 1) / ROWS;
   const int enough = (2048 + groups - 1) / groups;
   if (shares > enough) shares = enough;
   if (shares > 65535) shares = 65535;
   hipLaunchKernelGGL((kv_append_kernel<D, BF16>), dim3(groups, shares), dim3(kThreads), 0, stream,
-                     a, tokens);
+                     a, tokens_log, page_log);
   return hipGetLastError();
 }
 
