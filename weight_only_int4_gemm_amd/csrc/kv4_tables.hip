@@ -6,7 +6,8 @@
 // its tail, so what a call reads of it (head .. head + count) and what it
 // writes (from head + count on) never meet, and workgroups need not wait for
 // each other.  Every workgroup therefore makes the (small) prefix sums for
-// itself in LDS and then takes its share of the tokens and pages.  lens_out
+// itself in LDS, beside what it needs of each request, and then takes its
+// share of the tokens and pages.  lens_out
 // and state_out may be lens and state: the last workgroup to finish, counted
 // in state_out[3], writes them.
 //
@@ -18,8 +19,11 @@ namespace w4a16 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItemsPerGroup = 1024;  // tokens and pages of one workgroup
-constexpr int kMaxGroups = 256;
+constexpr int kItemsPerGroup = 256;  // tokens and pages of one workgroup
+constexpr int kMaxGroups = 512;
+constexpr int kMaxPerThread = KV4_MAX_REQUESTS / kThreads;
+constexpr size_t kDefaultLds = 60 * 1024;  // beyond that a launch has to ask
+constexpr int kOver = (int)0x80000000;  // with a length: more pages wanted than fit
 
 // Addition of non-negative numbers that stops at `most`: associative, so a
 // scan of it does not depend on its shape, and no length overflows it.
@@ -28,20 +32,19 @@ __device__ __forceinline__ int add_up_to(int a, int b, int most) {
   return s < (unsigned)most ? (int)s : most;
 }
 
+// Lengths of a request as they count, and whether it wants too many pages.
 struct Request {
-  int len, want, old_pages, new_pages;
+  int len, want;
   bool over;
 };
 
-__device__ __forceinline__ Request request(const KvTablesArgs& a, int b) {
+__device__ __forceinline__ Request request(const KvTablesArgs& a, int len, int want) {
   Request r;
   const int64_t most = (int64_t)a.max_pages * a.page;
-  const int len = a.lens[b] > 0 ? a.lens[b] : 0;
+  len = len > 0 ? len : 0;
   r.len = len < most ? len : (int)most;
-  r.want = a.want[b] > 0 ? a.want[b] : 0;
-  r.old_pages = (int)(((int64_t)r.len + a.page - 1) / a.page);
-  r.new_pages = (int)(((int64_t)r.want + a.page - 1) / a.page);
-  r.over = r.new_pages > a.max_pages;
+  r.want = want > 0 ? want : 0;
+  r.over = r.want > most;
   return r;
 }
 
@@ -57,9 +60,8 @@ __device__ __forceinline__ int owner(const int* sums, int n, int x) {
 
 // Served requests are those whose pages are there: cumulative need within
 // the free pages (requests that take none are always served).
-__device__ __forceinline__ bool served(const Request& r, int taken_before, int taken_upto,
-                                       int count) {
-  return !r.over && (taken_upto == taken_before || taken_upto <= count);
+__device__ __forceinline__ bool served(bool over, int need_before, int need_upto, int count) {
+  return !over && (need_upto == need_before || need_upto <= count);
 }
 
 __global__ __launch_bounds__(kThreads) void kv_tables_kernel(KvTablesArgs a) {
@@ -68,11 +70,14 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(KvTablesArgs a) {
   int* const tok = lds;
   int* const need = tok + a.B + 1;
   int* const back = need + a.B + 1;
+  int* const held = back + a.B + 1;  // [B]: lengths, with kOver
   __shared__ int wave_sum[3][kThreads / 64];
   __shared__ int s_refused, s_taken, s_last;
   constexpr int kMost = 0x7fffffff;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (a.B + kThreads - 1) / kThreads;
+  const int shift = 31 - __builtin_clz((unsigned)a.page);
+  auto pages_of = [&](int n) { return (int)(((int64_t)n + a.page - 1) >> shift); };
   const int b0 = tid * per < a.B ? tid * per : a.B;
   const int b1 = b0 + per < a.B ? b0 + per : a.B;
   if (tid == 0) s_refused = s_taken = 0;
@@ -82,15 +87,29 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(KvTablesArgs a) {
   int count = a.state[1];
   count = count < 0 ? 0 : count > a.pages ? a.pages : count;
 
+  // the loads of all of a thread's requests at once
+  int lens[kMaxPerThread], want[kMaxPerThread];
+#pragma unroll
+  for (int k = 0; k < kMaxPerThread; ++k) {
+    if (k >= per) break;
+    const int b = b0 + k < a.B ? b0 + k : a.B - 1;
+    lens[k] = a.lens[b];
+    want[k] = a.want[b];
+  }
   int sum[3] = {0, 0, 0};
-  for (int b = b0; b < b1; ++b) {
-    const Request r = request(a, b);
+#pragma unroll
+  for (int k = 0; k < kMaxPerThread; ++k) {
+    if (k >= per) break;
+    const int b = b0 + k;
+    if (b >= b1) break;
+    const Request r = request(a, lens[k], want[k]);
     const int grown = r.want > r.len ? r.want - r.len : 0;
-    const int diff = r.over ? 0 : r.new_pages - r.old_pages;
+    const int diff = r.over ? 0 : pages_of(r.want) - pages_of(r.len);
     // kept per request; made exclusive below
     tok[b + 1] = grown;
     need[b + 1] = diff > 0 ? diff : 0;
     back[b + 1] = diff < 0 ? -diff : 0;
+    held[b] = r.len | (r.over ? kOver : 0);
     sum[0] = add_up_to(sum[0], grown, a.capacity);
     sum[1] = add_up_to(sum[1], need[b + 1], kMost);
     sum[2] = add_up_to(sum[2], back[b + 1], kMost);
@@ -132,16 +151,14 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(KvTablesArgs a) {
   const int take = wanted < count ? wanted : count;
   for (int i = first; i < take; i += stride) {
     const int b = owner(need, a.B, i);
-    const Request r = request(a, b);
-    if (!served(r, need[b], need[b + 1], count)) continue;
-    const int col = r.old_pages + i - need[b];
+    if (!served(false, need[b], need[b + 1], count)) continue;  // over wants none
+    const int col = pages_of(held[b]) + i - need[b];
     a.table[(int64_t)b * a.max_pages + col] = a.ring[(head + (unsigned)i) % P];
   }
-  // pages given back, to the tail
+  // pages given back, to the tail: the last of the request's row
   for (int i = first; i < returned; i += stride) {
     const int b = owner(back, a.B, i);
-    const Request r = request(a, b);
-    const int col = r.new_pages + i - back[b];
+    const int col = pages_of(held[b]) - (back[b + 1] - i);
     a.ring[(head + (unsigned)count + (unsigned)i) % P] =
         a.table[(int64_t)b * a.max_pages + col];
   }
@@ -149,16 +166,16 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(KvTablesArgs a) {
     int slot = -1, pos = 0;
     if (t < tokens) {
       const int b = owner(tok, a.B, t);
-      const Request r = request(a, b);
-      pos = r.len + t - tok[b];
-      if (served(r, need[b], need[b + 1], count)) {
-        const int col = pos / a.page;
+      const int len = held[b] & ~kOver;
+      pos = len + t - tok[b];
+      if (served(held[b] & kOver, need[b], need[b + 1], count)) {
+        const int col = pos >> shift, old = pages_of(len);
         // a page of this call comes from the ring: the table's entry may
         // not be written yet
-        const unsigned id = col >= r.old_pages
-                                ? a.ring[(head + (unsigned)(need[b] + col - r.old_pages)) % P]
+        const unsigned id = col >= old
+                                ? a.ring[(head + (unsigned)(need[b] + col - old)) % P]
                                 : a.table[(int64_t)b * a.max_pages + col];
-        if (id < P) slot = (int)id * a.page + pos % a.page;
+        if (id < P) slot = (int)(id << shift) | (pos & (a.page - 1));
       }
     }
     a.slots[t] = slot;
@@ -178,8 +195,8 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(KvTablesArgs a) {
     if (!s_last) return;
   }
   for (int b = tid; b < a.B; b += kThreads) {
-    const Request r = request(a, b);
-    const bool ok = served(r, need[b], need[b + 1], count);
+    const Request r = request(a, a.lens[b], a.want[b]);
+    const bool ok = served(r.over, need[b], need[b + 1], count);
     a.lens_out[b] = ok ? r.want : r.len;
     if (!ok) atomicAdd(&s_refused, 1);
     else if (need[b + 1] > need[b]) atomicMax(&s_taken, need[b + 1]);
@@ -197,13 +214,19 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(KvTablesArgs a) {
 }  // namespace
 
 hipError_t launch_kv_tables(const KvTablesArgs& a, hipStream_t stream) {
-  // One workgroup covers the requests' own work; tokens beyond that are
-  // shared out.  Pages are at most as many as tokens, or released ones,
-  // which are few.
+  // A token per thread (pages are at most as many as tokens, or released
+  // ones, which are few): 1000 requests with 62 thousand new tokens take
+  // 17 us with 256 per workgroup, 21 with 1024.
   int64_t groups = ((int64_t)a.capacity + kItemsPerGroup - 1) / kItemsPerGroup;
   if (groups < 1) groups = 1;
   if (groups > kMaxGroups) groups = kMaxGroups;
-  const size_t lds = 3 * (size_t)(a.B + 1) * sizeof(int);
+  const size_t lds = (4 * (size_t)a.B + 3) * sizeof(int);
+  if (lds > kDefaultLds) {
+    const hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(kv_tables_kernel),
+        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(kv_tables_kernel, dim3((unsigned)groups), dim3(kThreads), lds, stream, a);
   return hipGetLastError();
 }
