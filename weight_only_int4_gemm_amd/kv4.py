@@ -25,6 +25,7 @@ A cache is a uint8 tensor [pages, heads, page, D + 8] (``alloc_kv4_cache``).
 from __future__ import annotations
 
 import ctypes
+import functools
 
 KV4_ROPE_HALVES = 0
 KV4_ROPE_PAIRS = 1
@@ -69,221 +70,247 @@ def declare(lib) -> None:
     lib.kv4_attention_describe.restype = i
 
 
-def _w4():
-    import weight_only_int4_gemm_amd as w4
-    return w4
+# Decode steps call these functions once per layer, so a call's own cost
+# counts: the library, torch and the package are looked up once, and a call
+# asks for the current device once.
+_lib = _torch = _pkg = None
 
 
-def _on_device(t, what):
+def _bind():
+    global _lib, _torch, _pkg
     import torch
+    import weight_only_int4_gemm_amd as pkg
+    _lib, _torch, _pkg = pkg.load(), torch, pkg
+
+
+def _start():
+    """The current device's index (binds the library on the first call)."""
+    if _lib is None:
+        _bind()
+    return _torch.cuda.current_device() if _torch.cuda.is_initialized() else -1
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device)
+    return _pkg._stream(stream)
+
+
+def _check(fn, status):
+    if status:
+        _pkg._check(fn, status)
+
+
+def _wrong_device(t, what, device):
     if t.device.type != "cuda":
         raise ValueError(f"{what}: must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{device}")
 
 
-def _flat(t, dtype, what, numel):
-    """A contiguous tensor of at least ``numel`` elements."""
-    if t.dtype != dtype:
+def _flat(t, dtype, what, numel, device):
+    """The address of a contiguous tensor of at least ``numel`` elements."""
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
     if t.numel() < numel:
         raise ValueError(f"{what}: {t.numel()} elements, the call needs {numel}")
-    _on_device(t, what)
+    if t.get_device() != device or device < 0:
+        _wrong_device(t, what, device)
     return t.data_ptr()
 
 
 def _dtype(t, what):
-    import torch
-    if t.dtype == torch.float16:
-        return 0
-    if t.dtype == torch.bfloat16:
-        return 1
-    raise TypeError(f"{what}: expected float16 or bfloat16, got {t.dtype}")
+    dtype = t.dtype
+    if dtype is _torch.float16:
+        return dtype, 0
+    if dtype is _torch.bfloat16:
+        return dtype, 1
+    raise TypeError(f"{what}: expected float16 or bfloat16, got {dtype}")
 
 
-def _rows(t, what, dtype, T=None, heads=None, D=None):
+def _rows(t, what, dtype, device, T=None, heads=None, D=None):
     """(pointer, token stride, head stride) of a [T][heads][D] tensor."""
-    if t.dim() != 3:
-        raise ValueError(f"{what}: expected [tokens, heads, channels], got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what}: expected [tokens, heads, channels], got {tuple(shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    for n, m, name in ((t.shape[0], T, "tokens"), (t.shape[1], heads, "heads"),
-                       (t.shape[2], D, "channels")):
-        if m is not None and n != m:
-            raise ValueError(f"{what}: {n} {name}, expected {m}")
+    n, h, d = shape
+    if T is not None and n != T:
+        raise ValueError(f"{what}: {n} tokens, expected {T}")
+    if heads is not None and h != heads:
+        raise ValueError(f"{what}: {h} heads, expected {heads}")
+    if D is not None and d != D:
+        raise ValueError(f"{what}: {d} channels, expected {D}")
     token, head, channel = t.stride()
-    if channel != 1 and t.shape[2] > 1:
+    if channel != 1 and d > 1:
         raise ValueError(f"{what}: channels must be contiguous")
-    _on_device(t, what)
+    if t.get_device() != device or device < 0:
+        _wrong_device(t, what, device)
     # strides of dimensions of one element mean nothing
-    if t.shape[0] == 1:
-        token = 0
-    if t.shape[1] == 1:
-        head = 0
-    return t.data_ptr(), token, head
+    return t.data_ptr(), 0 if n == 1 else token, 0 if h == 1 else head
 
 
-def _cache(t):
+def _cache(t, device):
     """(pointer, pages, heads, D, page) of a cache."""
-    import torch
-    if t.dim() != 4:
-        raise ValueError(f"cache: expected [pages, heads, page, D + 8], got {tuple(t.shape)}")
-    pages, heads, page, d8 = t.shape
-    return _flat(t, torch.uint8, "cache", 0), pages, heads, d8 - 8, page
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError(f"cache: expected [pages, heads, page, D + 8], got {tuple(shape)}")
+    pages, heads, page, d8 = shape
+    return _flat(t, _torch.uint8, "cache", 0, device), pages, heads, d8 - 8, page
 
 
-def _rope(positions, inv_freq, sections, T):
-    """The six rotation arguments, and the section array to keep alive."""
-    import torch
+def _rope(positions, inv_freq, sections, T, device):
+    """The rotation's arguments up to the section array."""
     axes = len(sections)
-    sec = (ctypes.c_int * max(1, axes))(*(int(n) for n in sections))
-    if positions.dtype != torch.int32:
+    sec = (ctypes.c_int * max(1, axes))(*sections)
+    if positions.dtype is not _torch.int32:
         raise TypeError(f"positions: expected torch.int32, got {positions.dtype}")
     if positions.dim() == 1:
         positions = positions[None]
     if positions.dim() != 2 or positions.shape[0] != axes or positions.shape[1] < T:
         raise ValueError(f"positions: expected [{axes}, {T}], got {tuple(positions.shape)}")
-    if positions.shape[1] > 1 and positions.stride(1) != 1:
+    row, token = positions.stride()
+    if token != 1 and positions.shape[1] > 1:
         raise ValueError("positions: tokens must be contiguous")
-    _on_device(positions, "positions")
-    stride = positions.stride(0) if axes > 1 else 0
-    freq = _flat(inv_freq, torch.float64, "inv_freq", sum(int(n) for n in sections))
-    return positions.data_ptr(), stride, freq, sec
+    if positions.get_device() != device or device < 0:
+        _wrong_device(positions, "positions", device)
+    freq = _flat(inv_freq, _torch.float64, "inv_freq", sum(sections), device)
+    return positions.data_ptr(), row if axes > 1 else 0, freq, sec, axes
 
 
 def kv4_layout_version() -> int:
-    return _w4().load().kv4_layout_version()
+    _start()
+    return _lib.kv4_layout_version()
 
 
 def kv4_cache_bytes(pages: int, heads: int, D: int, page: int) -> int:
-    return _w4().load().kv4_cache_bytes(int(pages), int(heads), int(D), int(page))
+    _start()
+    return _lib.kv4_cache_bytes(pages, heads, D, page)
 
 
 def kv4_tables(lens, want, table, ring, state, lens_out, state_out, q_start, slots, positions,
                page: int, stream=None) -> None:
-    import torch
-    w4 = _w4()
+    dev = _start()
     if table.dim() != 2:
         raise ValueError(f"table: expected [requests, pages], got {tuple(table.shape)}")
     B, max_pages = table.shape
-    i32 = torch.int32
+    i32 = _torch.int32
     capacity = slots.numel()
-    w4._check("kv4_tables", w4.load().kv4_tables(
-        _flat(lens, i32, "lens", B), _flat(want, i32, "want", B),
-        _flat(table, i32, "table", 0), max_pages, _flat(ring, i32, "ring", 0), ring.numel(),
-        _flat(state, i32, "state", 4), _flat(lens_out, i32, "lens_out", B),
-        _flat(state_out, i32, "state_out", 4), _flat(q_start, i32, "q_start", B + 1),
-        _flat(slots, i32, "slots", 0), _flat(positions, i32, "positions", capacity), capacity,
-        B, int(page), w4._stream(stream)))
+    _check("kv4_tables", _lib.kv4_tables(
+        _flat(lens, i32, "lens", B, dev), _flat(want, i32, "want", B, dev),
+        _flat(table, i32, "table", 0, dev), max_pages, _flat(ring, i32, "ring", 0, dev),
+        ring.numel(), _flat(state, i32, "state", 4, dev),
+        _flat(lens_out, i32, "lens_out", B, dev), _flat(state_out, i32, "state_out", 4, dev),
+        _flat(q_start, i32, "q_start", B + 1, dev), _flat(slots, i32, "slots", 0, dev),
+        _flat(positions, i32, "positions", capacity, dev), capacity, B, page,
+        _raw_stream(stream, dev)))
 
 
 def kv4_rope(X, Y, positions, inv_freq, sections, pairs: int = KV4_ROPE_HALVES,
              stream=None) -> None:
-    w4 = _w4()
-    dtype = _dtype(X, "X")
-    x = _rows(X, "X", X.dtype)
+    dev = _start()
+    dtype, code = _dtype(X, "X")
+    x = _rows(X, "X", dtype, dev)
     T, H, D = X.shape
-    y = _rows(Y, "Y", X.dtype, T, H, D)
-    pos, stride, freq, sec = _rope(positions, inv_freq, sections, T)
-    w4._check("kv4_rope", w4.load().kv4_rope(*x, *y, pos, stride, freq, sec, len(sections),
-                                             int(pairs), T, H, D, dtype, w4._stream(stream)))
+    _check("kv4_rope", _lib.kv4_rope(
+        *x, *_rows(Y, "Y", dtype, dev, T, H, D), *_rope(positions, inv_freq, sections, T, dev),
+        pairs, T, H, D, code, _raw_stream(stream, dev)))
 
 
 def kv4_append(K, V, slots, cache, stream=None) -> None:
-    import torch
-    w4 = _w4()
-    dtype = _dtype(K, "K")
-    c, pages, heads, D, page = _cache(cache)
-    k = _rows(K, "K", K.dtype, None, heads, D)
+    dev = _start()
+    dtype, code = _dtype(K, "K")
+    c, pages, heads, D, page = _cache(cache, dev)
+    k = _rows(K, "K", dtype, dev, None, heads, D)
     T = K.shape[0]
-    v = _rows(V, "V", K.dtype, T, heads, D)
-    w4._check("kv4_append", w4.load().kv4_append(
-        *k, *v, _flat(slots, torch.int32, "slots", T), c, T, heads, D, pages, page, dtype,
-        w4._stream(stream)))
+    _check("kv4_append", _lib.kv4_append(
+        *k, *_rows(V, "V", dtype, dev, T, heads, D), _flat(slots, _torch.int32, "slots", T, dev),
+        c, T, heads, D, pages, page, code, _raw_stream(stream, dev)))
 
 
 def kv4_rope_append(Q, K, V, Qout, positions, inv_freq, sections, pairs: int, slots, cache,
                     stream=None) -> None:
     """``Q`` and ``Qout`` may be None: only keys are rotated."""
-    import torch
-    w4 = _w4()
-    dtype = _dtype(K, "K")
-    c, pages, heads, D, page = _cache(cache)
-    k = _rows(K, "K", K.dtype, None, heads, D)
+    dev = _start()
+    dtype, code = _dtype(K, "K")
+    c, pages, heads, D, page = _cache(cache, dev)
+    k = _rows(K, "K", dtype, dev, None, heads, D)
     T = K.shape[0]
-    v = _rows(V, "V", K.dtype, T, heads, D)
+    v = _rows(V, "V", dtype, dev, T, heads, D)
     q, qo, Hq = (None, 0, 0), (None, 0, 0), 0
     if Q is not None:
-        q = _rows(Q, "Q", K.dtype, T, None, D)
+        q = _rows(Q, "Q", dtype, dev, T, None, D)
         Hq = Q.shape[1]
-        qo = _rows(Qout, "Qout", K.dtype, T, Hq, D)
-    pos, stride, freq, sec = _rope(positions, inv_freq, sections, T)
-    w4._check("kv4_rope_append", w4.load().kv4_rope_append(
-        *q, *k, *v, *qo, pos, stride, freq, sec, len(sections), int(pairs),
-        _flat(slots, torch.int32, "slots", T), c, T, Hq, heads, D, pages, page, dtype,
-        w4._stream(stream)))
+        qo = _rows(Qout, "Qout", dtype, dev, T, Hq, D)
+    _check("kv4_rope_append", _lib.kv4_rope_append(
+        *q, *k, *v, *qo, *_rope(positions, inv_freq, sections, T, dev), pairs,
+        _flat(slots, _torch.int32, "slots", T, dev), c, T, Hq, heads, D, pages, page, code,
+        _raw_stream(stream, dev)))
 
 
 def kv4_dequant_debug(slots, cache, K, V, stream=None) -> None:
-    import torch
-    w4 = _w4()
-    dtype = _dtype(K, "K")
-    c, pages, heads, D, page = _cache(cache)
+    dev = _start()
+    dtype, code = _dtype(K, "K")
+    c, pages, heads, D, page = _cache(cache, dev)
     T = K.shape[0]
     for t, what in ((K, "K"), (V, "V")):
-        if tuple(t.shape) != (T, heads, D):
+        if t.shape != (T, heads, D):
             raise ValueError(f"{what}: expected {(T, heads, D)}, got {tuple(t.shape)}")
-    w4._check("kv4_dequant_debug", w4.load().kv4_dequant_debug(
-        _flat(slots, torch.int32, "slots", T), c, _flat(K, K.dtype, "K", 0),
-        _flat(V, K.dtype, "V", 0), T, heads, D, pages, page, dtype, w4._stream(stream)))
+    _check("kv4_dequant_debug", _lib.kv4_dequant_debug(
+        _flat(slots, _torch.int32, "slots", T, dev), c, _flat(K, dtype, "K", 0, dev),
+        _flat(V, dtype, "V", 0, dev), T, heads, D, pages, page, code,
+        _raw_stream(stream, dev)))
 
 
 def kv4_attention_workspace_bytes(B: int, Hq: int, H: int, D: int, max_q: int, max_len: int,
                                   window: int = 0) -> int:
-    return _w4().load().kv4_attention_workspace_bytes(int(B), int(Hq), int(H), int(D),
-                                                      int(max_q), int(max_len), int(window))
+    _start()
+    return _lib.kv4_attention_workspace_bytes(B, Hq, H, D, max_q, max_len, window)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(device, *sizes):
+    """kv4_attention_workspace_bytes of a device: a number that follows from
+    the sizes alone."""
+    return _lib.kv4_attention_workspace_bytes(*sizes)
 
 
 def kv4_attention_describe(B: int, Hq: int, H: int, D: int, max_q: int, max_len: int,
                            window: int = 0, cus: int = 0) -> str:
-    w4 = _w4()
+    _start()
     buf = ctypes.create_string_buffer(256)
-    w4._check("kv4_attention_describe", w4.load().kv4_attention_describe(
-        int(B), int(Hq), int(H), int(D), int(max_q), int(max_len), int(window), int(cus), buf,
-        256))
+    _check("kv4_attention_describe", _lib.kv4_attention_describe(
+        B, Hq, H, D, max_q, max_len, window, cus, buf, 256))
     return buf.value.decode()
 
 
 def kv4_attention(Q, cache, table, lens, q_start, O, lse, scale: float, window: int, max_q: int,
                   max_len: int, workspace=None, stream=None) -> None:
     """``q_start`` None: one query per request; ``lse`` may be None."""
-    import torch
-    w4 = _w4()
-    dtype = _dtype(Q, "Q")
-    c, pages, heads, D, page = _cache(cache)
-    q = _rows(Q, "Q", Q.dtype, None, None, D)
+    dev = _start()
+    dtype, code = _dtype(Q, "Q")
+    c, pages, heads, D, page = _cache(cache, dev)
+    q = _rows(Q, "Q", dtype, dev, None, None, D)
     T, Hq, _ = Q.shape
-    o = _rows(O, "O", Q.dtype, T, Hq, D)
+    o = _rows(O, "O", dtype, dev, T, Hq, D)
     if table.dim() != 2:
         raise ValueError(f"table: expected [requests, pages], got {tuple(table.shape)}")
     B, max_pages = table.shape
     if q_start is None and T < B:
         raise ValueError(f"Q: {T} rows for {B} requests")
-    i32 = torch.int32
+    i32 = _torch.int32
     ws = None
     if workspace is not None:
-        need = kv4_attention_workspace_bytes(B, Hq, heads, D, max_q, max_len, window)
+        need = _workspace_bytes(dev, B, Hq, heads, D, max_q, max_len, window)
         ws = _flat(workspace, workspace.dtype, "workspace",
-                   -(-need // workspace.element_size()))
-    w4._check("kv4_attention", w4.load().kv4_attention(
-        *q, c, _flat(table, i32, "table", 0), max_pages, _flat(lens, i32, "lens", B),
-        None if q_start is None else _flat(q_start, i32, "q_start", B + 1), *o,
-        None if lse is None else _flat(lse, torch.float32, "lse", T * Hq), T, B, Hq, heads, D,
-        pages, page, float(scale), int(window), int(max_q), int(max_len), dtype, ws,
-        w4._stream(stream)))
+                   -(-need // workspace.element_size()), dev)
+    _check("kv4_attention", _lib.kv4_attention(
+        *q, c, _flat(table, i32, "table", 0, dev), max_pages, _flat(lens, i32, "lens", B, dev),
+        None if q_start is None else _flat(q_start, i32, "q_start", B + 1, dev), *o,
+        None if lse is None else _flat(lse, _torch.float32, "lse", T * Hq, dev), T, B, Hq, heads,
+        D, pages, page, scale, window, max_q, max_len, code, ws, _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------------------
