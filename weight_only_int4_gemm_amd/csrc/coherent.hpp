@@ -43,4 +43,12 @@ __device__ __forceinline__ float4_t load_coherent(__amdgpu_buffer_rsrc_t r, int 
                             __builtin_amdgcn_raw_buffer_load_b128(r, idx * 16, 0, kDeviceScope));
 }
 
+// The first two of them.
+typedef float float2_t __attribute__((ext_vector_type(2)));
+typedef unsigned uint2_vt __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ float2_t load_coherent2(__amdgpu_buffer_rsrc_t r, int idx) {
+  return __builtin_bit_cast(float2_t,
+                            __builtin_amdgcn_raw_buffer_load_b64(r, idx * 16, 0, kDeviceScope));
+}
+
 }  // namespace w4a16

@@ -205,6 +205,41 @@ __device__ __forceinline__ bool last_to_arrive(unsigned* counter, int parts, boo
   return *s_last;
 }
 
+// One vector of a row over all parts, BATCH parts' loads in flight at once.
+template <int BATCH>
+__device__ __forceinline__ float4_t join_row(__amdgpu_buffer_rsrc_t all, int part_vecs,
+                                             int parts, int at, int stat, float* m_out,
+                                             float* l_out) {
+  float m = kNone, l = 0.f;
+  float4_t x = {0.f, 0.f, 0.f, 0.f};
+  for (int o0 = 0; o0 < parts; o0 += BATCH) {
+    float2_t ml[BATCH];
+    float4_t y[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int o = o0 + k < parts ? o0 + k : parts - 1;
+      ml[k] = load_coherent2(all, o * part_vecs + stat);
+      y[k] = load_coherent(all, o * part_vecs + at);
+    }
+    float to = m;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) to = fmaxf(to, ml[k][0]);
+    const float f = exp2_hw(m - to);
+    x *= f;
+    l *= f;
+    m = to;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const float w = o0 + k < parts ? exp2_hw(ml[k][0] - to) : 0.f;
+      x += y[k] * w;
+      l += ml[k][1] * w;
+    }
+  }
+  *m_out = m;
+  *l_out = l;
+  return x;
+}
+
 // The last workgroup joins `rows` rows over all parts, in range order.
 template <int D, bool BF16, int THREADS>
 __device__ __forceinline__ void join_parts(const float* tile_base, int part_vecs, int parts,
@@ -216,31 +251,11 @@ __device__ __forceinline__ void join_parts(const float* tile_base, int part_vecs
   for (int v = threadIdx.x; v < rows * kVecs; v += THREADS) {
     const int row = v / kVecs, c = v % kVecs;
     const int at = row * kPartVecs<D> + c, stat = row * kPartVecs<D> + kVecs;
-    float m = kNone, l = 0.f;
-    float4_t x = {0.f, 0.f, 0.f, 0.f};
-    constexpr int kBatch = 16;  // parts whose loads are in flight together
-    for (int o0 = 0; o0 < parts; o0 += kBatch) {
-      float4_t ml[kBatch], y[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int o = o0 + k < parts ? o0 + k : parts - 1;
-        ml[k] = load_coherent(all, o * part_vecs + stat);
-        y[k] = load_coherent(all, o * part_vecs + at);
-      }
-      float to = m;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) to = fmaxf(to, ml[k][0]);
-      const float f = exp2_hw(m - to);
-      x *= f;
-      l *= f;
-      m = to;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const float w = o0 + k < parts ? exp2_hw(ml[k][0] - to) : 0.f;
-        x += y[k] * w;
-        l += ml[k][1] * w;
-      }
-    }
+    float m, l;
+    // (loads past the last part are loads again of the last: for few parts
+    // most of a large batch would be)
+    const float4_t x = parts <= 4 ? join_row<4>(all, part_vecs, parts, at, stat, &m, &l)
+                                  : join_row<16>(all, part_vecs, parts, at, stat, &m, &l);
     const float y[4] = {x[0], x[1], x[2], x[3]};
     out.store<BF16, 4>(row0 + row, 4 * c, y, l == 0.f ? 0.f : 1.0f / l);
     if (c == 0) out.store_lse(row0 + row, m, l);
