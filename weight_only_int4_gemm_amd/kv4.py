@@ -87,7 +87,7 @@ def _start():
     """The current device's index (binds the library on the first call)."""
     if _lib is None:
         _bind()
-    return _torch.cuda.current_device() if _torch.cuda.is_initialized() else -1
+    return _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -1
 
 
 def _raw_stream(stream, device):
@@ -161,23 +161,27 @@ def _cache(t, device):
     return _flat(t, _torch.uint8, "cache", 0, device), pages, heads, d8 - 8, page
 
 
+@functools.lru_cache(maxsize=64)
+def _sections(sections):
+    return (ctypes.c_int * max(1, len(sections)))(*sections), len(sections), sum(sections)
+
+
 def _rope(positions, inv_freq, sections, T, device):
     """The rotation's arguments up to the section array."""
-    axes = len(sections)
-    sec = (ctypes.c_int * max(1, axes))(*sections)
+    sec, axes, half = _sections(tuple(sections))
     if positions.dtype is not _torch.int32:
         raise TypeError(f"positions: expected torch.int32, got {positions.dtype}")
-    if positions.dim() == 1:
-        positions = positions[None]
-    if positions.dim() != 2 or positions.shape[0] != axes or positions.shape[1] < T:
+    shape, stride = positions.shape, positions.stride()
+    if len(shape) == 1:
+        shape, stride = (1, *shape), (0, *stride)
+    if len(shape) != 2 or shape[0] != axes or shape[1] < T:
         raise ValueError(f"positions: expected [{axes}, {T}], got {tuple(positions.shape)}")
-    row, token = positions.stride()
-    if token != 1 and positions.shape[1] > 1:
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError("positions: tokens must be contiguous")
     if positions.get_device() != device or device < 0:
         _wrong_device(positions, "positions", device)
-    freq = _flat(inv_freq, _torch.float64, "inv_freq", sum(sections), device)
-    return positions.data_ptr(), row if axes > 1 else 0, freq, sec, axes
+    return (positions.data_ptr(), stride[0] if axes > 1 else 0,
+            _flat(inv_freq, _torch.float64, "inv_freq", half, device), sec, axes)
 
 
 def kv4_layout_version() -> int:
