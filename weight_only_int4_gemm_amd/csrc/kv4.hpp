@@ -81,15 +81,15 @@ struct KvAttentionArgs {
 };
 
 // How a kv4_attention call is cut into work.
-//  nb     16-row blocks of query rows (query, head of the group) per wave
-//  rows   1: the waves of a workgroup take different query rows and walk the
-//         same tokens; 0: they share 16 * nb rows and divide the tokens
+//  row_tile  query rows (query, head of the group) of a workgroup
+//  rows   1: its waves take different ones and walk the same tokens;
+//         0: they share them and divide the tokens
 //  waves  waves per workgroup
 //  tiles  row tiles per (request, head)
 //  splits token ranges per row tile, one workgroup each, of `chunk` tokens
 //         (longer where a request is longer than planned)
 struct KvAttentionPlan {
-  int nb, rows, waves, tiles, splits, chunk;
+  int row_tile, rows, waves, tiles, splits, chunk;
   size_t workspace_bytes;
 };
 

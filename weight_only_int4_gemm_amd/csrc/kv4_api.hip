@@ -325,7 +325,7 @@ int kv4_attention_describe(int B, int Hq, int H, int D, int max_q, int max_len, 
   if (cus <= 0) return W4A16_ERR_DEVICE;
   const KvAttentionPlan p = make_kv_attention_plan(B, Hq, H, D, max_q, max_len, window, cus);
   snprintf(buf, len, "kv_attention<%d,%d,%s> grid=%lld block=%d tiles=%d splits=%d chunk=%d workspace=%zu",
-           D, p.nb, p.rows ? "rows" : "tokens", (long long)B * H * p.tiles * p.splits,
+           D, p.row_tile, p.rows ? "rows" : "tokens", (long long)B * H * p.tiles * p.splits,
            64 * p.waves, p.tiles, p.splits, p.chunk, p.workspace_bytes);
   return W4A16_OK;
 }

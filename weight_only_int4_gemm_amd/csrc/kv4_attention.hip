@@ -47,16 +47,40 @@ __device__ __forceinline__ float groups_max(float x) {
   return fmaxf(x, __shfl_xor(x, 32));
 }
 
+// Blocks of 16 columns (matrix operand) for a tile of ROWS query rows.
+template <int ROWS>
+constexpr int kBlocks = ROWS == 32 ? 2 : 1;
+
+// With at most eight rows, columns n and n + 8 are the same row.  The two
+// lanes then divide the softmax (one takes the first unit's tokens, the other
+// the second's), and FP16's two products with the values become one: columns
+// below 8 take the rounded weights, the others the remainders.
+template <int ROWS>
+constexpr bool kPaired = ROWS == 8;
+
+// The lane of the same four tokens eight columns on.
+__device__ __forceinline__ uint32_t pair_lane(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xf, 0xf, true);  // row_ror:8
+}
+__device__ __forceinline__ float pair_lane(float x) {
+  return __builtin_bit_cast(float, pair_lane(__builtin_bit_cast(uint32_t, x)));
+}
+
 // What one lane loads of two units.
-template <int D>
+template <int D, int ROWS>
 struct TileData {
+  static constexpr int PARAMS = kPaired<ROWS> ? 1 : 2;  // units a lane needs these of
   static constexpr int KV = D / 32;                 // key words per unit
   static constexpr int VV = D == 256 ? 2 : 1;       // value vectors per unit
   uint32_t k[2][KV];
   uint4v v[2][VV];
-  uint4v kp[2], vp[2];
+  uint4v kp[PARAMS], vp[PARAMS];
   bool valid[2];                                    // the unit's page exists
 };
+
+// Cache policy of the code loads: a workgroup reads them once (non-temporal).
+// 64 requests of 4096 tokens, 32 heads: 128 us with it, 147 without.
+constexpr int kStreamed = 2;
 
 // Where a head's units lie: page id `p` of it starts at
 // cache + head offset + p * page stride.
@@ -66,11 +90,12 @@ struct Pages {
   int shift, count; // log2 of a page's tokens, pages of the cache
 };
 
-template <int D>
-__device__ __forceinline__ void load_tile(TileData<D>& d, const Pages& pages, PageIds& ids,
+template <int D, int ROWS>
+__device__ __forceinline__ void load_tile(TileData<D, ROWS>& d, const Pages& pages, PageIds& ids,
                                           int t) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const uint8_t* base = nullptr;
+  const uint8_t* bases[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     if (u == 0 || pages.shift == 4) {
@@ -87,13 +112,13 @@ __device__ __forceinline__ void load_tile(TileData<D>& d, const Pages& pages, Pa
     const __amdgpu_buffer_rsrc_t unit = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t*>(base), (short)0, KvUnit<D>::bytes, 0x00020000);
     auto load16 = [&](int at, int plus) {
-      return __builtin_bit_cast(uint4v,
-                                __builtin_amdgcn_raw_buffer_load_b128(unit, at + plus, 0, 0));
+      return __builtin_bit_cast(
+          uint4v, __builtin_amdgcn_raw_buffer_load_b128(unit, at + plus, 0, kStreamed));
     };
     const int key = r * (D / 2) + g * (D / 8);
     if constexpr (D == 64) {
       const uint2v w =
-          __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(unit, key, 0, 0));
+          __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(unit, key, 0, kStreamed));
       d.k[u][0] = w[0];
       d.k[u][1] = w[1];
     } else {
@@ -106,10 +131,19 @@ __device__ __forceinline__ void load_tile(TileData<D>& d, const Pages& pages, Pa
     }
     const int value = g * (2 * D) + 16 * (D == 64 ? r >> 1 : r);
 #pragma unroll
-    for (int i = 0; i < TileData<D>::VV; ++i)
+    for (int i = 0; i < TileData<D, ROWS>::VV; ++i)
       d.v[u][i] = load16(value, KvUnit<D>::values + 256 * i);
-    d.kp[u] = load16(16 * g, KvUnit<D>::key_params);
-    d.vp[u] = load16(16 * g, KvUnit<D>::value_params);
+    if constexpr (!kPaired<ROWS>) {
+      const uint8_t* mine = base + 16 * g;
+      d.kp[u] = *reinterpret_cast<const uint4v*>(mine + KvUnit<D>::key_params);
+      d.vp[u] = *reinterpret_cast<const uint4v*>(mine + KvUnit<D>::value_params);
+    }
+    bases[u] = base;
+  }
+  if constexpr (kPaired<ROWS>) {
+    const uint8_t* mine = (lane & 8 ? bases[1] : bases[0]) + 16 * g;
+    d.kp[0] = *reinterpret_cast<const uint4v*>(mine + KvUnit<D>::key_params);
+    d.vp[0] = *reinterpret_cast<const uint4v*>(mine + KvUnit<D>::value_params);
   }
 }
 
@@ -138,10 +172,15 @@ struct Queries {
 // One tile.  `edge`: some of its tokens are not seen by some row.  What the
 // cache holds for those may be anything (NaN included), so they are taken out
 // of the probabilities and the weights, never multiplied by zero.
-template <int D, int NB, bool BF16>
-__device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB>& q,
-                                       Sums<D, NB>& s, int t, bool edge) {
+template <int D, int ROWS, bool BF16>
+__device__ __forceinline__ void attend(const TileData<D, ROWS>& d,
+                                       const Queries<D, kBlocks<ROWS>>& q,
+                                       Sums<D, kBlocks<ROWS>>& s, int t, bool edge) {
+  constexpr int NB = kBlocks<ROWS>;
+  constexpr bool PAIRED = kPaired<ROWS>;
+  constexpr int N = PAIRED ? 4 : 8;  // scores of a lane, per block
   const int lane = threadIdx.x & 63, g = lane >> 4;
+  const bool upper = PAIRED && (lane & 8);
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
   float4v raw[NB][2];
@@ -163,21 +202,25 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
     }
   }
 
+  if constexpr (PAIRED) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[0][0][i] = upper ? raw[0][1][i] : raw[0][0][i];
+  }
   auto key_params = [&](int i) { return d.kp[i >> 2][i & 3]; };
   auto value_params = [&](int i) { return d.vp[i >> 2][i & 3]; };
-  float scale[8];  // of the keys, times the logits' unit
+  float scale[N];  // of the keys, times the logits' unit
 #pragma unroll
-  for (int i = 0; i < 8; ++i) scale[i] = times_low_half(q.unit, key_params(i));
+  for (int i = 0; i < N; ++i) scale[i] = times_low_half(q.unit, key_params(i));
 
   // FP16: the remainders of the weights' rounding as a second operand
-  constexpr int kParts = BF16 ? 1 : 2;
+  constexpr int kParts = BF16 || PAIRED ? 1 : 2;
   uint4v weights[NB][kParts];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    float p[8], w[8], sum, most;
+    float p[N], w[N], sum, most;
     auto seen = [&](int i) {
-      const int j = (int)apart(t + 4 * g) + kKvUnit * (i >> 2) + (i & 3);
-      return d.valid[i >> 2] && j >= q.lo[nb] && j <= q.hi[nb];
+      const int j = (int)apart(t + 4 * g + (upper ? kKvUnit : 0)) + kKvUnit * (i >> 2) + (i & 3);
+      return (upper ? d.valid[1] : d.valid[i >> 2]) && j >= q.lo[nb] && j <= q.hi[nb];
     };
     // the logit less m: scale (q . c) + (offset sum q - m)
     auto logit = [&](int i, float m) {
@@ -186,14 +229,14 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
     };
     auto weigh = [&](float m) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < N; ++i) {
         p[i] = exp2_hw(logit(i, m));
         w[i] = times_low_half(p[i], value_params(i));
       }
       if (edge) {
         keep_branch();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < N; ++i) {
           p[i] = seen(i) ? p[i] : 0.f;
           w[i] = seen(i) ? w[i] : 0.f;
         }
@@ -201,9 +244,9 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
       sum = 0.f;
       most = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += p[i];
+      for (int i = 0; i < N; ++i) sum += p[i];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) most = fmaxf(fmaxf(most, w[i]), w[i + 1]);
+      for (int i = 0; i < N; i += 2) most = fmaxf(fmaxf(most, w[i]), w[i + 1]);
     };
     weigh(s.m[nb]);
     if (__any(most > kMostWeight || sum > kMostSum)) {
@@ -211,14 +254,16 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
       // a probability exceed 2^40 (values of scale 0).
       float top = kNone;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < N; ++i) {
         const float offset = high_half(apart(key_params(i)));
         float x = scale[i] * raw[nb][i >> 2][i & 3] + offset * q.sum[nb];
         if (edge) x = seen(i) ? x : -__builtin_inff();
         top = fmaxf(top, x + __builtin_amdgcn_logf(low_half(apart(value_params(i)))) - kTopWeight);
         top = fmaxf(top, x - kSumHeadroom);
       }
-      const float m = fmaxf(s.m[nb], groups_max(top));
+      top = groups_max(top);
+      if constexpr (PAIRED) top = fmaxf(top, pair_lane(top));
+      const float m = fmaxf(s.m[nb], top);
       const float f = exp2_hw(s.m[nb] - m);
       s.m[nb] = m;
       s.l[nb] *= f;
@@ -232,18 +277,32 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
     if (edge) {
       keep_branch();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s.z[nb] += seen(i) ? p[i] * high_half(apart(value_params(i))) : 0.f;
+      for (int i = 0; i < N; ++i) s.z[nb] += seen(i) ? p[i] * high_half(apart(value_params(i))) : 0.f;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s.z[nb] += p[i] * high_half(value_params(i));
+      for (int i = 0; i < N; ++i) s.z[nb] += p[i] * high_half(value_params(i));
     }
+    uint32_t h[N / 2], rest[N / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t h = pack_halves(w[2 * i], w[2 * i + 1]);
-      if constexpr (!BF16) {
-        weights[nb][1][i] = pack_halves(less_low_half(w[2 * i], h), less_high_half(w[2 * i + 1], h));
+    for (int i = 0; i < N / 2; ++i) {
+      h[i] = pack_halves(w[2 * i], w[2 * i + 1]);
+      if constexpr (!BF16)
+        rest[i] = pack_halves(less_low_half(w[2 * i], h[i]), less_high_half(w[2 * i + 1], h[i]));
+    }
+    if constexpr (PAIRED) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t keep = BF16 ? h[i] : upper ? rest[i] : h[i];
+        const uint32_t theirs = pair_lane(BF16 ? h[i] : upper ? h[i] : rest[i]);
+        weights[nb][0][i] = upper ? theirs : keep;
+        weights[nb][0][i + 2] = upper ? keep : theirs;
       }
-      weights[nb][0][i] = h;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        weights[nb][0][i] = h[i];
+        if constexpr (kParts == 2) weights[nb][1][i] = rest[i];
+      }
     }
   }
 
@@ -257,7 +316,7 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
   const uint32_t half = D == 64 ? (lane & 1) * 0x00020002u : 0u;
   constexpr int kBytes = D == 64 ? 2 : 4;
 #pragma unroll
-  for (int i = 0; i < TileData<D>::VV; ++i) {
+  for (int i = 0; i < TileData<D, ROWS>::VV; ++i) {
 #pragma unroll
     for (int b = 0; b < kBytes; ++b) {
       const uint32_t sel = (0x0c040c00u + 0x00010001u * b) + half;
@@ -281,9 +340,10 @@ __device__ __forceinline__ void attend(const TileData<D>& d, const Queries<D, NB
   }
 }
 
-template <int D, int NB, bool BF16>
-__device__ __forceinline__ void load_queries(Queries<D, NB>& q, const KvAttentionArgs& a,
+template <int D, int ROWS, bool BF16>
+__device__ __forceinline__ void load_queries(Queries<D, kBlocks<ROWS>>& q, const KvAttentionArgs& a,
                                              const Span& sp, int head, int group, int row0) {
+  constexpr int NB = kBlocks<ROWS>;
   const int lane = threadIdx.x & 63, g = lane >> 4;
   uint4v raw[NB][D / 64][2];
   auto element = [&](int nb, int p, int c) {
@@ -296,7 +356,7 @@ __device__ __forceinline__ void load_queries(Queries<D, NB>& q, const KvAttentio
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     // rows past the last repeat it; they are not stored
-    const int want = row0 + 16 * nb + (lane & 15);
+    const int want = row0 + 16 * nb + (lane & (kPaired<ROWS> ? 7 : 15));
     const int row = want < sp.rows ? want : sp.rows - 1;
     const int i = row / group;
     const uint16_t* src = a.q.p + (int64_t)(sp.tok0 + i) * a.q.token +
@@ -358,14 +418,14 @@ template <int D>
 constexpr int kLdsRow = D + 4;
 
 // Waves per SIMD the registers are divided for.
-template <int D, int NB>
-constexpr int kResident = D * NB <= 128 ? 2 : 1;
+template <int D, int ROWS>
+constexpr int kResident = D * kBlocks<ROWS> <= 128 ? 2 : 1;
 
-template <int D, int NB, bool BF16>
-__global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel(
+template <int D, int ROWS, bool BF16>
+__global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kernel(
     KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
     float* __restrict__ partials) {
-  constexpr int kRowTile = 16 * NB;
+  constexpr int NB = kBlocks<ROWS>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.Hq / a.H;
   int id = blockIdx.x;
@@ -375,8 +435,8 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel
   const int tile = id % tiles;
   id /= tiles;
   const int head = id % a.H, b = id / a.H;
-  const int row0 = tile * kRowTile;
-  const Span sp = span_of(a, b, group, row0, kRowTile);
+  const int row0 = tile * ROWS;
+  const Span sp = span_of(a, b, group, row0, ROWS);
   if (row0 >= sp.rows) return;
   const Range range = range_of(sp, split, splits, chunk);
   if (split >= range.parts) return;
@@ -386,7 +446,7 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel
   const int end = begin + each < range.end ? begin + each : range.end;
 
   Queries<D, NB> q;
-  load_queries<D, NB, BF16>(q, a, sp, head, group, row0);
+  load_queries<D, ROWS, BF16>(q, a, sp, head, group, row0);
   Sums<D, NB> s;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
@@ -398,7 +458,7 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel
   }
 
   // Inner tiles, which every row sees whole, need no mask.
-  const int row_last = row0 + kRowTile < sp.rows ? row0 + kRowTile - 1 : sp.rows - 1;
+  const int row_last = row0 + ROWS < sp.rows ? row0 + ROWS - 1 : sp.rows - 1;
   const int pos_first = sp.len - sp.nq + row0 / group;
   const int pos_last = sp.len - sp.nq + row_last / group;
   const int inner_end = pos_first + 1;  // exclusive
@@ -418,23 +478,23 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel
     // tile again, at the end): where a branch could skip them, the wait for a
     // tile would have to allow for both sides and so wait for the next one.
     constexpr int kAhead = 1;
-    TileData<D> ring[kAhead + 1];
+    TileData<D, ROWS> ring[kAhead + 1];
     const int last = begin + (end - begin - 1) / kTile * kTile;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int t = begin + k * kTile;
-      load_tile<D>(ring[k], pages, ids, t < last ? t : last);
+      load_tile<D, ROWS>(ring[k], pages, ids, t < last ? t : last);
     }
     for (int t0 = begin; t0 < end; t0 += (kAhead + 1) * kTile) {
 #pragma unroll
       for (int k = 0; k <= kAhead; ++k) {
         const int t = t0 + k * kTile, then = t + kAhead * kTile;
         if (t >= end) break;
-        load_tile<D>(ring[(k + kAhead) % (kAhead + 1)], pages, ids, then < last ? then : last);
-        const TileData<D>& cur = ring[k];
+        load_tile<D, ROWS>(ring[(k + kAhead) % (kAhead + 1)], pages, ids, then < last ? then : last);
+        const TileData<D, ROWS>& cur = ring[k];
         const bool edge =
             t < inner_begin || t + kTile > inner_end || !cur.valid[0] || !cur.valid[1];
-        attend<D, NB, BF16>(cur, q, s, t, edge);
+        attend<D, ROWS, BF16>(cur, q, s, t, edge);
       }
     }
   }
@@ -444,6 +504,17 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel
   float total[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
+    if constexpr (kPaired<ROWS>) {
+      s.l[nb] += pair_lane(s.l[nb]);
+      s.z[nb] += pair_lane(s.z[nb]);
+      if constexpr (!BF16) {
+        s.w[nb][0] += pair_lane(s.w[nb][0]);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s.acc[nb][c][i] += pair_lane(s.acc[nb][c][i]);
+      }
+    }
     total[nb] = groups_sum(s.l[nb]);
     const float fixed = groups_sum(s.z[nb]) - 8.0f * s.w[nb][0];
 #pragma unroll
@@ -456,11 +527,11 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel
   constexpr int kCols = D == 64 ? 4 : 8;  // neighbouring channels of a lane
   // Join the waves, in wave order, through LDS: each leaves its rows and
   // their (m, l), and the threads add them up per element.
-  constexpr int kSlab = 16 * NB * kLdsRow<D>;
+  constexpr int kSlab = ROWS * kLdsRow<D>;
   __shared__ float red[kWaves * kSlab];
-  __shared__ float s_m[kWaves][16 * NB], s_l[kWaves][16 * NB];
+  __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS];
   __shared__ bool s_last;
-  const int rows = sp.rows - row0 < 16 * NB ? sp.rows - row0 : 16 * NB;
+  const int rows = sp.rows - row0 < ROWS ? sp.rows - row0 : ROWS;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const int row = 16 * nb + n16;
@@ -510,7 +581,7 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel
   }
   // Publish this workgroup's rows, then count the arrival; the last
   // workgroup of the row tile joins them in range order.
-  constexpr int kVecsOfPart = kRowTile * kPartVecs<D>;
+  constexpr int kVecsOfPart = ROWS * kPartVecs<D>;
   const float* tile_base = partials + (int64_t)work * splits * kVecsOfPart * 4;
   {
     const __amdgpu_buffer_rsrc_t mine = coherent_rsrc(tile_base + split * kVecsOfPart * 4);
@@ -526,15 +597,15 @@ __global__ __launch_bounds__(kThreads, (kResident<D, NB>)) void kv_tokens_kernel
                                   counters + work);
 }
 
-template <int D, int NB>
+template <int D, int ROWS>
 hipError_t launch(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
                   unsigned* counters, float* partials, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)a.B * a.H * p.tiles * p.splits));
   if (dtype == W4A16_DTYPE_BF16)
-    hipLaunchKernelGGL((kv_tokens_kernel<D, NB, true>), grid, dim3(kThreads), 0, stream, a,
+    hipLaunchKernelGGL((kv_tokens_kernel<D, ROWS, true>), grid, dim3(kThreads), 0, stream, a,
                        p.tiles, p.splits, p.chunk, counters, partials);
   else
-    hipLaunchKernelGGL((kv_tokens_kernel<D, NB, false>), grid, dim3(kThreads), 0, stream, a,
+    hipLaunchKernelGGL((kv_tokens_kernel<D, ROWS, false>), grid, dim3(kThreads), 0, stream, a,
                        p.tiles, p.splits, p.chunk, counters, partials);
   return hipGetLastError();
 }
@@ -543,8 +614,9 @@ hipError_t launch(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
 template <int D>
 hipError_t launch_d(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
                     unsigned* counters, float* partials, hipStream_t stream) {
-  if (p.nb == 1) return launch<D, 1>(p, a, dtype, counters, partials, stream);
-  return launch<D, D == 256 ? 1 : 2>(p, a, dtype, counters, partials, stream);
+  if (p.row_tile == 8) return launch<D, 8>(p, a, dtype, counters, partials, stream);
+  if (p.row_tile == 16) return launch<D, 16>(p, a, dtype, counters, partials, stream);
+  return launch<D, D == 256 ? 16 : 32>(p, a, dtype, counters, partials, stream);
 }
 
 }  // namespace
@@ -567,9 +639,9 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
   const int64_t rows = (int64_t)(Hq / H) * max_q;
   // Many rows: the waves of a workgroup take 32 each and share the tokens.
   p.rows = rows > 64;
-  p.nb = p.rows ? 2 : D < 256 && rows > 16 ? 2 : 1;
+  p.row_tile = p.rows ? 128 : rows <= 8 ? 8 : D < 256 && rows > 16 ? 32 : 16;
   p.waves = kWaves;
-  const int tile_rows = 16 * p.nb * (p.rows ? p.waves : 1);
+  const int tile_rows = p.row_tile;
   p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
   p.splits = 1;
   int64_t keys = max_len;
@@ -578,11 +650,16 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
   p.chunk = (int)(keys < (1 << 30) ? keys : (1 << 30));
   const int64_t work = (int64_t)B * H * p.tiles;
   if (work <= kMaxSplitTiles) {
-    // Token ranges: rounds of resident workgroups times the steps of a wave
-    // in one, of which starting, joining the waves and joining the ranges
-    // are worth about kStart, kJoin steps.
-    constexpr int64_t kStart = 5, kJoin = 3;
-    const int64_t slots = (int64_t)cus * (D * (p.rows ? 1 : p.nb) <= 128 ? 2 : 1);
+    // Token ranges: rounds of workgroups times the steps of a wave in one,
+    // of which starting, joining the waves and joining the ranges are worth
+    // about kStart, kJoin and a quarter for each range.  With few rows a
+    // workgroup per compute unit reads about as fast as HBM gives, and more
+    // beside it only add ranges: one request of 131072 tokens, 8 heads, 32 us
+    // in 32 ranges, 34 in 61 or 64.  With more rows a second one fills the
+    // first's waits: 24 requests of 5 tokens, 37 us in two ranges, 42 in one.
+    constexpr int64_t kStart = 5, kJoin = 1;
+    const bool second = p.row_tile > 8 && D * (p.row_tile == 32 ? 2 : 1) <= 128;
+    const int64_t slots = (int64_t)cus * (second ? 2 : 1);
     const int64_t sharing = p.rows ? 1 : kWaves;  // waves that divide the tokens
     const int64_t steps = keys / kTile;
     const int64_t part = (int64_t)tile_rows * (D + 4) * (int64_t)sizeof(float);
@@ -593,7 +670,7 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
     for (int64_t i = 1; i <= most; ++i) {
       const int64_t rounds = (work * i + slots - 1) / slots;
       const int64_t each = ((steps + i - 1) / i + sharing - 1) / sharing;
-      const int64_t cost = rounds * (each + kStart) + (i > 1 ? kJoin : 0);
+      const int64_t cost = 4 * (rounds * (each + kStart) + (i > 1 ? kJoin : 0)) + i;
       if (i == 1 || cost < best) {
         best = cost;
         n = i;
