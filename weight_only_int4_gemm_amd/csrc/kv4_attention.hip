@@ -30,6 +30,18 @@
 // outputs it would be as large as it, so there the weights are two FP16
 // numbers, the rounded weight and its remainder, and the product with the
 // values runs twice.
+//
+// Work.  A workgroup has 8 or 16 query rows of one request and key/value
+// head and a range of its tokens, which its four waves divide; ranges are
+// joined by the workgroup that arrives last.  A tile of 32 tokens is loaded
+// one tile ahead, straight into registers: nothing is shared between waves.
+//
+// What bounds it (D = 128): HBM in decode steps, 64 requests of 4096 tokens
+// and 32 heads 127 us (6.2 TB/s), one of 131072 tokens and 8 heads 31 us (4.6
+// TB/s: the start and the join take about 8 us); eight dependent trips to
+// memory in short calls, one of 1000 tokens and 32 heads 8.7 us; vector and
+// matrix instructions, which hardly overlap, with more rows: 24 requests of 5
+// queries on windows of 4096 tokens, 32 heads on 8, D = 64, 32 us.
 #include "kv4_attention.hpp"
 
 namespace w4a16 {
@@ -37,6 +49,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
+
 // Sum and maximum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_sum(float x) {
   x += __shfl_xor(x, 16);
@@ -46,10 +59,6 @@ __device__ __forceinline__ float groups_max(float x) {
   x = fmaxf(x, __shfl_xor(x, 16));
   return fmaxf(x, __shfl_xor(x, 32));
 }
-
-// Blocks of 16 columns (matrix operand) for a tile of ROWS query rows.
-template <int ROWS>
-constexpr int kBlocks = ROWS == 32 ? 2 : 1;
 
 // With at most eight rows, columns n and n + 8 are the same row.  The two
 // lanes then divide the softmax (one takes the first unit's tokens, the other
@@ -147,64 +156,57 @@ __device__ __forceinline__ void load_tile(TileData<D, ROWS>& d, const Pages& pag
   }
 }
 
-// The sums of 16 * NB query rows over the tokens seen so far, for column
-// (row) lane % 16 of each block.
-template <int D, int NB>
+// The sums of the query rows over the tokens seen so far, for column (row)
+// lane % 16.
+template <int D>
 struct Sums {
-  float4v acc[NB][D / 16];  // sum of w c, in the operands' units
-  float4v w[NB];            // sum of w (every element the same)
-  float m[NB];              // reference
-  float l[NB], z[NB];       // this lane's part of sum p, sum p z
+  float4v acc[D / 16];  // sum of w c, in the operands' units
+  float4v w;            // sum of w (every element the same)
+  float m;              // reference
+  float l, z;           // this lane's part of sum p, sum p z
 };
 
 // A wave's query rows as operands, and what its columns need.
-template <int D, int NB>
+template <int D>
 struct Queries {
   // channels by parity of the nibble; the odd ones, which meet codes of 16
   // times the size, are divided by 16
-  uint4v even[NB][D / 64], odd[NB][D / 64];
-  float sum8[NB];    // -8 sum q, in the products' units
-  float unit;        // product units to base-2 logits
-  float sum[NB];     // sum q in base-2 logits
-  int lo[NB], hi[NB];  // keys seen: lo <= j <= hi
+  uint4v even[D / 64], odd[D / 64];
+  float sum8;  // -8 sum q, in the products' units
+  float unit;  // product units to base-2 logits
+  float sum;   // sum q in base-2 logits
+  int lo, hi;  // keys seen: lo <= j <= hi
 };
 
 // One tile.  `edge`: some of its tokens are not seen by some row.  What the
 // cache holds for those may be anything (NaN included), so they are taken out
 // of the probabilities and the weights, never multiplied by zero.
 template <int D, int ROWS, bool BF16>
-__device__ __forceinline__ void attend(const TileData<D, ROWS>& d,
-                                       const Queries<D, kBlocks<ROWS>>& q,
-                                       Sums<D, kBlocks<ROWS>>& s, int t, bool edge) {
-  constexpr int NB = kBlocks<ROWS>;
+__device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries<D>& q,
+                                       Sums<D>& s, int t, bool edge) {
   constexpr bool PAIRED = kPaired<ROWS>;
-  constexpr int N = PAIRED ? 4 : 8;  // scores of a lane, per block
+  constexpr int N = PAIRED ? 4 : 8;  // scores of a lane
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const bool upper = PAIRED && (lane & 8);
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
-  float4v raw[NB][2];
+  float4v raw[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-      raw[nb][u] = float4v{q.sum8[nb], q.sum8[nb], q.sum8[nb], q.sum8[nb]};
+    raw[u] = float4v{q.sum8, q.sum8, q.sum8, q.sum8};
 #pragma unroll
     for (int p = 0; p < D / 64; ++p) {
       const uint32_t w0 = d.k[u][2 * p], w1 = d.k[u][2 * p + 1];
       const uint4v e = {w0 & kLow, w1 & kLow, (w0 >> 8) & kLow, (w1 >> 8) & kLow};
       const uint4v o = {w0 & kHigh, w1 & kHigh, (w0 >> 8) & kHigh, (w1 >> 8) & kHigh};
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        raw[nb][u] = mfma(e, q.even[nb][p], raw[nb][u]);
-        raw[nb][u] = mfma(o, q.odd[nb][p], raw[nb][u]);
-      }
+      raw[u] = mfma(e, q.even[p], raw[u]);
+      raw[u] = mfma(o, q.odd[p], raw[u]);
     }
   }
 
   if constexpr (PAIRED) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[0][0][i] = upper ? raw[0][1][i] : raw[0][0][i];
+    for (int i = 0; i < 4; ++i) raw[0][i] = upper ? raw[1][i] : raw[0][i];
   }
   auto key_params = [&](int i) { return d.kp[i >> 2][i & 3]; };
   auto value_params = [&](int i) { return d.vp[i >> 2][i & 3]; };
@@ -214,103 +216,98 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d,
 
   // FP16: the remainders of the weights' rounding as a second operand
   constexpr int kParts = BF16 || PAIRED ? 1 : 2;
-  uint4v weights[NB][kParts];
+  uint4v weights[kParts];
+  float p[N], w[N], sum, most;
+  auto seen = [&](int i) {
+    const int j = (int)apart(t + 4 * g + (upper ? kKvUnit : 0)) + kKvUnit * (i >> 2) + (i & 3);
+    return (upper ? d.valid[1] : d.valid[i >> 2]) && j >= q.lo && j <= q.hi;
+  };
+  // the logit less m: scale (q . c) + (offset sum q - m)
+  auto logit = [&](int i, float m) {
+    return __builtin_fmaf(scale[i], raw[i >> 2][i & 3],
+                          __builtin_fmaf(high_half(key_params(i)), q.sum, -m));
+  };
+  auto weigh = [&](float m) {
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    float p[N], w[N], sum, most;
-    auto seen = [&](int i) {
-      const int j = (int)apart(t + 4 * g + (upper ? kKvUnit : 0)) + kKvUnit * (i >> 2) + (i & 3);
-      return (upper ? d.valid[1] : d.valid[i >> 2]) && j >= q.lo[nb] && j <= q.hi[nb];
-    };
-    // the logit less m: scale (q . c) + (offset sum q - m)
-    auto logit = [&](int i, float m) {
-      return __builtin_fmaf(scale[i], raw[nb][i >> 2][i & 3],
-                            __builtin_fmaf(high_half(key_params(i)), q.sum[nb], -m));
-    };
-    auto weigh = [&](float m) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        p[i] = exp2_hw(logit(i, m));
-        w[i] = times_low_half(p[i], value_params(i));
-      }
-      if (edge) {
-        keep_branch();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          p[i] = seen(i) ? p[i] : 0.f;
-          w[i] = seen(i) ? w[i] : 0.f;
-        }
-      }
-      sum = 0.f;
-      most = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) sum += p[i];
-#pragma unroll
-      for (int i = 0; i < N; i += 2) most = fmaxf(fmaxf(most, w[i]), w[i + 1]);
-    };
-    weigh(s.m[nb]);
-    if (__any(most > kMostWeight || sum > kMostSum)) {
-      // Move the reference: the largest weight becomes 2^8, unless that lets
-      // a probability exceed 2^40 (values of scale 0).
-      float top = kNone;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float offset = high_half(apart(key_params(i)));
-        float x = scale[i] * raw[nb][i >> 2][i & 3] + offset * q.sum[nb];
-        if (edge) x = seen(i) ? x : -__builtin_inff();
-        top = fmaxf(top, x + __builtin_amdgcn_logf(low_half(apart(value_params(i)))) - kTopWeight);
-        top = fmaxf(top, x - kSumHeadroom);
-      }
-      top = groups_max(top);
-      if constexpr (PAIRED) top = fmaxf(top, pair_lane(top));
-      const float m = fmaxf(s.m[nb], top);
-      const float f = exp2_hw(s.m[nb] - m);
-      s.m[nb] = m;
-      s.l[nb] *= f;
-      s.z[nb] *= f;
-      s.w[nb] *= f;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) s.acc[nb][c] *= f;
-      weigh(m);
+    for (int i = 0; i < N; ++i) {
+      p[i] = exp2_hw(logit(i, m));
+      w[i] = times_low_half(p[i], value_params(i));
     }
-    s.l[nb] += sum;
     if (edge) {
       keep_branch();
 #pragma unroll
-      for (int i = 0; i < N; ++i) s.z[nb] += seen(i) ? p[i] * high_half(apart(value_params(i))) : 0.f;
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) s.z[nb] += p[i] * high_half(value_params(i));
-    }
-    uint32_t h[N / 2], rest[N / 2];
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      h[i] = pack_halves(w[2 * i], w[2 * i + 1]);
-      if constexpr (!BF16)
-        rest[i] = pack_halves(less_low_half(w[2 * i], h[i]), less_high_half(w[2 * i + 1], h[i]));
-    }
-    if constexpr (PAIRED) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t keep = BF16 ? h[i] : upper ? rest[i] : h[i];
-        const uint32_t theirs = pair_lane(BF16 ? h[i] : upper ? h[i] : rest[i]);
-        weights[nb][0][i] = upper ? theirs : keep;
-        weights[nb][0][i + 2] = upper ? keep : theirs;
+      for (int i = 0; i < N; ++i) {
+        p[i] = seen(i) ? p[i] : 0.f;
+        w[i] = seen(i) ? w[i] : 0.f;
       }
-    } else {
+    }
+    sum = 0.f;
+    most = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        weights[nb][0][i] = h[i];
-        if constexpr (kParts == 2) weights[nb][1][i] = rest[i];
-      }
+    for (int i = 0; i < N; ++i) sum += p[i];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) most = fmaxf(fmaxf(most, w[i]), w[i + 1]);
+  };
+  weigh(s.m);
+  if (__any(most > kMostWeight || sum > kMostSum)) {
+    // Move the reference: the largest weight becomes 2^8, unless that lets
+    // a probability exceed 2^40 (values of scale 0).
+    float top = kNone;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float offset = high_half(apart(key_params(i)));
+      float x = scale[i] * raw[i >> 2][i & 3] + offset * q.sum;
+      if (edge) x = seen(i) ? x : -__builtin_inff();
+      top = fmaxf(top, x + __builtin_amdgcn_logf(low_half(apart(value_params(i)))) - kTopWeight);
+      top = fmaxf(top, x - kSumHeadroom);
+    }
+    top = groups_max(top);
+    if constexpr (PAIRED) top = fmaxf(top, pair_lane(top));
+    const float m = fmaxf(s.m, top);
+    const float f = exp2_hw(s.m - m);
+    s.m = m;
+    s.l *= f;
+    s.z *= f;
+    s.w *= f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) s.acc[c] *= f;
+    weigh(m);
+  }
+  s.l += sum;
+  if (edge) {
+    keep_branch();
+#pragma unroll
+    for (int i = 0; i < N; ++i) s.z += seen(i) ? p[i] * high_half(apart(value_params(i))) : 0.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s.z += p[i] * high_half(value_params(i));
+  }
+  uint32_t h[N / 2], rest[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    h[i] = pack_halves(w[2 * i], w[2 * i + 1]);
+    if constexpr (!BF16)
+      rest[i] = pack_halves(less_low_half(w[2 * i], h[i]), less_high_half(w[2 * i + 1], h[i]));
+  }
+  if constexpr (PAIRED) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t keep = BF16 ? h[i] : upper ? rest[i] : h[i];
+      const uint32_t theirs = pair_lane(BF16 ? h[i] : upper ? h[i] : rest[i]);
+      weights[0][i] = upper ? theirs : keep;
+      weights[0][i + 2] = upper ? keep : theirs;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      weights[0][i] = h[i];
+      if constexpr (kParts == 2) weights[1][i] = rest[i];
     }
   }
 
   const uint4v ones = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int k = 0; k < kParts; ++k) s.w[nb] = mfma(ones, weights[nb][k], s.w[nb]);
+  for (int k = 0; k < kParts; ++k) s.w = mfma(ones, weights[k], s.w);
 
   // byte b of two tokens' words into the two halves of a register
   const uint32_t half = D == 64 ? (lane & 1) * 0x00020002u : 0u;
@@ -330,54 +327,48 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d,
       }
       const int c = 2 * (kBytes * i + b);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) {
-          s.acc[nb][c] = mfma(e, weights[nb][k], s.acc[nb][c]);
-          s.acc[nb][c + 1] = mfma(o, weights[nb][k], s.acc[nb][c + 1]);
-        }
+      for (int k = 0; k < kParts; ++k) {
+        s.acc[c] = mfma(e, weights[k], s.acc[c]);
+        s.acc[c + 1] = mfma(o, weights[k], s.acc[c + 1]);
+      }
     }
   }
 }
 
 template <int D, int ROWS, bool BF16>
-__device__ __forceinline__ void load_queries(Queries<D, kBlocks<ROWS>>& q, const KvAttentionArgs& a,
+__device__ __forceinline__ void load_queries(Queries<D>& q, const KvAttentionArgs& a,
                                              const Span& sp, int head, int group, int row0) {
-  constexpr int NB = kBlocks<ROWS>;
   const int lane = threadIdx.x & 63, g = lane >> 4;
-  uint4v raw[NB][D / 64][2];
-  auto element = [&](int nb, int p, int c) {
-    const uint32_t w = raw[nb][p][c >> 3][(c >> 1) & 3];
+  uint4v raw[D / 64][2];
+  auto element = [&](int p, int c) {
+    const uint32_t w = raw[p][c >> 3][(c >> 1) & 3];
     const uint32_t bits = c & 1 ? w >> 16 : w & 0xffffu;
     if constexpr (BF16) return __builtin_bit_cast(float, bits << 16);
     else return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
   };
-  float top = 0.f;  // the largest magnitude of the rows that are finite
+  // rows past the last repeat it; they are not stored
+  const int want = row0 + (lane & (kPaired<ROWS> ? 7 : 15));
+  const int row = want < sp.rows ? want : sp.rows - 1;
+  const int i = row / group;
+  const uint16_t* src = a.q.p + (int64_t)(sp.tok0 + i) * a.q.token +
+                        (int64_t)(head * group + row - i * group) * a.q.head;
+  uint32_t most = 0;
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    // rows past the last repeat it; they are not stored
-    const int want = row0 + 16 * nb + (lane & (kPaired<ROWS> ? 7 : 15));
-    const int row = want < sp.rows ? want : sp.rows - 1;
-    const int i = row / group;
-    const uint16_t* src = a.q.p + (int64_t)(sp.tok0 + i) * a.q.token +
-                          (int64_t)(head * group + row - i * group) * a.q.head;
-    uint32_t most = 0;
+  for (int p = 0; p < D / 64; ++p) {
+    const uint4v* w = reinterpret_cast<const uint4v*>(src + 8 * (g * (D / 32) + 2 * p));
+    raw[p][0] = w[0];
+    raw[p][1] = w[1];
 #pragma unroll
-    for (int p = 0; p < D / 64; ++p) {
-      const uint4v* w = reinterpret_cast<const uint4v*>(src + 8 * (g * (D / 32) + 2 * p));
-      raw[nb][p][0] = w[0];
-      raw[nb][p][1] = w[1];
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        most = max(most, __builtin_bit_cast(uint32_t, element(nb, p, c)) & 0x7fffffffu);
-    }
-    most = max(most, (uint32_t)__shfl_xor((int)most, 16));
-    most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-    if (most < 0x7f800000u) top = fmaxf(top, __builtin_bit_cast(float, most));
-    const int pos = sp.len - sp.nq + i;
-    q.hi[nb] = pos;
-    q.lo[nb] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+    for (int c = 0; c < 16; ++c)
+      most = max(most, __builtin_bit_cast(uint32_t, element(p, c)) & 0x7fffffffu);
   }
+  most = max(most, (uint32_t)__shfl_xor((int)most, 16));
+  most = max(most, (uint32_t)__shfl_xor((int)most, 32));
+  // the largest magnitude of the rows that are finite
+  float top = most < 0x7f800000u ? __builtin_bit_cast(float, most) : 0.f;
+  const int pos = sp.len - sp.nq + i;
+  q.hi = pos;
+  q.lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
 #pragma unroll
   for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
   // The wave's rows are brought near FP16's upper end by one power of two:
@@ -390,26 +381,23 @@ __device__ __forceinline__ void load_queries(Queries<D, kBlocks<ROWS>>& q, const
   const float back = __builtin_bit_cast(float, (uint32_t)(127 - 13 + e) << 23);
   const float logits = a.scale * kLog2e * back;
   q.unit = logits * 0x1p24f;
+  float sum = 0.f;
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    float sum = 0.f;
+  for (int p = 0; p < D / 64; ++p) {
+    _Float16 h[16];
 #pragma unroll
-    for (int p = 0; p < D / 64; ++p) {
-      _Float16 h[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        h[c] = (_Float16)(element(nb, p, c) * (c & 1 ? 0.0625f * up : up));
-        sum += (float)h[c] * (c & 1 ? 16.0f : 1.0f);
-      }
-      const half8 even = {h[0], h[4], h[8], h[12], h[2], h[6], h[10], h[14]};
-      const half8 odd = {h[1], h[5], h[9], h[13], h[3], h[7], h[11], h[15]};
-      q.even[nb][p] = __builtin_bit_cast(uint4v, even);
-      q.odd[nb][p] = __builtin_bit_cast(uint4v, odd);
+    for (int c = 0; c < 16; ++c) {
+      h[c] = (_Float16)(element(p, c) * (c & 1 ? 0.0625f * up : up));
+      sum += (float)h[c] * (c & 1 ? 16.0f : 1.0f);
     }
-    sum = groups_sum(sum);
-    q.sum8[nb] = sum * -0x1p-21f;
-    q.sum[nb] = sum * logits;
+    const half8 even = {h[0], h[4], h[8], h[12], h[2], h[6], h[10], h[14]};
+    const half8 odd = {h[1], h[5], h[9], h[13], h[3], h[7], h[11], h[15]};
+    q.even[p] = __builtin_bit_cast(uint4v, even);
+    q.odd[p] = __builtin_bit_cast(uint4v, odd);
   }
+  sum = groups_sum(sum);
+  q.sum8 = sum * -0x1p-21f;
+  q.sum = sum * logits;
 }
 
 // Rows of D floats of a block in LDS, padded so that the 16 rows of a store
@@ -419,13 +407,12 @@ constexpr int kLdsRow = D + 4;
 
 // Waves per SIMD the registers are divided for.
 template <int D, int ROWS>
-constexpr int kResident = D * kBlocks<ROWS> <= 128 ? 2 : 1;
+constexpr int kResident = D <= 128 || kPaired<ROWS> ? 2 : 1;
 
 template <int D, int ROWS, bool BF16>
 __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kernel(
     KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
     float* __restrict__ partials) {
-  constexpr int NB = kBlocks<ROWS>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.Hq / a.H;
   int id = blockIdx.x;
@@ -445,17 +432,14 @@ __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kern
   const int begin = range.begin + wave * each;
   const int end = begin + each < range.end ? begin + each : range.end;
 
-  Queries<D, NB> q;
+  Queries<D> q;
   load_queries<D, ROWS, BF16>(q, a, sp, head, group, row0);
-  Sums<D, NB> s;
+  Sums<D> s;
+  s.m = kNone;
+  s.l = s.z = 0.f;
+  s.w = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    s.m[nb] = kNone;
-    s.l[nb] = s.z[nb] = 0.f;
-    s.w[nb] = float4v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) s.acc[nb][c] = float4v{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int c = 0; c < D / 16; ++c) s.acc[c] = float4v{0.f, 0.f, 0.f, 0.f};
 
   // Inner tiles, which every row sees whole, need no mask.
   const int row_last = row0 + ROWS < sp.rows ? row0 + ROWS - 1 : sp.rows - 1;
@@ -490,7 +474,8 @@ __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kern
       for (int k = 0; k <= kAhead; ++k) {
         const int t = t0 + k * kTile, then = t + kAhead * kTile;
         if (t >= end) break;
-        load_tile<D, ROWS>(ring[(k + kAhead) % (kAhead + 1)], pages, ids, then < last ? then : last);
+        load_tile<D, ROWS>(ring[(k + kAhead) % (kAhead + 1)], pages, ids,
+                           then < last ? then : last);
         const TileData<D, ROWS>& cur = ring[k];
         const bool edge =
             t < inner_begin || t + kTile > inner_end || !cur.valid[0] || !cur.valid[1];
@@ -501,28 +486,24 @@ __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kern
 
   // Each lane's rows as true sums: O (unnormalised), sum p.
   const int g = lane >> 4, n16 = lane & 15;
-  float total[NB];
+  if constexpr (kPaired<ROWS>) {
+    s.l += pair_lane(s.l);
+    s.z += pair_lane(s.z);
+    if constexpr (!BF16) {
+      s.w[0] += pair_lane(s.w[0]);
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    if constexpr (kPaired<ROWS>) {
-      s.l[nb] += pair_lane(s.l[nb]);
-      s.z[nb] += pair_lane(s.z[nb]);
-      if constexpr (!BF16) {
-        s.w[nb][0] += pair_lane(s.w[nb][0]);
+      for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s.acc[nb][c][i] += pair_lane(s.acc[nb][c][i]);
-      }
+        for (int i = 0; i < 4; ++i) s.acc[c][i] += pair_lane(s.acc[c][i]);
     }
-    total[nb] = groups_sum(s.l[nb]);
-    const float fixed = groups_sum(s.z[nb]) - 8.0f * s.w[nb][0];
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        s.acc[nb][c][i] = s.acc[nb][c][i] * (c & 1 ? 0x1p20f : 0x1p24f) + fixed;
   }
+  const float total = groups_sum(s.l);
+  const float fixed = groups_sum(s.z) - 8.0f * s.w[0];
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s.acc[c][i] = s.acc[c][i] * (c & 1 ? 0x1p20f : 0x1p24f) + fixed;
 
   constexpr int kCols = D == 64 ? 4 : 8;  // neighbouring channels of a lane
   // Join the waves, in wave order, through LDS: each leaves its rows and
@@ -532,22 +513,18 @@ __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kern
   __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS];
   __shared__ bool s_last;
   const int rows = sp.rows - row0 < ROWS ? sp.rows - row0 : ROWS;
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int row = 16 * nb + n16;
-    if (row >= rows) continue;
+  if (n16 < rows) {
     if (g == 0) {
-      s_m[wave][row] = s.m[nb];
-      s_l[wave][row] = total[nb];
+      s_m[wave][n16] = s.m;
+      s_l[wave][n16] = total;
     }
-    float* at = red + wave * kSlab + row * kLdsRow<D> + kCols * 4 * g;
+    float* at = red + wave * kSlab + n16 * kLdsRow<D> + kCols * 4 * g;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < D / 16; c += 4)
         *reinterpret_cast<float4v*>(at + kCols * i + c % kCols + c / kCols * 128) =
-            float4v{s.acc[nb][c][i], s.acc[nb][c + 1][i], s.acc[nb][c + 2][i],
-                    s.acc[nb][c + 3][i]};
+            float4v{s.acc[c][i], s.acc[c + 1][i], s.acc[c + 2][i], s.acc[c + 3][i]};
   }
   __syncthreads();
   // Four neighbouring channels of a row over all waves, and its (m, l).
@@ -610,13 +587,11 @@ hipError_t launch(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
   return hipGetLastError();
 }
 
-// A second block of 256-channel rows does not fit the registers.
 template <int D>
 hipError_t launch_d(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
                     unsigned* counters, float* partials, hipStream_t stream) {
-  if (p.row_tile == 8) return launch<D, 8>(p, a, dtype, counters, partials, stream);
-  if (p.row_tile == 16) return launch<D, 16>(p, a, dtype, counters, partials, stream);
-  return launch<D, D == 256 ? 16 : 32>(p, a, dtype, counters, partials, stream);
+  return p.row_tile == 8 ? launch<D, 8>(p, a, dtype, counters, partials, stream)
+                         : launch<D, 16>(p, a, dtype, counters, partials, stream);
 }
 
 }  // namespace
@@ -630,61 +605,88 @@ hipError_t launch_kv_tokens(const KvAttentionPlan& p, const KvAttentionArgs& a, 
   }
 }
 
+namespace {
+
 // What partial results may take of a workspace.
 constexpr int64_t kMostPartBytes = ((int64_t)192 << 20) - (int64_t)kCounterHeaderBytes;
 
+// A plan for row tiles of `row_tile` rows, and an estimate of its time in us.
+//
+// A workgroup takes a step of 32 tokens (a wave of four, where waves divide
+// the tokens) in `alone`, or in `shared` beside a second one on its compute
+// unit; kStart steps go by before and after.  With up to eight rows a second
+// one gains nothing: HBM bounds the first.  Rounds of workgroups end
+// unevenly, and requests of a batch are taken to hold 0.65 of the longest
+// one on average.  Token ranges cost their partial results' way to memory
+// and back, and the join, in which one workgroup reads all of a row tile's.
+// (Measured, with the best count of ranges and with one: one request of
+// 131072 tokens, 8 heads, 32 ranges, 31 us, 208 with 3; 500 queries over
+// 8192 tokens, 4, 137 us, 268 with one; 24 x 476 over 6597, 595 with 2, 478
+// with one.)
+double plan_for(KvAttentionPlan* p, int row_tile, int B, int H, int64_t rows, int D,
+                int64_t keys, int cus) {
+  constexpr double kStart = 5, kJoin = 0.6, kPartsRate = 1e6, kJoinRate = 64e3;  // bytes per us
+  constexpr double kUneven = 0.35, kAverage = 0.65;
+  p->row_tile = row_tile;
+  p->rows = row_tile == 128;
+  p->waves = kWaves;
+  p->tiles = (int)((rows + row_tile - 1) / row_tile);
+  p->splits = 1;
+  p->chunk = (int)(keys < (1 << 30) ? keys : (1 << 30));
+  const int size = D == 64 ? 0 : D == 128 ? 1 : 2;
+  constexpr double kAlone[3][3] = {{0.6, 0.75, 1.3}, {0.7, 0.8, 1.4}, {0.9, 1.05, 2.0}};
+  constexpr double kShared[3][3] = {{0.6, 0.75, 1.3}, {0.8, 1.05, 1.4}, {1.2, 1.6, 2.0}};
+  const int kind = row_tile == 8 ? 0 : row_tile == 16 ? 1 : 2;
+  const double alone = kAlone[kind][size], shared = kShared[kind][size];
+  const bool second = shared > alone;
+  const int64_t work = (int64_t)B * H * p->tiles;
+  const int64_t sharing = p->rows ? 1 : kWaves;  // waves that divide the tokens
+  const int64_t steps = keys / kTile;
+  const int64_t part = (int64_t)row_tile * (D + 4) * (int64_t)sizeof(float);
+  int64_t most = (steps + sharing - 1) / sharing;
+  if (most > 16 * (int64_t)cus / work + 1) most = 16 * (int64_t)cus / work + 1;
+  if (most > kMostPartBytes / (work * part)) most = kMostPartBytes / (work * part);
+  if (most < 1 || work > kMaxSplitTiles) most = 1;
+  double best = 0;
+  int64_t n = 1;
+  for (int64_t i = 1; i <= most; ++i) {
+    const int64_t each = ((steps + i - 1) / i + sharing - 1) / sharing;
+    const bool both = second && work * i > cus;
+    const double load = (double)(work * i) / (both ? 2 * cus : cus);
+    const double rounds = (B > 1 ? load * kAverage : load) + kUneven;
+    double cost = (load <= 1 || rounds < 1 ? 1 : rounds) * (each + kStart) *
+                  (both ? shared : alone);
+    if (i > 1) cost += kJoin + work * i * part / kPartsRate + i * part / kJoinRate;
+    if (i == 1 || cost < best) {
+      best = cost;
+      n = i;
+    }
+  }
+  if (n > 1) {
+    p->chunk = (int)((keys + n - 1) / n + kTile - 1) / kTile * kTile;
+    p->splits = (int)((keys + p->chunk - 1) / p->chunk);
+    p->workspace_bytes = kCounterHeaderBytes + (size_t)(work * p->splits * part);
+  }
+  return best;
+}
+
+}  // namespace
+
+// Up to eight rows pair columns.  Beyond that tiles of 16 rows have the
+// waits of two workgroups per compute unit overlap and waste few rows; tiles
+// of 128 unpack the codes once for all, which pays when they are full and the
+// chip is (2 x 2048 queries: 0.74 ms; 32 x 128 queries over 1024 tokens, 32
+// heads: 105 us against 187 in tiles of 16; 8 x 96 over 2048: 78 against 48).
 KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, int max_len,
                                        int window, int cus) {
-  KvAttentionPlan p{};
   const int64_t rows = (int64_t)(Hq / H) * max_q;
-  // Many rows: the waves of a workgroup take 32 each and share the tokens.
-  p.rows = rows > 64;
-  p.row_tile = p.rows ? 128 : rows <= 8 ? 8 : D < 256 && rows > 16 ? 32 : 16;
-  p.waves = kWaves;
-  const int tile_rows = p.row_tile;
-  p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
-  p.splits = 1;
   int64_t keys = max_len;
   if (window > 0 && keys > (int64_t)window + max_q) keys = (int64_t)window + max_q;
   keys = (keys + kTile - 1) / kTile * kTile + kTile;
-  p.chunk = (int)(keys < (1 << 30) ? keys : (1 << 30));
-  const int64_t work = (int64_t)B * H * p.tiles;
-  if (work <= kMaxSplitTiles) {
-    // Token ranges: rounds of workgroups times the steps of a wave in one,
-    // of which starting, joining the waves and joining the ranges are worth
-    // about kStart, kJoin and a quarter for each range.  With few rows a
-    // workgroup per compute unit reads about as fast as HBM gives, and more
-    // beside it only add ranges: one request of 131072 tokens, 8 heads, 32 us
-    // in 32 ranges, 34 in 61 or 64.  With more rows a second one fills the
-    // first's waits: 24 requests of 5 tokens, 37 us in two ranges, 42 in one.
-    constexpr int64_t kStart = 5, kJoin = 1;
-    const bool second = p.row_tile > 8 && D * (p.row_tile == 32 ? 2 : 1) <= 128;
-    const int64_t slots = (int64_t)cus * (second ? 2 : 1);
-    const int64_t sharing = p.rows ? 1 : kWaves;  // waves that divide the tokens
-    const int64_t steps = keys / kTile;
-    const int64_t part = (int64_t)tile_rows * (D + 4) * (int64_t)sizeof(float);
-    int64_t most = 8 * slots / work + 1;
-    if (most > (steps + sharing - 1) / sharing) most = (steps + sharing - 1) / sharing;
-    if (most > kMostPartBytes / (work * part)) most = kMostPartBytes / (work * part);
-    int64_t best = 0, n = 1;
-    for (int64_t i = 1; i <= most; ++i) {
-      const int64_t rounds = (work * i + slots - 1) / slots;
-      const int64_t each = ((steps + i - 1) / i + sharing - 1) / sharing;
-      const int64_t cost = 4 * (rounds * (each + kStart) + (i > 1 ? kJoin : 0)) + i;
-      if (i == 1 || cost < best) {
-        best = cost;
-        n = i;
-      }
-    }
-    if (n > 1) {
-      p.chunk = (int)((keys + n - 1) / n + kTile - 1) / kTile * kTile;
-      p.splits = (int)((keys + p.chunk - 1) / p.chunk);
-    }
-  }
-  if (p.splits > 1)
-    p.workspace_bytes = kCounterHeaderBytes + (size_t)work * p.splits * tile_rows * (D + 4) *
-                                                  sizeof(float);
-  return p;
+  KvAttentionPlan few{}, many{};
+  const double time = plan_for(&few, rows <= 8 ? 8 : 16, B, H, rows, D, keys, cus);
+  if (rows <= 64) return few;
+  return plan_for(&many, 128, B, H, rows, D, keys, cus) < time ? many : few;
 }
 
 hipError_t launch_kv_attention(const KvAttentionPlan& p, const KvAttentionArgs& a, int D,
