@@ -87,9 +87,12 @@ struct TileData {
   bool valid[2];                                    // the unit's page exists
 };
 
-// Cache policy of the code loads: a workgroup reads them once (non-temporal).
-// 64 requests of 4096 tokens, 32 heads: 128 us with it, 147 without.
-constexpr int kStreamed = 2;
+// Cache policy of the code loads.  With paired rows a workgroup alone reads
+// them, once (non-temporal: 64 requests of 4096 tokens, 32 heads, 128 us, 147
+// without); with more rows neighbouring row tiles find them in the L2 (91
+// requests of 18 rows, 66 us, 77 with non-temporal loads).
+template <int ROWS>
+constexpr int kPolicy = kPaired<ROWS> ? 2 : 0;
 
 // Where a head's units lie: page id `p` of it starts at
 // cache + head offset + p * page stride.
@@ -122,12 +125,13 @@ __device__ __forceinline__ void load_tile(TileData<D, ROWS>& d, const Pages& pag
         const_cast<uint8_t*>(base), (short)0, KvUnit<D>::bytes, 0x00020000);
     auto load16 = [&](int at, int plus) {
       return __builtin_bit_cast(
-          uint4v, __builtin_amdgcn_raw_buffer_load_b128(unit, at + plus, 0, kStreamed));
+          uint4v, __builtin_amdgcn_raw_buffer_load_b128(unit, at + plus, 0, kPolicy<ROWS>));
     };
     const int key = r * (D / 2) + g * (D / 8);
     if constexpr (D == 64) {
       const uint2v w =
-          __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(unit, key, 0, kStreamed));
+          __builtin_bit_cast(
+              uint2v, __builtin_amdgcn_raw_buffer_load_b64(unit, key, 0, kPolicy<ROWS>));
       d.k[u][0] = w[0];
       d.k[u][1] = w[1];
     } else {
@@ -415,13 +419,18 @@ __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kern
     float* __restrict__ partials) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.Hq / a.H;
-  int id = blockIdx.x;
-  const int split = id % splits;
-  id /= splits;
-  const int work = id;               // (request, head, row tile)
-  const int tile = id % tiles;
-  id /= tiles;
-  const int head = id % a.H, b = id / a.H;
+  // Row tiles of one token range read the same codes: workgroups 8 apart, in
+  // turn on the same XCD, whose L2 then holds them (3 requests of 294 rows
+  // over 16600 tokens: 97 -> 74 us).
+  const int id = blockIdx.x, ranges = gridDim.x / tiles, whole = ranges & ~7;
+  const bool tail = id >= whole * tiles;
+  const int width = tail ? ranges - whole : 8, in = tail ? id - whole * tiles : id;
+  const int tile = in / width % tiles;
+  int range_id = (tail ? whole : in / (8 * tiles) * 8) + in % width;
+  const int split = range_id % splits;
+  range_id /= splits;                       // (request, head)
+  const int work = range_id * tiles + tile;
+  const int head = range_id % a.H, b = range_id / a.H;
   const int row0 = tile * ROWS;
   const Span sp = span_of(a, b, group, row0, ROWS);
   if (row0 >= sp.rows) return;
