@@ -66,6 +66,24 @@ struct KvTablesArgs {
   int capacity, B, page;
 };
 
+// Division of 0 <= n < 2^31 by a number the host knows: with 2^(s-1) < d <=
+// 2^s and m = floor(2^32 (2^s - d) / d) + 1, floor(n / d) is
+// (n + floor(n m / 2^32)) >> s (the round-up reciprocal).  A workgroup's start
+// is a chain of divisions; by the instruction for reciprocals they take 1 us.
+struct Divisor {
+  uint32_t d, m;
+  int s;
+  Divisor() = default;
+  explicit Divisor(int by) : d((uint32_t)by), m(0), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)((((1ull << s) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ int of(int n) const {
+    return (int)(((uint32_t)n + __umulhi((uint32_t)n, m)) >> s);
+  }
+  __device__ __forceinline__ int rest(int n) const { return n - of(n) * (int)d; }
+};
+
 struct KvAttentionArgs {
   Rows q;
   const uint8_t* cache;
@@ -78,6 +96,8 @@ struct KvAttentionArgs {
   int T, B, Hq, H, pages, page;
   float scale;
   int window, max_q;
+  // of the plan: row tiles, token ranges, tokens of a range
+  Divisor tiles, splits, chunk, group, heads;
 };
 
 // How a kv4_attention call is cut into work.

@@ -353,7 +353,7 @@ __device__ __forceinline__ void load_queries(Queries<D>& q, const KvAttentionArg
   // rows past the last repeat it; they are not stored
   const int want = row0 + (lane & (kPaired<ROWS> ? 7 : 15));
   const int row = want < sp.rows ? want : sp.rows - 1;
-  const int i = row / group;
+  const int i = a.group.of(row);
   const uint16_t* src = a.q.p + (int64_t)(sp.tok0 + i) * a.q.token +
                         (int64_t)(head * group + row - i * group) * a.q.head;
   uint32_t most = 0;
@@ -415,26 +415,33 @@ constexpr int kResident = D <= 128 || kPaired<ROWS> ? 2 : 1;
 
 template <int D, int ROWS, bool BF16>
 __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kernel(
-    KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
-    float* __restrict__ partials) {
+    KvAttentionArgs a, unsigned* __restrict__ counters, float* __restrict__ partials) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = a.Hq / a.H;
+  const int group = (int)a.group.d, splits = (int)a.splits.d;
   // Row tiles of one token range read the same codes: workgroups 8 apart, in
   // turn on the same XCD, whose L2 then holds them (3 requests of 294 rows
   // over 16600 tokens: 97 -> 74 us).
-  const int id = blockIdx.x, ranges = gridDim.x / tiles, whole = ranges & ~7;
-  const bool tail = id >= whole * tiles;
-  const int width = tail ? ranges - whole : 8, in = tail ? id - whole * tiles : id;
-  const int tile = in / width % tiles;
-  int range_id = (tail ? whole : in / (8 * tiles) * 8) + in % width;
-  const int split = range_id % splits;
-  range_id /= splits;                       // (request, head)
-  const int work = range_id * tiles + tile;
-  const int head = range_id % a.H, b = range_id / a.H;
+  int id = blockIdx.x, tile = 0;
+  const int tiles = (int)a.tiles.d;
+  if (tiles > 1) {
+    const int ranges = a.tiles.of(gridDim.x), whole = ranges & ~7;
+    if (id < whole * tiles) {
+      tile = a.tiles.rest(id >> 3);
+      id = (a.tiles.of(id >> 3) << 3) + (id & 7);
+    } else {
+      const int in = id - whole * tiles, width = ranges - whole;
+      tile = in / width;
+      id = whole + in % width;
+    }
+  }
+  const int split = a.splits.rest(id);
+  id = a.splits.of(id);                     // (request, head)
+  const int work = id * tiles + tile;
+  const int head = a.heads.rest(id), b = a.heads.of(id);
   const int row0 = tile * ROWS;
-  const Span sp = span_of(a, b, group, row0, ROWS);
+  const Span sp = span_of(a, b, row0, ROWS);
   if (row0 >= sp.rows) return;
-  const Range range = range_of(sp, split, splits, chunk);
+  const Range range = range_of(a, sp, split);
   if (split >= range.parts) return;
   // the waves divide the range
   const int each = ((range.end - range.begin + kTile - 1) / kTile + kWaves - 1) / kWaves * kTile;
@@ -452,8 +459,8 @@ __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kern
 
   // Inner tiles, which every row sees whole, need no mask.
   const int row_last = row0 + ROWS < sp.rows ? row0 + ROWS - 1 : sp.rows - 1;
-  const int pos_first = sp.len - sp.nq + row0 / group;
-  const int pos_last = sp.len - sp.nq + row_last / group;
+  const int pos_first = sp.len - sp.nq + a.group.of(row0);
+  const int pos_last = sp.len - sp.nq + a.group.of(row_last);
   const int inner_end = pos_first + 1;  // exclusive
   const int inner_begin = a.window > 0 && pos_last >= a.window ? pos_last - a.window + 1 : 0;
 
@@ -553,7 +560,7 @@ __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kern
     return x;
   };
   constexpr int kVecs = D / 4;
-  const Output out(a, sp, head, group);
+  const Output out(a, sp, head);
   if (range.parts == 1) {
     for (int v = threadIdx.x; v < rows * kVecs; v += kThreads) {
       const int row = v / kVecs, ch = v % kVecs * 4;
@@ -589,10 +596,10 @@ hipError_t launch(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
   const dim3 grid((unsigned)((int64_t)a.B * a.H * p.tiles * p.splits));
   if (dtype == W4A16_DTYPE_BF16)
     hipLaunchKernelGGL((kv_tokens_kernel<D, ROWS, true>), grid, dim3(kThreads), 0, stream, a,
-                       p.tiles, p.splits, p.chunk, counters, partials);
+                       counters, partials);
   else
     hipLaunchKernelGGL((kv_tokens_kernel<D, ROWS, false>), grid, dim3(kThreads), 0, stream, a,
-                       p.tiles, p.splits, p.chunk, counters, partials);
+                       counters, partials);
   return hipGetLastError();
 }
 
@@ -698,8 +705,14 @@ KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, i
   return plan_for(&many, 128, B, H, rows, D, keys, cus) < time ? many : few;
 }
 
-hipError_t launch_kv_attention(const KvAttentionPlan& p, const KvAttentionArgs& a, int D,
+hipError_t launch_kv_attention(const KvAttentionPlan& p, const KvAttentionArgs& args, int D,
                                int dtype, void* workspace, hipStream_t stream) {
+  KvAttentionArgs a = args;
+  a.tiles = Divisor(p.tiles);
+  a.splits = Divisor(p.splits);
+  a.chunk = Divisor(p.chunk);
+  a.group = Divisor(a.Hq / a.H);
+  a.heads = Divisor(a.H);
   unsigned* counters = static_cast<unsigned*>(workspace);
   float* partials =
       reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterHeaderBytes);

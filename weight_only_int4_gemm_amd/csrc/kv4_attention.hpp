@@ -78,7 +78,7 @@ struct Span {
 };
 
 // The tokens of a row tile.
-__device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int group, int row0,
+__device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int row0,
                                         int row_tile) {
   Span s;
   const int64_t most = (int64_t)a.max_pages * a.page;
@@ -96,10 +96,10 @@ __device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int gro
   }
   // queries beyond max_q are not computed
   const int nq = s.nq < a.max_q ? s.nq : a.max_q;
-  s.rows = nq * group;
+  s.rows = nq * (int)a.group.d;
   const int last = row0 + row_tile < s.rows ? row0 + row_tile : s.rows;
-  const int first_pos = s.len - s.nq + row0 / group;
-  const int last_pos = s.len - s.nq + (last - 1) / group;
+  const int first_pos = s.len - s.nq + a.group.of(row0);
+  const int last_pos = s.len - s.nq + a.group.of(last > 0 ? last - 1 : 0);
   s.begin = a.window > 0 && first_pos >= a.window ? first_pos - a.window + 1 : 0;
   s.begin &= ~(kTile - 1);
   s.end = last_pos + 1 > s.begin ? last_pos + 1 : s.begin;
@@ -132,12 +132,14 @@ struct Range {
   int begin, end;  // empty rows: begin == end
 };
 
-__device__ __forceinline__ Range range_of(const Span& sp, int split, int splits, int chunk) {
+__device__ __forceinline__ Range range_of(const KvAttentionArgs& a, const Span& sp,
+                                            int split) {
   Range r;
-  int per = chunk;
-  r.parts = (sp.end - sp.begin + per - 1) / per;
+  const int splits = (int)a.splits.d;
+  int per = (int)a.chunk.d;
+  r.parts = a.chunk.of(sp.end - sp.begin + per - 1);
   if (r.parts > splits) {
-    per = ((sp.end - sp.begin + splits - 1) / splits + kTile - 1) / kTile * kTile;
+    per = (a.splits.of(sp.end - sp.begin + splits - 1) + kTile - 1) / kTile * kTile;
     r.parts = (sp.end - sp.begin + per - 1) / per;
   }
   if (r.parts < 1) r.parts = 1;
@@ -151,18 +153,19 @@ struct Output {
   uint16_t* o;
   int64_t o_token, o_head;
   float* lse;
-  int tok0, head0, group, heads;  // head0: the first query head of the group
+  int tok0, head0, heads;  // head0: the first query head of the group
+  Divisor group;
 
-  __device__ __forceinline__ Output(const KvAttentionArgs& a, const Span& sp, int head, int grp)
+  __device__ __forceinline__ Output(const KvAttentionArgs& a, const Span& sp, int head)
       : o(a.o), o_token(a.o_token), o_head(a.o_head), lse(a.lse), tok0(sp.tok0),
-        head0(head * grp), group(grp), heads(a.Hq) {}
+        head0(head * (int)a.group.d), heads(a.Hq), group(a.group) {}
 
   // N (4 or 8) neighbouring channels of a row, each times inv and rounded.
   template <bool BF16, int N>
   __device__ __forceinline__ void store(int row, int ch, const float* x, float inv) const {
-    const int i = row / group;
+    const int i = group.of(row);
     uint16_t* dst = o + (int64_t)(tok0 + i) * o_token +
-                    (int64_t)(head0 + row - i * group) * o_head + ch;
+                    (int64_t)(head0 + row - i * (int)group.d) * o_head + ch;
     uint32_t w[N / 2];
 #pragma unroll
     for (int k = 0; k < N / 2; ++k) {
@@ -182,8 +185,8 @@ struct Output {
 
   __device__ __forceinline__ void store_lse(int row, float m, float l) const {
     if (!lse) return;
-    const int i = row / group;
-    lse[(int64_t)(tok0 + i) * heads + head0 + row - i * group] =
+    const int i = group.of(row);
+    lse[(int64_t)(tok0 + i) * heads + head0 + row - i * (int)group.d] =
         l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
   }
 };

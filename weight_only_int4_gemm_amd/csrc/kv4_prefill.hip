@@ -321,31 +321,30 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
 
 template <int D, bool BF16>
 __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
-    KvAttentionArgs a, int tiles, int splits, int chunk, unsigned* __restrict__ counters,
-    float* __restrict__ partials) {
+    KvAttentionArgs a, unsigned* __restrict__ counters, float* __restrict__ partials) {
   constexpr int F = D / 16, CB = D / 32, W = D / 8, M = 32 / W;
   __shared__ Stage<D> stage[2];
   __shared__ float s_top[kWaves];
   __shared__ bool s_last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5;
-  const int group = a.Hq / a.H;
+  const int group = (int)a.group.d, splits = (int)a.splits.d;
   // Heads next to each other (they go to unlike XCDs), then the row tiles of
   // a request, the last, which see the most tokens, first.  Neighbours in this
   // order are about equally long: the shader engines take workgroups in turn,
   // so requests of unlike lengths side by side would load them unevenly
   // (two requests, one three times as long: 1.21 against 0.87 ms).
   int id = blockIdx.x;
-  const int split = id % splits;
-  id /= splits;
-  const int head = id % a.H;
-  id /= a.H;
-  const int tile = tiles - 1 - id % tiles, b = id / tiles;
+  const int split = a.splits.rest(id), tiles = (int)a.tiles.d;
+  id = a.splits.of(id);
+  const int head = a.heads.rest(id);
+  id = a.heads.of(id);
+  const int tile = tiles - 1 - a.tiles.rest(id), b = a.tiles.of(id);
   const int work = (b * a.H + head) * tiles + tile;
   const int row0 = tile * kRowTile;
-  const Span sp = span_of(a, b, group, row0, kRowTile);
+  const Span sp = span_of(a, b, row0, kRowTile);
   if (row0 >= sp.rows) return;
-  const Range range = range_of(sp, split, splits, chunk);
+  const Range range = range_of(a, sp, split);
   if (split >= range.parts) return;
 
   // This wave's rows; rows past the last repeat it and are not stored.
@@ -353,7 +352,7 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
   const bool idle = wave_row0 >= sp.rows;
   const int want = wave_row0 + (lane & 31);
   const int row = want < sp.rows ? want : sp.rows - 1;
-  const int qi = row / group;
+  const int qi = a.group.of(row);
   const uint16_t* src = a.q.p + (int64_t)(sp.tok0 + qi) * a.q.token +
                         (int64_t)(head * group + row - qi * group) * a.q.head;
   const int pos = sp.len - sp.nq + qi;
@@ -457,7 +456,7 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
     }
   }
 
-  const Output out(a, sp, head, group);
+  const Output out(a, sp, head);
   const float total = s.l + __shfl_xor(s.l, 32);
   const float fixed = s.z + __shfl_xor(s.z, 32);
   // Eight neighbouring channels of word 8 k + 4 h + r of this lane's row.
@@ -510,11 +509,11 @@ hipError_t launch(const KvAttentionPlan& p, const KvAttentionArgs& a, int dtype,
   const dim3 grid((unsigned)((int64_t)a.B * a.H * p.tiles * p.splits));
   const dim3 block(kThreads);
   if (dtype == W4A16_DTYPE_BF16)
-    hipLaunchKernelGGL((kv_rows_kernel<D, true>), grid, block, 0, stream, a, p.tiles, p.splits,
-                       p.chunk, counters, partials);
+    hipLaunchKernelGGL((kv_rows_kernel<D, true>), grid, block, 0, stream, a, counters,
+                       partials);
   else
-    hipLaunchKernelGGL((kv_rows_kernel<D, false>), grid, block, 0, stream, a, p.tiles, p.splits,
-                       p.chunk, counters, partials);
+    hipLaunchKernelGGL((kv_rows_kernel<D, false>), grid, block, 0, stream, a, counters,
+                       partials);
   return hipGetLastError();
 }
 
