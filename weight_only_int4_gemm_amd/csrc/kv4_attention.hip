@@ -50,14 +50,37 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 
-// Sum and maximum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
+// Reductions without the LDS's lane exchanges (0.1 us each, one after
+// another in a workgroup's start and end).  Over the four lane groups (lanes
+// l, l ^ 16, l ^ 32, l ^ 48), by swaps of rows and halves:
+template <typename Op>
+__device__ __forceinline__ float over_groups(float x, Op op) {
+  const uint32_t w = __builtin_bit_cast(uint32_t, x);
+  const auto rows = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  x = op(__builtin_bit_cast(float, (uint32_t)rows[0]), __builtin_bit_cast(float, (uint32_t)rows[1]));
+  const uint32_t v = __builtin_bit_cast(uint32_t, x);
+  const auto halves = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return op(__builtin_bit_cast(float, (uint32_t)halves[0]),
+            __builtin_bit_cast(float, (uint32_t)halves[1]));
+}
 __device__ __forceinline__ float groups_sum(float x) {
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
+  return over_groups(x, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float groups_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+  return over_groups(x, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// Over the 16 columns of a lane group.
+template <int CTRL>
+__device__ __forceinline__ float other_column(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float columns_max(float x) {
+  x = fmaxf(x, other_column<0xb1>(x));    // quad_perm 1 0 3 2
+  x = fmaxf(x, other_column<0x4e>(x));    // quad_perm 2 3 0 1
+  x = fmaxf(x, other_column<0x141>(x));   // row_half_mirror
+  return fmaxf(x, other_column<0x140>(x));  // row_mirror
 }
 
 // With at most eight rows, columns n and n + 8 are the same row.  The two
@@ -366,15 +389,15 @@ __device__ __forceinline__ void load_queries(Queries<D>& q, const KvAttentionArg
     for (int c = 0; c < 16; ++c)
       most = max(most, __builtin_bit_cast(uint32_t, element(p, c)) & 0x7fffffffu);
   }
-  most = max(most, (uint32_t)__shfl_xor((int)most, 16));
-  most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-  // the largest magnitude of the rows that are finite
-  float top = most < 0x7f800000u ? __builtin_bit_cast(float, most) : 0.f;
+  // the largest magnitude of the rows that are finite: as numbers, infinities
+  // and NaN taken for infinity
+  float top = groups_max(
+      __builtin_bit_cast(float, most < 0x7f800000u ? most : 0x7f800000u));
+  top = top < __builtin_inff() ? top : 0.f;
   const int pos = sp.len - sp.nq + i;
   q.hi = pos;
   q.lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-#pragma unroll
-  for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+  top = columns_max(top);
   // The wave's rows are brought near FP16's upper end by one power of two:
   // every score keeps 2^-30 of the largest one among them, however small the
   // queries (the odd channels are divided by 16, which FP16's smallest step
