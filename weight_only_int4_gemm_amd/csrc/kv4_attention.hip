@@ -688,7 +688,7 @@ double plan_for(KvAttentionPlan* p, int row_tile, int B, int H, int64_t rows, in
   if (most < 1 || work > kMaxSplitTiles) most = 1;
   double best = 0;
   int64_t n = 1;
-  for (int64_t i = 1; i <= most; ++i) {
+  for (int64_t i = 1; i <= most; i += 1 + i / 32) {
     const int64_t each = ((steps + i - 1) / i + sharing - 1) / sharing;
     const bool both = second && work * i > cus;
     const double load = (double)(work * i) / (both ? 2 * cus : cus);
