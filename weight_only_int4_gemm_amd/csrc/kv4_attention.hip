@@ -664,7 +664,7 @@ constexpr int64_t kMostPartBytes = ((int64_t)192 << 20) - (int64_t)kCounterHeade
 // with one.)
 double plan_for(KvAttentionPlan* p, int row_tile, int B, int H, int64_t rows, int D,
                 int64_t keys, int cus) {
-  constexpr double kStart = 5, kJoin = 1.2, kPartsRate = 1e6, kJoinRate = 64e3;  // bytes per us
+  constexpr double kStart = 5, kJoin = 1.4, kPartsRate = 1e6, kJoinRate = 64e3;  // bytes per us
   constexpr double kUneven = 0.35, kAverage = 0.65;
   p->row_tile = row_tile;
   p->rows = row_tile == 128;
