@@ -142,6 +142,75 @@ def test_attention_through_every_kernel(dtype, case):
     assert (np.abs(got[~empty] - lse[~empty]) <= tol).all()
 
 
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_what_no_query_sees_reaches_no_result(case):
+    """NaN in every place that is masked for all queries, in either kernel,
+    changes no bit; nor does a workspace another plan has used."""
+    import torch
+    D, Hq, H, page, lens, new, window, (max_q, max_len), kernel, ranges = CASES[case]
+    say("attention masked", *CASES[case])
+    rng = np.random.default_rng(300 + case)
+    q, cache, table, starts = _inputs(rng, lens, new, page, Hq, H, D, "float16")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = (torch.tensor(table, **i32), torch.tensor(lens, **i32), torch.tensor(starts, **i32))
+    nbytes = max(w4.kv4_attention_workspace_bytes(len(lens), Hq, H, D, mq, ml, window)
+                 for mq, ml in ((max_q, max_len), (max(new), max(lens) + 1)))
+    ws = torch.zeros(nbytes + 16, dtype=torch.uint8, device="cuda")
+
+    def run(mq, ml):
+        O, L = torch.full_like(q, 9.0), torch.full(q.shape[:2], 9.0, device="cuda")
+        w4.kv4_attention(q, cache, *args, O, L, D ** -0.5, window, mq, ml, ws)
+        torch.cuda.synchronize()
+        return O, L
+
+    before = run(max_q, max_len)
+    other = run(max(new), max(lens) + 1)            # the plan of the sizes as they are
+    seen = np.zeros(cache.shape[0] * page, bool)
+    for b, n in enumerate(lens):
+        first = max(0, n - new[b] - window + 1) if window else 0
+        j = np.arange(first, n)
+        if new[b]:
+            seen[table[b, j // page].astype(np.int64) * page + j % page] = True
+    bad = torch.from_numpy(np.flatnonzero(~seen).astype(np.int32)).cuda()
+    assert bad.numel() > 0
+    K = torch.full((bad.numel(), H, D), float("nan"), dtype=torch.float16, device="cuda")
+    w4.kv4_append(K, K, bad, cache)
+    for then, now in zip((*before, *other), (*run(max_q, max_len), *run(max(new), max(lens) + 1))):
+        assert torch.isfinite(then.float()).all() or (lens[-1] < new[-1])
+        assert torch.equal(then, now)
+
+
+@pytest.mark.parametrize("case", [i for i, c in enumerate(CASES) if max(c[5]) > 1])
+def test_a_stored_nan_stays_with_the_queries_that_see_it(case):
+    """The last token of every request that has several queries is NaN: its
+    last query is, the others are within the reference's bounds as before."""
+    import torch
+    D, Hq, H, page, lens, new, window, (max_q, max_len), kernel, ranges = CASES[case]
+    say("attention nan", *CASES[case])
+    rng = np.random.default_rng(400 + case)
+    q, cache, table, starts = _inputs(rng, lens, new, page, Hq, H, D, "bfloat16")
+    scale, n = D ** -0.5, max(lens)
+    want, lse, weight, size, floor, reach = _reference(q, cache, table, lens, starts, scale, window)
+    last = [b for b in range(len(lens)) if new[b] > 1 and lens[b] >= 1]
+    slots = torch.tensor([int(table[b, (lens[b] - 1) // page]) * page + (lens[b] - 1) % page
+                          for b in last], dtype=torch.int32, device="cuda")
+    K = torch.full((len(last), H, D), float("nan"), dtype=torch.float16, device="cuda")
+    w4.kv4_append(K, K, slots, cache)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    O, L = torch.full_like(q, 9.0), torch.full(q.shape[:2], 9.0, device="cuda")
+    w4.kv4_attention(q, cache, torch.tensor(table, **i32), torch.tensor(lens, **i32),
+                     torch.tensor(starts, **i32), O, L, scale, window, max_q, max_len,
+                     w4.alloc_kv4_workspace(len(lens), Hq, H, D, max_q, max_len, window))
+    torch.cuda.synchronize()
+    got = O.double().cpu().numpy()
+    hit = [int(starts[b + 1]) - 1 for b in last]
+    assert np.isnan(got[hit]).all() and np.isnan(L.cpu().numpy()[hit]).all()
+    rest = np.setdiff1d(np.arange(q.shape[0]), hit)
+    bound = (2.0 ** -8 * np.abs(want) + 2.0 ** -25 * (1 + floor) + 2.0 ** -11 * weight
+             + (16 * U * reach[..., None] + (64 + n / 32) * U) * size)
+    assert (np.abs(got - want) <= bound)[rest].all()
+
+
 def test_the_cases_reach_what_they_name():
     """On the device they were chosen for."""
     import torch
