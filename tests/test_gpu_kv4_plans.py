@@ -211,6 +211,58 @@ def test_a_stored_nan_stays_with_the_queries_that_see_it(case):
     assert (np.abs(got - want) <= bound)[rest].all()
 
 
+@pytest.mark.parametrize("queries,planned", [(1, 1), (5, 5), (40, 2048)])
+@pytest.mark.parametrize("kind", range(5))
+def test_attention_of_values_of_every_size(kind, queries, planned):
+    """8 heads on one, so 8, 40 and 320 rows: each kernel.  Value scales over
+    FP16's whole range in one sequence, rising and falling; constant values
+    (scale 0); one key that takes all the weight; BF16 queries of any size."""
+    import torch
+    rng = np.random.default_rng(500 + kind)
+    page, H, Hq, D, n = 16, 1, 8, 128, 700
+    pages = -(-n // page)
+    table = np.arange(pages, dtype=np.int32)[None]
+    k = rng.standard_normal((n, H, D)).astype(np.float32)
+    v = rng.standard_normal((n, H, D)).astype(np.float32)
+    qs = rng.standard_normal((queries, Hq, D)).astype(np.float32)
+    if kind == 0:
+        v *= np.exp2(np.linspace(-20, 12, n))[:, None, None].astype(np.float32)
+    elif kind == 1:
+        v *= np.exp2(np.linspace(12, -20, n))[:, None, None].astype(np.float32)
+    elif kind == 2:
+        v[::2] = 0.75
+        v[:64] = 0
+    elif kind == 3:
+        k[401] = 4 * qs[0, 0]
+    else:
+        qs *= np.exp2(np.array([-120.0, -40, 3, 0, -7, -1, 2, -80]))[None, :, None]
+    dtype = "bfloat16" if kind == 4 else "float16"
+    max_len = 6000 if planned > queries else n
+    text = w4.kv4_attention_describe(1, Hq, H, D, planned, max_len, 0, CUS)
+    say("attention sizes", kind, queries, text)
+    assert f"<128,{8 if queries == 1 else 16 if queries == 5 else 128}," in text
+    cache = torch.empty((pages, H, page, D + 8), dtype=torch.uint8, device="cuda")
+    K, V = (torch.from_numpy(x).half().cuda() for x in (k, v))
+    w4.kv4_append(K, V, torch.arange(n, dtype=torch.int32, device="cuda"), cache)
+    q = torch.from_numpy(qs.astype(np.float32)).to(getattr(torch, dtype)).cuda()
+    starts, i32 = np.array([0, queries]), dict(dtype=torch.int32, device="cuda")
+    O, L = torch.full_like(q, 9.0), torch.full(q.shape[:2], 9.0, device="cuda")
+    w4.kv4_attention(q, cache, torch.tensor(table, **i32), torch.tensor([n], **i32),
+                     torch.tensor(starts, **i32), O, L, 0.5, 0, planned, max_len,
+                     w4.alloc_kv4_workspace(1, Hq, H, D, planned, max_len))
+    torch.cuda.synchronize()
+    want, lse, weight, size, floor, reach = _reference(q, cache, table, [n], starts, 0.5, 0)
+    # scores are summed among those of a workgroup: 2^-30 of the largest
+    reach = np.maximum(reach, 2.0 ** -6 * reach.max())
+    step = 2.0 ** -11 if dtype == "bfloat16" else 2.0 ** -21
+    bound = (torch.finfo(q.dtype).eps / 2 * np.abs(want) + 2.0 ** -25 * (1 + floor)
+             + step * weight + (16 * U * reach[..., None] + (64 + n / 32) * U) * size)
+    err = np.abs(O.double().cpu().numpy() - want)
+    assert (err <= bound).all(), float((err / bound).max())
+    tol = 8 * U * reach + 64 * U * (1 + np.abs(lse))
+    assert (np.abs(L.double().cpu().numpy() - lse) <= tol).all()
+
+
 def test_the_cases_reach_what_they_name():
     """On the device they were chosen for."""
     import torch
