@@ -280,3 +280,39 @@ def test_the_cases_reach_what_they_name():
         seen.add((D, text.split(",")[1], split))
     for D in (64, 128, 256):
         assert (D, "128", True) in seen and {r for d, r, _ in seen if d == D} >= {"8", "16", "128"}
+
+
+@pytest.mark.parametrize("queries,planned", [(1, 1), (5, 5), (40, 2048)])
+@pytest.mark.parametrize("power", [9, 12, 30, 60])
+def test_a_large_query_costs_its_neighbours_nothing(queries, planned, power):
+    """Every third row 2^power as large as the others: those keep the bounds
+    that follow from their own size."""
+    import torch
+    rng = np.random.default_rng(600 + power)
+    page, H, Hq, D, n = 32, 1, 8, 128, 300
+    pages = -(-n // page)
+    table = np.arange(pages, dtype=np.int32)[None]
+    max_len = 6000 if planned > queries else n
+    say("attention neighbours", queries, power)
+    k, v = rng.standard_normal((2, n, H, D)).astype(np.float32)
+    cache = torch.empty((pages, H, page, D + 8), dtype=torch.uint8, device="cuda")
+    K, V = (torch.from_numpy(x).half().cuda() for x in (k, v))
+    w4.kv4_append(K, V, torch.arange(n, dtype=torch.int32, device="cuda"), cache)
+    qs = rng.standard_normal((queries * Hq, D)).astype(np.float32)
+    qs[::3] *= 2.0 ** power
+    q = torch.from_numpy(qs.reshape(queries, Hq, D)).bfloat16().cuda()
+    starts, i32 = np.array([0, queries]), dict(dtype=torch.int32, device="cuda")
+    O, L = torch.full_like(q, 9.0), torch.full(q.shape[:2], 9.0, device="cuda")
+    w4.kv4_attention(q, cache, torch.tensor(table, **i32), torch.tensor([n], **i32),
+                     torch.tensor(starts, **i32), O, L, D ** -0.5, 0, planned, max_len,
+                     w4.alloc_kv4_workspace(1, Hq, H, D, planned, max_len))
+    torch.cuda.synchronize()
+    want, lse, weight, size, floor, reach = _reference(q, cache, table, [n], starts, D ** -0.5, 0)
+    small = np.arange(queries * Hq).reshape(queries, Hq) % 3 != 0
+    bound = (2.0 ** -8 * np.abs(want) + 2.0 ** -25 * (1 + floor) + 2.0 ** -11 * weight
+             + (16 * U * reach[..., None] + (64 + n / 32) * U) * size)
+    err = np.abs(O.double().cpu().numpy() - want)
+    assert np.isfinite(O.float().cpu().numpy()).all()
+    assert (err <= bound)[small].all(), float((err / bound)[small].max())
+    got = L.double().cpu().numpy()
+    assert (np.abs(got - lse) <= 8 * U * reach + 64 * U * (1 + np.abs(lse)))[small].all()

@@ -70,19 +70,6 @@ __device__ __forceinline__ float groups_max(float x) {
   return over_groups(x, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// Over the 16 columns of a lane group.
-template <int CTRL>
-__device__ __forceinline__ float other_column(float x) {
-  return __builtin_bit_cast(
-      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float columns_max(float x) {
-  x = fmaxf(x, other_column<0xb1>(x));    // quad_perm 1 0 3 2
-  x = fmaxf(x, other_column<0x4e>(x));    // quad_perm 2 3 0 1
-  x = fmaxf(x, other_column<0x141>(x));   // row_half_mirror
-  return fmaxf(x, other_column<0x140>(x));  // row_mirror
-}
-
 // With at most eight rows, columns n and n + 8 are the same row.  The two
 // lanes then divide the softmax (one takes the first unit's tokens, the other
 // the second's), and FP16's two products with the values become one: columns
@@ -254,10 +241,14 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
     return __builtin_fmaf(scale[i], raw[i >> 2][i & 3],
                           __builtin_fmaf(high_half(key_params(i)), q.sum, -m));
   };
-  auto weigh = [&](float m) {
+  // `again`: m has just moved to where every weight fits; logits so large
+  // that their rounding says otherwise are held to it.
+  auto weigh = [&](float m, bool again) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      p[i] = exp2_hw(logit(i, m));
+      float x = logit(i, m);
+      if (again) x = held(x, apart(value_params(i)));
+      p[i] = exp2_hw(x);
       w[i] = times_low_half(p[i], value_params(i));
     }
     if (edge) {
@@ -275,7 +266,7 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
 #pragma unroll
     for (int i = 0; i < N; i += 2) most = fmaxf(fmaxf(most, w[i]), w[i + 1]);
   };
-  weigh(s.m);
+  weigh(s.m, false);
   if (__any(most > kMostWeight || sum > kMostSum)) {
     // Move the reference: the largest weight becomes 2^8, unless that lets
     // a probability exceed 2^40 (values of scale 0).
@@ -298,7 +289,7 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
     s.w *= f;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) s.acc[c] *= f;
-    weigh(m);
+    weigh(m, true);
   }
   s.l += sum;
   if (edge) {
@@ -389,19 +380,17 @@ __device__ __forceinline__ void load_queries(Queries<D>& q, const KvAttentionArg
     for (int c = 0; c < 16; ++c)
       most = max(most, __builtin_bit_cast(uint32_t, element(p, c)) & 0x7fffffffu);
   }
-  // the largest magnitude of the rows that are finite: as numbers, infinities
-  // and NaN taken for infinity
+  // the row's largest magnitude, 0 with an infinity or a NaN
   float top = groups_max(
       __builtin_bit_cast(float, most < 0x7f800000u ? most : 0x7f800000u));
   top = top < __builtin_inff() ? top : 0.f;
   const int pos = sp.len - sp.nq + i;
   q.hi = pos;
   q.lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-  top = columns_max(top);
-  // The wave's rows are brought near FP16's upper end by one power of two:
-  // every score keeps 2^-30 of the largest one among them, however small the
-  // queries (the odd channels are divided by 16, which FP16's smallest step
-  // would otherwise cut into).
+  // Every row is brought near FP16's upper end by a power of two of its own:
+  // a score keeps 2^-30 of the largest one its row could have, however small
+  // the queries (the odd channels are divided by 16, which FP16's smallest
+  // step would otherwise cut into).
   int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
   e = e < -100 ? -100 : e;
   const float up = __builtin_bit_cast(float, (uint32_t)(127 + 13 - e) << 23);

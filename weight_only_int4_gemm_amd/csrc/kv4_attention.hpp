@@ -69,6 +69,15 @@ __device__ __forceinline__ uint32_t apart(uint32_t w) {
   return w;
 }
 
+// A logit less its moved reference, at most what the move provides for:
+// weights 2^kTopWeight (one more for rounding), probabilities 2^kSumHeadroom.
+// A NaN stays one.
+__device__ __forceinline__ float held(float x, uint32_t value_params) {
+  const float most =
+      fminf(kTopWeight - __builtin_amdgcn_logf(low_half(value_params)), kSumHeadroom) + 1.f;
+  return x > most ? most : x;
+}
+
 // Query rows of a workgroup and the tokens they see.
 struct Span {
   int len, nq, tok0;    // tokens held, queries, first query row of the request

@@ -208,7 +208,9 @@ __device__ __forceinline__ float16v scores(const Stage<D>& st, int tile, const u
 // The probabilities of a tile under reference m: packed weights, and their
 // sums.  Parameters are read as they are used, four tokens at a time.  EDGE:
 // some token is not seen by some row; what the cache holds for it may be
-// anything, so it is taken out, not multiplied by zero.
+// anything, so it is taken out, not multiplied by zero.  (Rows of very unlike
+// sizes go this way too, with `back`, so that it costs the usual way nothing.)
+// AGAIN: after the reference has moved.
 template <bool BF16>
 struct Weights {
   uint4v w[2];                   // [unit]
@@ -217,15 +219,16 @@ struct Weights {
   bool over;                     // out of the reference's range
 };
 
-template <int D, bool BF16, bool EDGE>
+template <int D, bool BF16, bool EDGE, bool AGAIN = false>
 __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int tile,
-                                      const float16v& raw, float sum_q, float m, uint32_t there,
-                                      int t, int lo, int hi) {
+                                      const float16v& raw, float sum_q, float back, float m,
+                                      uint32_t there, int t, int lo, int hi) {
   const int h = (threadIdx.x & 63) >> 5;
-  // known here only: the usual path must not compute any of the masks
+  // known here only: the usual path must not compute masks or products
   if constexpr (EDGE) {
     t = (int)apart(t);
     there = apart(there);
+    back = __builtin_bit_cast(float, apart(__builtin_bit_cast(uint32_t, back)));
   }
   const _Float16 kMostHalf = (_Float16)kMostWeight;  // what is larger rounds to it, or to infinity
   half2v most;
@@ -239,8 +242,10 @@ __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int 
     float w[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      float p = exp2_hw(
-          __builtin_fmaf(ks[r], raw[4 * a + r], __builtin_fmaf(kz[r], sum_q, -m)));
+      const float product = EDGE ? raw[4 * a + r] * back : raw[4 * a + r];
+      float x = __builtin_fmaf(ks[r], product, __builtin_fmaf(kz[r], sum_q, -m));
+      if constexpr (AGAIN) x = held(x, vp[r]);
+      float p = exp2_hw(x);
       w[r] = times_low_half(p, vp[r]);
       float z = high_half(vp[r]);
       if constexpr (EDGE) {
@@ -269,20 +274,21 @@ __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int 
 
 template <int D, bool BF16>
 __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const uint4v* q,
-                                            float sum_q, RowSums<D>& s, uint32_t there, int t,
-                                            bool edge, int lo, int hi) {
+                                            float sum_q, float back, RowSums<D>& s,
+                                            uint32_t there, int t, bool edge, int lo, int hi) {
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const float16v raw = scores<D>(st, tile, q);
   Weights<BF16> o;
   if (edge)
-    weigh<D, BF16, true>(o, st, tile, raw, sum_q, s.m, there, t, lo, hi);
+    weigh<D, BF16, true>(o, st, tile, raw, sum_q, back, s.m, there, t, lo, hi);
   else
-    weigh<D, BF16, false>(o, st, tile, raw, sum_q, s.m, there, t, lo, hi);
+    weigh<D, BF16, false>(o, st, tile, raw, sum_q, back, s.m, there, t, lo, hi);
   if (__any(o.over)) {
     // Move the reference, as the other kernel does.
     float top = kNone;
     const int t1 = (int)apart(t);
     const uint32_t there1 = apart(there);
+    const float back1 = __builtin_bit_cast(float, apart(__builtin_bit_cast(uint32_t, back)));
 #pragma unroll 1
     for (int a = 0; a < 4; ++a) {
       const int at = 8 * a + 4 * h;
@@ -290,7 +296,7 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
       for (int r = 0; r < 4; ++r) {
         const int j = t1 + at + r, i = 32 * tile + at + r;
         const float got = a == 0 ? raw[r] : a == 1 ? raw[4 + r] : a == 2 ? raw[8 + r] : raw[12 + r];
-        const float x = st.ks[i] * got + st.kz[i] * sum_q;
+        const float x = st.ks[i] * (got * back1) + st.kz[i] * sum_q;
         const bool seen = (there1 >> (at + r) & 1) && j >= lo && j <= hi;
         const float y = fmaxf(x + __builtin_amdgcn_logf(low_half(st.vp[i])) - kTopWeight,
                               x - kSumHeadroom);
@@ -305,7 +311,7 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
     s.z *= f;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) s.acc[c] *= f;
-    weigh<D, BF16, true>(o, st, tile, raw, sum_q, s.m, there, t, lo, hi);
+    weigh<D, BF16, true, true>(o, st, tile, raw, sum_q, back, s.m, there, t, lo, hi);
   }
   s.l += o.sum;
   s.z += o.z;
@@ -324,7 +330,7 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
     KvAttentionArgs a, unsigned* __restrict__ counters, float* __restrict__ partials) {
   constexpr int F = D / 16, CB = D / 32, W = D / 8, M = 32 / W;
   __shared__ Stage<D> stage[2];
-  __shared__ float s_top[kWaves];
+  __shared__ float s_top[kWaves], s_low[kWaves];
   __shared__ bool s_last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5;
@@ -376,10 +382,13 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
   }
 
   // Queries as operands: 16-bit floats times one power of two that brings the
-  // workgroup's largest finite row near FP16's upper end (as the other
-  // kernel's, per workgroup: the keys' scales are stored in logits).
+  // workgroup's largest finite row near FP16's upper end; the keys' scales
+  // are stored in logits with it.  Rows that would lose bits by that, 2^-10
+  // of the largest or smaller, are rare: then (`wide`) every row has a power
+  // of its own, and its products are brought back by it.
   uint4v q[F];
-  float sum_q = 0.f, unit;
+  float sum_q = 0.f, unit, back = 1.f;
+  bool wide;
   {
     uint4v raw[F];
     uint32_t most = 0;
@@ -398,16 +407,33 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
     }
     most = max(most, (uint32_t)__shfl_xor((int)most, 32));
     float top = most < 0x7f800000u ? __builtin_bit_cast(float, most) : 0.f;
+    auto exponent = [](float x) {
+      const int e = (int)(__builtin_bit_cast(uint32_t, x) >> 23) - 127;
+      return e < -100 ? -100 : e;
+    };
+    auto power = [](int e) { return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23); };
+    const float mine = top;
+    float low = top > 0.f ? top : __builtin_inff();
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-    if (lane == 0) s_top[wave] = top;
+    for (int d = 1; d < 32; d *= 2) {
+      top = fmaxf(top, __shfl_xor(top, d));
+      low = fminf(low, __shfl_xor(low, d));
+    }
+    if (lane == 0) {
+      s_top[wave] = top;
+      s_low[wave] = low;
+    }
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_top[w]);
-    int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
-    e = e < -100 ? -100 : e;
-    const float up = __builtin_bit_cast(float, (uint32_t)(127 + 13 - e) << 23);
-    unit = a.scale * kLog2e * __builtin_bit_cast(float, (uint32_t)(127 - 13 + e) << 23);
+    for (int w = 0; w < kWaves; ++w) {
+      top = fmaxf(top, s_top[w]);
+      low = fminf(low, s_low[w]);
+    }
+    wide = __builtin_amdgcn_readfirstlane(low < top * 0x1p-10f);
+    const int e = exponent(wide ? mine : top);
+    const float up = power(13 - e);
+    unit = a.scale * kLog2e * power(wide ? -13 : e - 13);
+    if (wide) back = power(e);
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       _Float16 x[8];
@@ -422,7 +448,7 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
       q[f] = __builtin_bit_cast(uint4v, v);
     }
     sum_q += __shfl_xor(sum_q, 32);
-    sum_q *= unit;
+    sum_q *= unit * back;
   }
 
   RowSums<D> s;
@@ -445,8 +471,8 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
         // tiles beyond the range belong to the next workgroup, or to none
         if (idle || t >= range.end || t > pos_last || t + kTile <= lo_first) continue;
         const uint32_t there = st.there[2 * k] | (uint32_t)st.there[2 * k + 1] << 16;
-        const bool edge = t < lo_last || t + kTile > pos_first + 1 || there != 0xffffffffu;
-        attend_rows<D, BF16>(st, k, q, sum_q, s, there, t, edge, lo, pos);
+        const bool edge = t < lo_last || t + kTile > pos_first + 1 || there != 0xffffffffu || wide;
+        attend_rows<D, BF16>(st, k, q, sum_q, back, s, there, t, edge, lo, pos);
       }
       if (n + 1 < steps) {
         pr.unpack(stage[(n + 1) & 1], unit);
