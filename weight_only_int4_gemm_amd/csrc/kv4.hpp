@@ -64,6 +64,7 @@ struct KvTablesArgs {
   const int32_t* state;
   int32_t *lens_out, *state_out, *q_start, *slots, *positions;
   int capacity, B, page;
+  int token_groups;  // workgroups that take tokens; the others take pages
 };
 
 // Division of 0 <= n < 2^31 by a number the host knows: with 2^(s-1) < d <=

@@ -180,7 +180,7 @@ int kv4_tables(const int32_t* lens, const int32_t* want, int32_t* table, int max
     }
   if (current_cus(nullptr) <= 0) return W4A16_ERR_DEVICE;
   KvTablesArgs a{lens, want, table, max_pages, ring, pages, state, lens_out, state_out, q_start,
-                 slots, positions, capacity, B, page};
+                 slots, positions, capacity, B, page, 0};
   return done(launch_kv_tables(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -8,11 +8,14 @@
 // each other.  Every workgroup therefore makes the (small) prefix sums for
 // itself in LDS, beside what it needs of each request, and then takes its
 // share of the tokens and pages.  lens_out and state_out may be lens and
-// state: the last workgroup to finish, counted in state_out[3], writes them.
+// state: then the last workgroup to finish, counted in state_out[3], writes
+// them.
 //
 // What bounds it: latency alone.  The launch, the trip for the lengths, the
-// scan, a binary search in LDS, the trip for the page, the arrival.  256
-// requests of one token: 5.5 us; 1000 with 62 thousand tokens: 11.7 us.
+// scan, a binary search in LDS, the trip for the page, in place the arrival.
+// 256 requests of one token: 4.3 us (5.1 in place); 1000 with 62 thousand tokens: 8.4 us (11.7
+// with one kind of workgroup for tokens and pages, one after another, and an
+// arrival whatever the outputs).
 #include "../../include/w4a16_kv4.h"
 #include "kv4.hpp"
 
@@ -132,7 +135,9 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
 #pragma unroll
   for (int s = 0; s < 3; ++s) {
     int base = 0;
-    for (int w = 0; w < wave; ++w) base = add_up_to(base, wave_sum[s][w], most[s]);
+#pragma unroll
+    for (int w = 0; w < THREADS / 64 - 1; ++w)  // (all read at once)
+      base = add_up_to(base, w < wave ? wave_sum[s][w] : 0, most[s]);
     int x = add_up_to(base, before[s], most[s]);
     int* const sums = s == 0 ? tok : s == 1 ? need : back;
     for (int b = b0; b < b1; ++b) {
@@ -144,11 +149,16 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
   __syncthreads();
 
   const int tokens = tok[a.B], wanted = need[a.B], returned = back[a.B];
-  const int stride = gridDim.x * THREADS;
-  const int first = blockIdx.x * THREADS + tid;
+  // A workgroup alone does everything (in place that spares the arrival); of
+  // several the last ones do the pages, beside the tokens of the others.
+  const int page_groups = gridDim.x - a.token_groups;
+  const bool pages_only = (int)blockIdx.x >= a.token_groups;
+  const bool tokens_only = page_groups > 0 && !pages_only;
+  const int stride = (pages_only ? page_groups : a.token_groups) * THREADS;
+  const int first = ((int)blockIdx.x - (pages_only ? a.token_groups : 0)) * THREADS + tid;
 
   // pages taken: request b's j-th new page is the ring's (need[b] + j)-th
-  const int take = wanted < count ? wanted : count;
+  const int take = tokens_only ? 0 : wanted < count ? wanted : count;
   for (int i = first; i < take; i += stride) {
     const int b = owner(need, a.B, i);
     if (!served(false, need[b], need[b + 1], count)) continue;  // over wants none
@@ -156,13 +166,13 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
     a.table[(int64_t)b * a.max_pages + col] = a.ring[(head + (unsigned)i) % P];
   }
   // pages given back, to the tail: the last of the request's row
-  for (int i = first; i < returned; i += stride) {
+  for (int i = first; i < (tokens_only ? 0 : returned); i += stride) {
     const int b = owner(back, a.B, i);
     const int col = pages_of(held[b]) - (back[b + 1] - i);
     a.ring[(head + (unsigned)count + (unsigned)i) % P] =
         a.table[(int64_t)b * a.max_pages + col];
   }
-  for (int t = first; t < a.capacity; t += stride) {
+  for (int t = first; t < (pages_only ? 0 : a.capacity); t += stride) {
     int slot = -1, pos = 0;
     if (t < tokens) {
       const int b = owner(tok, a.B, t);
@@ -181,10 +191,15 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
     a.slots[t] = slot;
     a.positions[t] = pos;
   }
-  for (int b = first; b <= a.B; b += stride) a.q_start[b] = tok[b];
+  if (!tokens_only)
+    for (int b = first; b <= a.B; b += stride) a.q_start[b] = tok[b];
 
-  // The last workgroup writes what others may still have been reading.
-  if (gridDim.x > 1) {
+  // In place, the last workgroup writes what others may still have been
+  // reading; otherwise one writes at once.
+  const bool in_place = a.lens_out == a.lens || a.state_out == a.state;
+  if (!in_place) {
+    if (blockIdx.x != gridDim.x - 1) return;
+  } else if (gridDim.x > 1) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     if (tid == 0)
@@ -215,10 +230,17 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
 }
 
 template <int THREADS>
-hipError_t launch(const KvTablesArgs& a, hipStream_t stream) {
+hipError_t launch(const KvTablesArgs& args, hipStream_t stream) {
+  KvTablesArgs a = args;
   int64_t groups = ((int64_t)a.capacity + THREADS - 1) / THREADS;
   if (groups < 1) groups = 1;
   if (groups > kMaxGroups) groups = kMaxGroups;
+  a.token_groups = (int)groups;
+  if (groups > 1 || (a.lens_out != a.lens && a.state_out != a.state)) {
+    // as many as there are pages to take, and one page a request to return
+    int64_t pages = ((int64_t)a.capacity / a.page + 2 * a.B + THREADS - 1) / THREADS;
+    groups += pages < 1 ? 1 : pages > kMaxGroups ? kMaxGroups : pages;
+  }
   const size_t lds = (4 * (size_t)a.B + 3) * sizeof(int);
   if (lds > kDefaultLds) {
     const hipError_t e = hipFuncSetAttribute(
@@ -236,7 +258,7 @@ hipError_t launch(const KvTablesArgs& a, hipStream_t stream) {
 hipError_t launch_kv_tables(const KvTablesArgs& a, hipStream_t stream) {
   // A token per thread (pages are fewer).  Large workgroups scan many
   // requests in fewer steps, and fewer of them arrive at the end: 1000
-  // requests with 62 thousand tokens take 11.7 us with 1024 threads each, 17
+  // requests with 62 thousand tokens took 11.7 us with 1024 threads each, 17
   // with 256.  A decode step of 256 requests fits one small workgroup.
   return a.B <= 256 && a.capacity <= 1024 ? launch<256>(a, stream) : launch<1024>(a, stream);
 }
