@@ -10,7 +10,10 @@
 // Codes as operands.  Four bits c in the mantissa of an FP16 whose other bits
 // are zero are the subnormal c 2^-24 (16 c 2^-24 when they sit one nibble
 // higher); the matrix instruction takes subnormals exactly.  One AND per two
-// codes is then the whole unpacking.
+// codes is then the whole unpacking.  The sums, though, are cut off relative
+// to what the operands' exponents allow, and leading zeros of a subnormal
+// count there: keys, whose products are the logits, are moved to the top of
+// the mantissa (one more shift per word; the logits' error is a third).
 //
 // Layout.  The keys are the first operand (rows = 16 tokens), the queries the
 // second (columns = 16 query rows), so lane l holds scores of column l % 16
@@ -204,24 +207,35 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
   const bool upper = PAIRED && (lane & 8);
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
-  float4v raw[2];
+  // The matrix unit cuts off low bits at every addition: sums from zero, of
+  // few products, and -8 sum q added after them, keep a third less error in
+  // the logits than one sum that starts with it.
+  constexpr bool TWO = D > 64;
+  float4v raw[2], odd[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    raw[u] = float4v{q.sum8, q.sum8, q.sum8, q.sum8};
+    raw[u] = odd[u] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int p = 0; p < D / 64; ++p) {
       const uint32_t w0 = d.k[u][2 * p], w1 = d.k[u][2 * p + 1];
-      const uint4v e = {w0 & kLow, w1 & kLow, (w0 >> 8) & kLow, (w1 >> 8) & kLow};
-      const uint4v o = {w0 & kHigh, w1 & kHigh, (w0 >> 8) & kHigh, (w1 >> 8) & kHigh};
+      const uint32_t a0 = w0 << 2, a1 = w1 << 2, b0 = w0 >> 6, b1 = w1 >> 6;
+      const uint4v e = {a0 & kKeyLow, a1 & kKeyLow, b0 & kKeyLow, b1 & kKeyLow};
+      const uint4v o = {a0 & kKeyHigh, a1 & kKeyHigh, b0 & kKeyHigh, b1 & kKeyHigh};
       raw[u] = mfma(e, q.even[p], raw[u]);
-      raw[u] = mfma(o, q.odd[p], raw[u]);
+      if constexpr (TWO) odd[u] = mfma(o, q.odd[p], odd[u]);
+      else raw[u] = mfma(o, q.odd[p], raw[u]);
     }
   }
 
   if constexpr (PAIRED) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[0][i] = upper ? raw[1][i] : raw[0][i];
+    for (int i = 0; i < 4; ++i) {
+      raw[0][i] = upper ? raw[1][i] : raw[0][i];
+      if constexpr (TWO) odd[0][i] = upper ? odd[1][i] : odd[0][i];
+    }
   }
+#pragma unroll
+  for (int u = 0; u < N / 4; ++u) raw[u] = (TWO ? raw[u] + odd[u] : raw[u]) + q.sum8;
   auto key_params = [&](int i) { return d.kp[i >> 2][i & 3]; };
   auto value_params = [&](int i) { return d.vp[i >> 2][i & 3]; };
   float scale[N];  // of the keys, times the logits' unit
@@ -396,7 +410,7 @@ __device__ __forceinline__ void load_queries(Queries<D>& q, const KvAttentionArg
   const float up = __builtin_bit_cast(float, (uint32_t)(127 + 13 - e) << 23);
   const float back = __builtin_bit_cast(float, (uint32_t)(127 - 13 + e) << 23);
   const float logits = a.scale * kLog2e * back;
-  q.unit = logits * 0x1p24f;
+  q.unit = logits * 0x1p22f;
   float sum = 0.f;
 #pragma unroll
   for (int p = 0; p < D / 64; ++p) {
@@ -412,7 +426,7 @@ __device__ __forceinline__ void load_queries(Queries<D>& q, const KvAttentionArg
     q.odd[p] = __builtin_bit_cast(uint4v, odd);
   }
   sum = groups_sum(sum);
-  q.sum8 = sum * -0x1p-21f;
+  q.sum8 = sum * -0x1p-19f;
   q.sum = sum * logits;
 }
 

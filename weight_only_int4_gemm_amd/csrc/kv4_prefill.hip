@@ -148,14 +148,14 @@ struct Producer {
         const int x = lane + 64 * part_of(m), r = 16 * (unit % 2) + x % 16, q = x / 16 % J;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t w = a[m][i], w8 = w >> 8;
-          // word 4 q + i; subnormals c 2^-24 and 16 c 2^-24, as in the other kernel
+          const uint32_t w = a[m][i] << 2, w8 = a[m][i] >> 6;
+          // word 4 q + i; subnormals 4 c 2^-24 and 64 c 2^-24, as in the other kernel
           st.k[unit / 2][2 * q + i / 2][32 * (i % 2) + r] =
-              uint4v{w & kLow, w & kHigh, w8 & kLow, w8 & kHigh};
+              uint4v{w & kKeyLow, w & kKeyHigh, w8 & kKeyLow, w8 & kKeyHigh};
         }
         if (m == 0 && q == 0) {
           const int token = 16 * unit + lane % 16;
-          st.ks[token] = low_half(kp) * unit_of_logits * 0x1p24f;
+          st.ks[token] = low_half(kp) * unit_of_logits * 0x1p22f;
           st.kz[token] = high_half(kp) - 8.f * low_half(kp);
           st.vp[token] = vp;
           if (lane % 16 == 0) st.there[unit] = valid ? 0xffffu : 0u;
