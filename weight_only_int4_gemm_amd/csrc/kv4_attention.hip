@@ -8,12 +8,14 @@
 // offsets touch one number per key or per probability instead of D.
 //
 // Codes as operands.  Four bits c in the mantissa of an FP16 whose other bits
-// are zero are the subnormal c 2^-24 (16 c 2^-24 when they sit one nibble
-// higher); the matrix instruction takes subnormals exactly.  One AND per two
-// codes is then the whole unpacking.  The sums, though, are cut off relative
-// to what the operands' exponents allow, and leading zeros of a subnormal
-// count there: keys, whose products are the logits, are moved to the top of
-// the mantissa (one more shift per word; the logits' error is a third).
+// are zero are the subnormal c 2^-24 (times a power of two by where they
+// sit); the matrix instruction takes subnormals exactly.  One AND per two
+// codes is then the unpacking.  The sums, though, are cut off relative to
+// what the operands' exponents allow, and leading zeros of a subnormal count
+// there, so the codes are moved to the top of the mantissa, a shift or two
+// per word.  Left at its bottom they cost 1% and, of one FP16 request of
+// 100000 tokens, four times the output's rounding; logits were five times as
+// far off.
 //
 // Layout.  The keys are the first operand (rows = 16 tokens), the queries the
 // second (columns = 16 query rows), so lane l holds scores of column l % 16
@@ -205,7 +207,6 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
   constexpr int N = PAIRED ? 4 : 8;  // scores of a lane
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const bool upper = PAIRED && (lane & 8);
-  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
   // The matrix unit cuts off low bits at every addition: sums from zero, of
   // few products, and -8 sum q added after them, keep a third less error in
@@ -219,8 +220,8 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
     for (int p = 0; p < D / 64; ++p) {
       const uint32_t w0 = d.k[u][2 * p], w1 = d.k[u][2 * p + 1];
       const uint32_t a0 = w0 << 2, a1 = w1 << 2, b0 = w0 >> 6, b1 = w1 >> 6;
-      const uint4v e = {a0 & kKeyLow, a1 & kKeyLow, b0 & kKeyLow, b1 & kKeyLow};
-      const uint4v o = {a0 & kKeyHigh, a1 & kKeyHigh, b0 & kKeyHigh, b1 & kKeyHigh};
+      const uint4v e = {a0 & kLowCodes, a1 & kLowCodes, b0 & kLowCodes, b1 & kLowCodes};
+      const uint4v o = {a0 & kHighCodes, a1 & kHighCodes, b0 & kHighCodes, b1 & kHighCodes};
       raw[u] = mfma(e, q.even[p], raw[u]);
       if constexpr (TWO) odd[u] = mfma(o, q.odd[p], odd[u]);
       else raw[u] = mfma(o, q.odd[p], raw[u]);
@@ -341,21 +342,36 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
 #pragma unroll
   for (int k = 0; k < kParts; ++k) s.w = mfma(ones, weights[k], s.w);
 
-  // byte b of two tokens' words into the two halves of a register
+  // Byte b of two tokens' words into the two halves of a register, moved up
+  // by two bits like the keys' codes.  Words moved as they are serve for the
+  // first three bytes, whose halves then take a bit field that spans two.
   const uint32_t half = D == 64 ? (lane & 1) * 0x00020002u : 0u;
   constexpr int kBytes = D == 64 ? 2 : 4;
 #pragma unroll
   for (int i = 0; i < TileData<D, ROWS>::VV; ++i) {
+    uint4v moved[2];
+    if constexpr (D > 64) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) moved[u] = d.v[u][i] << 2;
+    }
 #pragma unroll
     for (int b = 0; b < kBytes; ++b) {
-      const uint32_t sel = (0x0c040c00u + 0x00010001u * b) + half;
-      uint4v both, e, o;
+      uint4v e, o;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint4v& v = d.v[k >> 1][i];
-        both[k] = __builtin_amdgcn_perm(v[2 * (k & 1) + 1], v[2 * (k & 1)], sel);
-        e[k] = both[k] & kLow;
-        o[k] = both[k] & kHigh;
+        uint32_t both;
+        if (D > 64 && b < 3) {
+          const uint4v& v = moved[k >> 1];
+          both = __builtin_amdgcn_perm(v[2 * (k & 1) + 1], v[2 * (k & 1)],
+                                       0x05040100u + 0x01010101u * b);
+        } else {
+          const uint4v& v = d.v[k >> 1][i];
+          both = __builtin_amdgcn_perm(v[2 * (k & 1) + 1], v[2 * (k & 1)],
+                                       (0x0c040c00u + 0x00010001u * b) + half)
+                 << 2;
+        }
+        e[k] = both & kLowCodes;
+        o[k] = both & kHighCodes;
       }
       const int c = 2 * (kBytes * i + b);
 #pragma unroll
@@ -545,7 +561,7 @@ __global__ __launch_bounds__(kThreads, (kResident<D, ROWS>)) void kv_tokens_kern
   for (int c = 0; c < D / 16; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      s.acc[c][i] = s.acc[c][i] * (c & 1 ? 0x1p20f : 0x1p24f) + fixed;
+      s.acc[c][i] = s.acc[c][i] * (c & 1 ? 0x1p18f : 0x1p22f) + fixed;
 
   constexpr int kCols = D == 64 ? 4 : 8;  // neighbouring channels of a lane
   // Join the waves, in wave order, through LDS: each leaves its rows and

@@ -13,7 +13,7 @@ constexpr int kTile = 32;                   // tokens of one step: two units
 constexpr int kWaitLoads = 0x0f70;          // s_waitcnt: all vector loads, nothing else
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr uint32_t kKeyLow = 0x003c003cu, kKeyHigh = 0x03c003c0u;  // codes of keys, moved up by two
+constexpr uint32_t kLowCodes = 0x003c003cu, kHighCodes = 0x03c003c0u;  // of codes, moved up by two bits
 constexpr float kNone = -1e30f;             // reference of a column that has seen no key
 constexpr float kMostWeight = 32768.0f;     // of a weight, before the reference moves
 constexpr float kTopWeight = 8.0f;          // log2 of the largest weight after it has

@@ -151,7 +151,7 @@ struct Producer {
           const uint32_t w = a[m][i] << 2, w8 = a[m][i] >> 6;
           // word 4 q + i; subnormals 4 c 2^-24 and 64 c 2^-24, as in the other kernel
           st.k[unit / 2][2 * q + i / 2][32 * (i % 2) + r] =
-              uint4v{w & kKeyLow, w & kKeyHigh, w8 & kKeyLow, w8 & kKeyHigh};
+              uint4v{w & kLowCodes, w & kHighCodes, w8 & kLowCodes, w8 & kHighCodes};
         }
         if (m == 0 && q == 0) {
           const int token = 16 * unit + lane % 16;
