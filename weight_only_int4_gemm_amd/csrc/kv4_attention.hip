@@ -12,10 +12,10 @@
 // sit); the matrix instruction takes subnormals exactly.  One AND per two
 // codes is then the unpacking.  The sums, though, are cut off relative to
 // what the operands' exponents allow, and leading zeros of a subnormal count
-// there, so the codes are moved to the top of the mantissa, a shift or two
-// per word.  Left at its bottom they cost 1% and, of one FP16 request of
-// 100000 tokens, four times the output's rounding; logits were five times as
-// far off.
+// there.  So the codes are moved to the top of the mantissa, a shift or two
+// per word, for 1% of a decode step: at the bottom an FP16 request of 100000
+// tokens was four times the output's rounding off (one now), and logits were
+// five times as far off.
 //
 // Layout.  The keys are the first operand (rows = 16 tokens), the queries the
 // second (columns = 16 query rows), so lane l holds scores of column l % 16
@@ -208,14 +208,12 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const bool upper = PAIRED && (lane & 8);
 
-  // The matrix unit cuts off low bits at every addition: sums from zero, of
-  // few products, and -8 sum q added after them, keep a third less error in
-  // the logits than one sum that starts with it.
-  constexpr bool TWO = D > 64;
-  float4v raw[2], odd[2];
+  // The sums start from zero, not from -8 sum q: what the matrix unit cuts off
+  // goes by the largest addend.
+  float4v raw[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    raw[u] = odd[u] = float4v{0.f, 0.f, 0.f, 0.f};
+    raw[u] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int p = 0; p < D / 64; ++p) {
       const uint32_t w0 = d.k[u][2 * p], w1 = d.k[u][2 * p + 1];
@@ -223,20 +221,16 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
       const uint4v e = {a0 & kLowCodes, a1 & kLowCodes, b0 & kLowCodes, b1 & kLowCodes};
       const uint4v o = {a0 & kHighCodes, a1 & kHighCodes, b0 & kHighCodes, b1 & kHighCodes};
       raw[u] = mfma(e, q.even[p], raw[u]);
-      if constexpr (TWO) odd[u] = mfma(o, q.odd[p], odd[u]);
-      else raw[u] = mfma(o, q.odd[p], raw[u]);
+      raw[u] = mfma(o, q.odd[p], raw[u]);
     }
   }
 
   if constexpr (PAIRED) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      raw[0][i] = upper ? raw[1][i] : raw[0][i];
-      if constexpr (TWO) odd[0][i] = upper ? odd[1][i] : odd[0][i];
-    }
+    for (int i = 0; i < 4; ++i) raw[0][i] = upper ? raw[1][i] : raw[0][i];
   }
 #pragma unroll
-  for (int u = 0; u < N / 4; ++u) raw[u] = (TWO ? raw[u] + odd[u] : raw[u]) + q.sum8;
+  for (int u = 0; u < N / 4; ++u) raw[u] += q.sum8;
   auto key_params = [&](int i) { return d.kp[i >> 2][i & 3]; };
   auto value_params = [&](int i) { return d.vp[i >> 2][i & 3]; };
   float scale[N];  // of the keys, times the logits' unit
