@@ -42,9 +42,9 @@
 // one tile ahead, straight into registers: nothing is shared between waves.
 //
 // What bounds it (D = 128): HBM in decode steps, 64 requests of 4096 tokens
-// and 32 heads 127 us (6.2 TB/s), one of 131072 tokens and 8 heads 31 us (4.6
+// and 32 heads 129 us (6.1 TB/s), one of 131072 tokens and 8 heads 31 us (4.6
 // TB/s: the start and the join take about 8 us); eight dependent trips to
-// memory in short calls, one of 1000 tokens and 32 heads 8.7 us; vector and
+// memory in short calls, one of 1000 tokens and 32 heads 8.3 us; vector and
 // matrix instructions, which hardly overlap, with more rows: 24 requests of 5
 // queries on windows of 4096 tokens, 32 heads on 8, D = 64, 32 us.
 #include "kv4_attention.hpp"

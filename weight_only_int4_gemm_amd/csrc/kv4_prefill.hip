@@ -16,7 +16,8 @@
 // take 0.34 us per wave together, 0.22 and 0.17 alone), so a tile of 32 x 32
 // scores costs their sum, 512 + about 880 cycles with D = 128, and the kernel
 // runs at 0.92 of that: 2 x 2048 queries over up to 8192 keys, 64 heads of
-// 128, BF16: 0.83 ms, 690 TFLOP/s (the library's 16384^3 product: 1364).  For
+// 128, BF16: 0.84 ms under the profiler, 0.72 to 0.75 without, 760 to 800
+// TFLOP/s (a 16384^3 product of the matrix library: 1364).  For
 // the same reason these did not help: two groups of waves that change places
 // between softmax and products at barriers (0.91), eight waves per workgroup
 // (0.85), the next tile's products between the softmax's instructions (0.87
