@@ -76,8 +76,9 @@ size_t kv4_cache_bytes(int pages, int heads, int D, int page);
  * old/new the pages that lens/want tokens take, the requests in order:
  *  - want > lens: takes new - old pages from the head of the ring, in
  *    request order, and writes them to table[b][old .. new).  If the pages
- *    wanted up to and including this request exceed `count`, or new exceeds
- *    max_pages, the request is refused: it keeps its length and pages.
+ *    wanted up to and including this request exceed `count`, new exceeds
+ *    max_pages, or its new tokens do not all lie below `capacity` (see
+ *    q_start), the request is refused: it keeps its length and pages.
  *  - want < lens: pages new .. old of its row go to the tail of the ring
  *    (available to the next call); the row's entries beyond new stay as
  *    they are and mean nothing.
@@ -87,7 +88,11 @@ size_t kv4_cache_bytes(int pages, int heads, int D, int page);
  * to `capacity`; new token i of request b is token t = q_start[b] + i:
  * positions[t] = lens[b] + i and slots[t] is its place in the cache, -1 if
  * refused or if its page id is outside the cache.  Entries from q_start[B]
- * to capacity get slot -1, position 0.
+ * to capacity get slot -1, position 0.  So every token below lens_out[b] has
+ * a slot, now or from an earlier call.  The rows of a refused request still
+ * count in q_start: its tokens are not stored, and kv4_attention computes its
+ * queries over the tokens it holds (the last at position lens_out[b] - 1),
+ * results that mean nothing.
  *
  * lens, want (device, read) int32 [B]; lengths below 0 count as 0, lens
  * above max_pages * page as that.  table (device, read and written) int32

@@ -182,11 +182,14 @@ def tables(lens, want, table, ring, state, capacity, page):
     lens_out, q_start = [], [0]
     slots, positions = [-1] * capacity, [0] * capacity
     wanted = taken = returned = refused = 0
+    ends = 0                                # new tokens so far, refused or not
     for b in range(B):
         n = min(max(int(lens[b]), 0), width * page)
         w = max(int(want[b]), 0)
         old, new = -(-n // page), -(-w // page)
-        ok = new <= width
+        grown = max(0, w - n)
+        ends += grown
+        ok = new <= width and (grown == 0 or ends <= capacity)
         if ok and new > old:
             ids = []
             if wanted + new - old <= count:
@@ -201,7 +204,7 @@ def tables(lens, want, table, ring, state, capacity, page):
             for i in range(new, old):
                 ring[(head + count + returned) % pages] = before[b, i]
                 returned += 1
-        for i in range(max(0, w - n)):
+        for i in range(grown):
             t = q_start[-1] + i
             if t >= capacity:
                 break
@@ -210,7 +213,7 @@ def tables(lens, want, table, ring, state, capacity, page):
                 pid = int(table[b, (n + i) // page])
                 if 0 <= pid < pages:
                     slots[t] = pid * page + (n + i) % page
-        q_start.append(min(capacity, q_start[-1] + max(0, w - n)))
+        q_start.append(min(capacity, ends))
         lens_out.append(w if ok else n)
     state_out = [(head + taken) % pages, min(pages, count - taken + returned), refused, 0]
     return (np.array(lens_out, np.int32), table, ring, np.array(state_out, np.int32),

@@ -60,7 +60,9 @@ __device__ __forceinline__ int owner(const int* sums, int n, int x) {
 }
 
 // Served requests are those whose pages are there: cumulative need within
-// the free pages (requests that take none are always served).
+// the free pages (requests that take none are always served).  The pages of a
+// request refused for its tokens need no leaving out of later sums: those
+// tokens leave no room for any request after it that grows.
 __device__ __forceinline__ bool served(bool over, int need_before, int need_upto, int count) {
   return !over && (need_upto == need_before || need_upto <= count);
 }
@@ -77,6 +79,9 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
   __shared__ int wave_sum[3][THREADS / 64];
   __shared__ int s_refused, s_taken, s_last;
   constexpr int kMost = 0x7fffffff;
+  // new tokens are summed to one past what there is room for, which tells a
+  // request that ends at the room's end from one that does not fit
+  const int most_tokens = a.capacity + 1;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (a.B + THREADS - 1) / THREADS;
   const int shift = 31 - __builtin_clz((unsigned)a.page);
@@ -113,11 +118,11 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
     need[b + 1] = diff > 0 ? diff : 0;
     back[b + 1] = diff < 0 ? -diff : 0;
     held[b] = r.len | (r.over ? kOver : 0);
-    sum[0] = add_up_to(sum[0], grown, a.capacity);
+    sum[0] = add_up_to(sum[0], grown, most_tokens);
     sum[1] = add_up_to(sum[1], need[b + 1], kMost);
     sum[2] = add_up_to(sum[2], back[b + 1], kMost);
   }
-  const int most[3] = {a.capacity, kMost, kMost};
+  const int most[3] = {most_tokens, kMost, kMost};
   int before[3];
 #pragma unroll
   for (int s = 0; s < 3; ++s) {
@@ -148,7 +153,10 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
   }
   __syncthreads();
 
-  const int tokens = tok[a.B], wanted = need[a.B], returned = back[a.B];
+  const int tokens = tok[a.B] < a.capacity ? tok[a.B] : a.capacity;
+  const int wanted = need[a.B], returned = back[a.B];
+  // whether the tokens of a request that grows all have room
+  auto fits = [&](int b) { return tok[b + 1] <= a.capacity; };
   // A workgroup alone does everything (in place that spares the arrival); of
   // several the last ones do the pages, beside the tokens of the others.
   const int page_groups = gridDim.x - a.token_groups;
@@ -161,7 +169,7 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
   const int take = tokens_only ? 0 : wanted < count ? wanted : count;
   for (int i = first; i < take; i += stride) {
     const int b = owner(need, a.B, i);
-    if (!served(false, need[b], need[b + 1], count)) continue;  // over wants none
+    if (!fits(b) || !served(false, need[b], need[b + 1], count)) continue;  // over wants none
     const int col = pages_of(held[b]) + i - need[b];
     a.table[(int64_t)b * a.max_pages + col] = a.ring[(head + (unsigned)i) % P];
   }
@@ -178,7 +186,7 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
       const int b = owner(tok, a.B, t);
       const int len = held[b] & ~kOver;
       pos = len + t - tok[b];
-      if (served(held[b] & kOver, need[b], need[b + 1], count)) {
+      if (fits(b) && served(held[b] & kOver, need[b], need[b + 1], count)) {
         const int col = pos >> shift, old = pages_of(len);
         // a page of this call comes from the ring: the table's entry may
         // not be written yet
@@ -192,7 +200,8 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
     a.positions[t] = pos;
   }
   if (!tokens_only)
-    for (int b = first; b <= a.B; b += stride) a.q_start[b] = tok[b];
+    for (int b = first; b <= a.B; b += stride)
+      a.q_start[b] = tok[b] < a.capacity ? tok[b] : a.capacity;
 
   // In place, the last workgroup writes what others may still have been
   // reading; otherwise one writes at once.
@@ -214,7 +223,7 @@ __global__ __launch_bounds__(THREADS) void kv_tables_kernel(KvTablesArgs a) {
     const int b = b0 + k;
     if (b >= b1) break;
     const Request r = request(a, lens[k], want[k]);
-    const bool ok = served(r.over, need[b], need[b + 1], count);
+    const bool ok = (r.want <= r.len || fits(b)) && served(r.over, need[b], need[b + 1], count);
     a.lens_out[b] = ok ? r.want : r.len;
     if (!ok) atomicAdd(&s_refused, 1);
     else if (need[b + 1] > need[b]) atomicMax(&s_taken, need[b + 1]);
