@@ -245,19 +245,15 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
     const int j = (int)apart(t + 4 * g + (upper ? kKvUnit : 0)) + kKvUnit * (i >> 2) + (i & 3);
     return (upper ? d.valid[1] : d.valid[i >> 2]) && j >= q.lo && j <= q.hi;
   };
-  // the logit less m: scale (q . c) + (offset sum q - m)
-  auto logit = [&](int i, float m) {
+  // the logit less the reference: scale (q . c) + (offset sum q - m)
+  auto logit_less_m = [&](int i) {
     return __builtin_fmaf(scale[i], raw[i >> 2][i & 3],
-                          __builtin_fmaf(high_half(key_params(i)), q.sum, -m));
+                          __builtin_fmaf(high_half(key_params(i)), q.sum, -s.m));
   };
-  // `again`: m has just moved to where every weight fits; logits so large
-  // that their rounding says otherwise are held to it.
-  auto weigh = [&](float m, bool again) {
+  auto weigh = [&](auto&& less_m) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float x = logit(i, m);
-      if (again) x = held(x, apart(value_params(i)));
-      p[i] = exp2_hw(x);
+      p[i] = exp2_hw(less_m(i));
       w[i] = times_low_half(p[i], value_params(i));
     }
     if (edge) {
@@ -275,18 +271,20 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
 #pragma unroll
     for (int i = 0; i < N; i += 2) most = fmaxf(fmaxf(most, w[i]), w[i + 1]);
   };
-  weigh(s.m, false);
+  weigh(logit_less_m);
   if (__any(most > kMostWeight || sum > kMostSum)) {
     // Move the reference: the largest weight becomes 2^8, unless that lets
-    // a probability exceed 2^40 (values of scale 0).
-    float top = kNone;
+    // a probability exceed 2^40 (values of scale 0).  Each logit is formed
+    // once: the reference comes from the same numbers that it is then taken
+    // off, so however coarse FP32 is at their size the largest keeps its weight.
+    float x[N], top = kNone;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float offset = high_half(apart(key_params(i)));
-      float x = scale[i] * raw[i >> 2][i & 3] + offset * q.sum;
-      if (edge) x = seen(i) ? x : -__builtin_inff();
-      top = fmaxf(top, x + __builtin_amdgcn_logf(low_half(apart(value_params(i)))) - kTopWeight);
-      top = fmaxf(top, x - kSumHeadroom);
+      x[i] = __builtin_fmaf(scale[i], raw[i >> 2][i & 3],
+                            high_half(apart(key_params(i))) * q.sum);
+      const float y = !edge || seen(i) ? x[i] : -__builtin_inff();
+      top = fmaxf(top, y + __builtin_amdgcn_logf(low_half(apart(value_params(i)))) - kTopWeight);
+      top = fmaxf(top, y - kSumHeadroom);
     }
     top = groups_max(top);
     if constexpr (PAIRED) top = fmaxf(top, pair_lane(top));
@@ -298,7 +296,8 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
     s.w *= f;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) s.acc[c] *= f;
-    weigh(m, true);
+    // (rounding may still say more than the move provides for: held to it)
+    weigh([&](int i) { return held(x[i] - m, apart(value_params(i))); });
   }
   s.l += sum;
   if (edge) {

@@ -206,6 +206,11 @@ __device__ __forceinline__ float16v scores(const Stage<D>& st, int tile, const u
   return raw;
 }
 
+// A logit by itself, where the reference moves.
+__device__ __forceinline__ float logit(float ks, float product, float kz, float sum_q) {
+  return __builtin_fmaf(ks, product, kz * sum_q);
+}
+
 // The probabilities of a tile under reference m: packed weights, and their
 // sums.  Parameters are read as they are used, four tokens at a time.  EDGE:
 // some token is not seen by some row; what the cache holds for it may be
@@ -244,8 +249,8 @@ __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int 
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float product = EDGE ? raw[4 * a + r] * back : raw[4 * a + r];
-      float x = __builtin_fmaf(ks[r], product, __builtin_fmaf(kz[r], sum_q, -m));
-      if constexpr (AGAIN) x = held(x, vp[r]);
+      const float x = AGAIN ? held(logit(ks[r], product, kz[r], sum_q) - m, vp[r])
+                            : __builtin_fmaf(ks[r], product, __builtin_fmaf(kz[r], sum_q, -m));
       float p = exp2_hw(x);
       w[r] = times_low_half(p, vp[r]);
       float z = high_half(vp[r]);
@@ -285,7 +290,8 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
   else
     weigh<D, BF16, false>(o, st, tile, raw, sum_q, back, s.m, there, t, lo, hi);
   if (__any(o.over)) {
-    // Move the reference, as the other kernel does.
+    // Move the reference, as the other kernel does, from the same logits that
+    // `weigh` then takes it off.
     float top = kNone;
     const int t1 = (int)apart(t);
     const uint32_t there1 = apart(there);
@@ -297,7 +303,7 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
       for (int r = 0; r < 4; ++r) {
         const int j = t1 + at + r, i = 32 * tile + at + r;
         const float got = a == 0 ? raw[r] : a == 1 ? raw[4 + r] : a == 2 ? raw[8 + r] : raw[12 + r];
-        const float x = st.ks[i] * (got * back1) + st.kz[i] * sum_q;
+        const float x = logit(st.ks[i], got * back1, st.kz[i], sum_q);
         const bool seen = (there1 >> (at + r) & 1) && j >= lo && j <= hi;
         const float y = fmaxf(x + __builtin_amdgcn_logf(low_half(st.vp[i])) - kTopWeight,
                               x - kSumHeadroom);
