@@ -106,3 +106,13 @@ def _verify(case, decided):
 def test_large_logits_keep_their_largest_key(queries, planned, dtype, every, power):
     _verify(_case(700 + power, 300, queries, planned, power, every, dtype),
             0.9 if every == 1 else 0.3)
+
+
+@pytest.mark.parametrize("queries,planned", KERNELS)
+@pytest.mark.parametrize("power", [102, 106, 110])
+def test_rows_whose_every_logit_is_far_below_zero_are_not_empty(queries, planned, power):
+    """A prompt from its first token: the first rows see few keys, half of them
+    with negative logits only, past any finite stand-in for "no key yet"."""
+    for seed in range(3):
+        _verify(_case(720 + power + 1000 * seed, queries, queries, planned, power, 1, "bfloat16"),
+                0.5)

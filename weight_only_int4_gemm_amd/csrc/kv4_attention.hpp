@@ -14,7 +14,9 @@ constexpr int kWaitLoads = 0x0f70;          // s_waitcnt: all vector loads, noth
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr uint32_t kLowCodes = 0x003c003cu, kHighCodes = 0x03c003c0u;  // of codes, moved up by two bits
-constexpr float kNone = -1e30f;             // reference of a column that has seen no key
+// Reference of a column that has seen no key: below every logit (base 2) that
+// FP32 holds, and finite, so that differences of two are numbers.
+constexpr float kNone = -0x1.fffffep127f;
 constexpr float kMostWeight = 32768.0f;     // of a weight, before the reference moves
 constexpr float kTopWeight = 8.0f;          // log2 of the largest weight after it has
 constexpr float kMostSum = 0x1p60f;         // of a tile's probabilities, likewise
