@@ -184,7 +184,9 @@ int kv4_dequant_debug(const int32_t* slots, const uint8_t* cache, uint16_t* K, u
  * sums are FP32; the only roundings to 16 bits are the probability times
  * the value's scale (to FP16; for FP16 calls the remainder is carried too)
  * and the output.  A query's size costs other queries no precision; logits
- * beyond FP32's integers (2^24) are told apart as far as FP32 does.
+ * beyond FP32's integers (2^24) are told apart as far as FP32 does, and the
+ * largest keeps its weight.  A logit (base 2) beyond FP32's range counts as
+ * that infinity: no weight below it, a NaN above.
  *
  * Q (device, read), O (device, write): 16-bit [T][Hq][D], token and head
  * strides in elements, multiples of 8, contiguous channels, 16-byte

@@ -116,3 +116,59 @@ def test_rows_whose_every_logit_is_far_below_zero_are_not_empty(queries, planned
     for seed in range(3):
         _verify(_case(720 + power + 1000 * seed, queries, queries, planned, power, 1, "bfloat16"),
                 0.5)
+
+
+@pytest.mark.parametrize("queries,planned", KERNELS)
+@pytest.mark.parametrize("every", [1, 3])
+@pytest.mark.parametrize("power", [100, 115, 122, 125])
+def test_queries_at_the_end_of_their_range(queries, planned, every, power):
+    """BF16 queries up to their type's end, whose logits FP32 still holds, and
+    rows of zeros beside them."""
+    _verify(_case(760 + power, 300, queries, planned, power, every, "bfloat16", zero=True), 0.1)
+
+
+@pytest.mark.parametrize("queries,planned", KERNELS)
+@pytest.mark.parametrize("power", [100, 110, 120])
+def test_scales_of_any_size(queries, planned, power):
+    """The same by the scale of the call, with FP16 queries."""
+    _verify(_case(780 + power, 300, queries, planned, power, 1, "float16", zero=True), 0.5)
+
+
+@pytest.mark.parametrize("queries,planned", KERNELS)
+def test_small_queries_under_a_large_scale(queries, planned):
+    """Ordinary logits as 2^-95 times 2^95 are those of 1 times 1, bit for bit."""
+    import torch
+    results = []
+    for power in (0, 95):
+        rng = np.random.default_rng(790)
+        n, page, Hq, D = 200, 32, 8, 128
+        k, v = rng.standard_normal((2, 224, 1, D)).astype(np.float32)
+        cache = torch.empty((7, 1, page, D + 8), dtype=torch.uint8, device="cuda")
+        K, V = (torch.from_numpy(x).half().cuda() for x in (k, v))
+        w4.kv4_append(K, V, torch.arange(224, dtype=torch.int32, device="cuda"), cache)
+        q = torch.from_numpy(rng.standard_normal((queries, Hq, D)) * 2.0 ** -power).to(
+            torch.float32).bfloat16().cuda()
+        max_len = 6000 if planned > queries else n
+        say("attention scale", queries, power)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        O, L = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        w4.kv4_attention(q, cache, torch.arange(7, **i32)[None], torch.tensor([n], **i32),
+                         torch.tensor([0, queries], **i32), O, L, D ** -0.5 * 2.0 ** power, 0,
+                         planned, max_len, w4.alloc_kv4_workspace(1, Hq, 1, D, planned, max_len))
+        torch.cuda.synchronize()
+        results.append((O, L))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("queries,planned", KERNELS)
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("power", [30, 105, 124])
+def test_large_rows_of_other_head_sizes(queries, planned, D, power):
+    _verify(_case(800 + power, 200, queries, planned, power, 2, "bfloat16", zero=True, D=D), 0.2)
+
+
+@pytest.mark.parametrize("queries,planned", KERNELS)
+@pytest.mark.parametrize("power", [30, 124])
+def test_large_rows_over_joined_ranges(queries, planned, power):
+    """More tokens than a range holds: parts with unlike references are joined."""
+    _verify(_case(820 + power, 1500, queries, planned, power, 2, "bfloat16", page=64), 0.4)

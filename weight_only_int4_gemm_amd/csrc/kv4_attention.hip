@@ -195,6 +195,8 @@ struct Queries {
   float unit;  // product units to base-2 logits
   float sum;   // sum q in base-2 logits
   int lo, hi;  // keys seen: lo <= j <= hi
+  bool large;  // some row's logits may pass 2^kMostLogits (the same in all lanes):
+  float up;    // this column's are then `up` times what unit and sum make
 };
 
 // One tile.  `edge`: some of its tokens are not seen by some row.  What the
@@ -272,16 +274,17 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
     for (int i = 0; i < N; i += 2) most = fmaxf(fmaxf(most, w[i]), w[i + 1]);
   };
   weigh(logit_less_m);
-  if (__any(most > kMostWeight || sum > kMostSum)) {
+  if (q.large || __any(most > kMostWeight || sum > kMostSum)) {
     // Move the reference: the largest weight becomes 2^8, unless that lets
     // a probability exceed 2^40 (values of scale 0).  Each logit is formed
     // once: the reference comes from the same numbers that it is then taken
     // off, so however coarse FP32 is at their size the largest keeps its weight.
+    // (Large rows come here with every tile.)
     float x[N], top = kNone;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      x[i] = __builtin_fmaf(scale[i], raw[i >> 2][i & 3],
-                            high_half(apart(key_params(i))) * q.sum);
+      x[i] = q.up * __builtin_fmaf(scale[i], raw[i >> 2][i & 3],
+                                   high_half(apart(key_params(i))) * q.sum);
       const float y = !edge || seen(i) ? x[i] : -__builtin_inff();
       top = fmaxf(top, y + __builtin_amdgcn_logf(low_half(apart(value_params(i)))) - kTopWeight);
       top = fmaxf(top, y - kSumHeadroom);
@@ -414,11 +417,13 @@ __device__ __forceinline__ void load_queries(Queries<D>& q, const KvAttentionArg
   // a score keeps 2^-30 of the largest one its row could have, however small
   // the queries (the odd channels are divided by 16, which FP16's smallest
   // step would otherwise cut into).
-  int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
+  int e = exponent_of(top);
   e = e < -100 ? -100 : e;
-  const float up = __builtin_bit_cast(float, (uint32_t)(127 + 13 - e) << 23);
-  const float back = __builtin_bit_cast(float, (uint32_t)(127 - 13 + e) << 23);
-  const float logits = a.scale * kLog2e * back;
+  const float up = power_of_two(13 - e);
+  const int by = large_by(a.scale, e);
+  q.large = __any(by > 0);
+  q.up = power_of_two(by < 127 ? by : 127);
+  const float logits = a.scale * (kLog2e * power_of_two(e - 13 - by));
   q.unit = logits * 0x1p22f;
   float sum = 0.f;
 #pragma unroll

@@ -22,11 +22,27 @@ constexpr float kTopWeight = 8.0f;          // log2 of the largest weight after 
 constexpr float kMostSum = 0x1p60f;         // of a tile's probabilities, likewise
 constexpr float kSumHeadroom = 40.0f;       // log2 of a probability over the reference
 
+// Logits whose size may pass 2^kMostLogits (the scale's exponent plus that of a
+// row's largest query) are formed 2^large_by() smaller: FP32 then holds every
+// number on the way, whatever the parameters (2^16, 23 of them) and channels.
+constexpr int kMostLogits = 95;
+
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ int exponent_of(float x) {  // x >= 0
+  return (int)(__builtin_bit_cast(uint32_t, x) >> 23) - 127;
+}
+__device__ __forceinline__ float power_of_two(int e) {  // -126 <= e <= 127
+  return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+}
+__device__ __forceinline__ int large_by(float scale, int e) {
+  const int by = exponent_of(scale) + e - kMostLogits;
+  return by > 0 ? by : 0;
+}
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 

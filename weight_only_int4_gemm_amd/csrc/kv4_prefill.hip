@@ -206,9 +206,9 @@ __device__ __forceinline__ float16v scores(const Stage<D>& st, int tile, const u
   return raw;
 }
 
-// A logit by itself, where the reference moves.
-__device__ __forceinline__ float logit(float ks, float product, float kz, float sum_q) {
-  return __builtin_fmaf(ks, product, kz * sum_q);
+// A logit by itself, where the reference moves; `up` is 1 but for large rows.
+__device__ __forceinline__ float logit(float ks, float product, float kz, float sum_q, float up) {
+  return up * __builtin_fmaf(ks, product, kz * sum_q);
 }
 
 // The probabilities of a tile under reference m: packed weights, and their
@@ -227,8 +227,8 @@ struct Weights {
 
 template <int D, bool BF16, bool EDGE, bool AGAIN = false>
 __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int tile,
-                                      const float16v& raw, float sum_q, float back, float m,
-                                      uint32_t there, int t, int lo, int hi) {
+                                      const float16v& raw, float sum_q, float back, float up,
+                                      float m, uint32_t there, int t, int lo, int hi) {
   const int h = (threadIdx.x & 63) >> 5;
   // known here only: the usual path must not compute masks or products
   if constexpr (EDGE) {
@@ -249,7 +249,7 @@ __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int 
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float product = EDGE ? raw[4 * a + r] * back : raw[4 * a + r];
-      const float x = AGAIN ? held(logit(ks[r], product, kz[r], sum_q) - m, vp[r])
+      const float x = AGAIN ? held(logit(ks[r], product, kz[r], sum_q, up) - m, vp[r])
                             : __builtin_fmaf(ks[r], product, __builtin_fmaf(kz[r], sum_q, -m));
       float p = exp2_hw(x);
       w[r] = times_low_half(p, vp[r]);
@@ -280,16 +280,17 @@ __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int 
 
 template <int D, bool BF16>
 __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const uint4v* q,
-                                            float sum_q, float back, RowSums<D>& s,
-                                            uint32_t there, int t, bool edge, int lo, int hi) {
+                                            float sum_q, float back, bool large, float up,
+                                            RowSums<D>& s, uint32_t there, int t, bool edge,
+                                            int lo, int hi) {
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const float16v raw = scores<D>(st, tile, q);
   Weights<BF16> o;
   if (edge)
-    weigh<D, BF16, true>(o, st, tile, raw, sum_q, back, s.m, there, t, lo, hi);
+    weigh<D, BF16, true>(o, st, tile, raw, sum_q, back, up, s.m, there, t, lo, hi);
   else
-    weigh<D, BF16, false>(o, st, tile, raw, sum_q, back, s.m, there, t, lo, hi);
-  if (__any(o.over)) {
+    weigh<D, BF16, false>(o, st, tile, raw, sum_q, back, up, s.m, there, t, lo, hi);
+  if (large || __any(o.over)) {
     // Move the reference, as the other kernel does, from the same logits that
     // `weigh` then takes it off.
     float top = kNone;
@@ -303,7 +304,7 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
       for (int r = 0; r < 4; ++r) {
         const int j = t1 + at + r, i = 32 * tile + at + r;
         const float got = a == 0 ? raw[r] : a == 1 ? raw[4 + r] : a == 2 ? raw[8 + r] : raw[12 + r];
-        const float x = logit(st.ks[i], got * back1, st.kz[i], sum_q);
+        const float x = logit(st.ks[i], got * back1, st.kz[i], sum_q, up);
         const bool seen = (there1 >> (at + r) & 1) && j >= lo && j <= hi;
         const float y = fmaxf(x + __builtin_amdgcn_logf(low_half(st.vp[i])) - kTopWeight,
                               x - kSumHeadroom);
@@ -318,7 +319,7 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
     s.z *= f;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) s.acc[c] *= f;
-    weigh<D, BF16, true, true>(o, st, tile, raw, sum_q, back, s.m, there, t, lo, hi);
+    weigh<D, BF16, true, true>(o, st, tile, raw, sum_q, back, up, s.m, there, t, lo, hi);
   }
   s.l += o.sum;
   s.z += o.z;
@@ -392,10 +393,13 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
   // workgroup's largest finite row near FP16's upper end; the keys' scales
   // are stored in logits with it.  Rows that would lose bits by that, 2^-10
   // of the largest or smaller, are rare: then (`wide`) every row has a power
-  // of its own, and its products are brought back by it.
+  // of its own, and its products are brought back by it.  (The unit of the
+  // logits then goes by 2^20 or the largest row, if that is smaller: both it
+  // and every row's way back are numbers FP32 holds.)  Rows whose logits may
+  // be `large` go that way too, formed 2^`by` times smaller.
   uint4v q[F];
-  float sum_q = 0.f, unit, back = 1.f;
-  bool wide;
+  float sum_q = 0.f, unit, back = 1.f, up_logits;
+  bool wide, large;
   {
     uint4v raw[F];
     uint32_t most = 0;
@@ -415,10 +419,9 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
     most = max(most, (uint32_t)__shfl_xor((int)most, 32));
     float top = most < 0x7f800000u ? __builtin_bit_cast(float, most) : 0.f;
     auto exponent = [](float x) {
-      const int e = (int)(__builtin_bit_cast(uint32_t, x) >> 23) - 127;
+      const int e = exponent_of(x);
       return e < -100 ? -100 : e;
     };
-    auto power = [](int e) { return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23); };
     const float mine = top;
     float low = top > 0.f ? top : __builtin_inff();
 #pragma unroll
@@ -436,11 +439,15 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
       top = fmaxf(top, s_top[w]);
       low = fminf(low, s_low[w]);
     }
-    wide = __builtin_amdgcn_readfirstlane(low < top * 0x1p-10f);
-    const int e = exponent(wide ? mine : top);
-    const float up = power(13 - e);
-    unit = a.scale * kLog2e * power(wide ? -13 : e - 13);
-    if (wide) back = power(e);
+    const int most_e = __builtin_amdgcn_readfirstlane(exponent(top));
+    const int by = large_by(a.scale, most_e);
+    large = by > 0;
+    wide = large || __builtin_amdgcn_readfirstlane(low < top * 0x1p-10f);
+    const int e = wide ? exponent(mine) : most_e, base = wide && most_e > 20 ? 20 : most_e;
+    const float up = power_of_two(13 - e);
+    up_logits = power_of_two(by < 127 ? by : 127);
+    unit = a.scale * (kLog2e * power_of_two(base - 13 - by > -126 ? base - 13 - by : -126));
+    if (wide) back = power_of_two(e - base > -126 ? e - base : -126);
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       _Float16 x[8];
@@ -455,7 +462,7 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
       q[f] = __builtin_bit_cast(uint4v, v);
     }
     sum_q += __shfl_xor(sum_q, 32);
-    sum_q *= unit * back;
+    sum_q = sum_q * unit * back;
   }
 
   RowSums<D> s;
@@ -479,7 +486,7 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
         if (idle || t >= range.end || t > pos_last || t + kTile <= lo_first) continue;
         const uint32_t there = st.there[2 * k] | (uint32_t)st.there[2 * k + 1] << 16;
         const bool edge = t < lo_last || t + kTile > pos_first + 1 || there != 0xffffffffu || wide;
-        attend_rows<D, BF16>(st, k, q, sum_q, back, s, there, t, edge, lo, pos);
+        attend_rows<D, BF16>(st, k, q, sum_q, back, large, up_logits, s, there, t, edge, lo, pos);
       }
       if (n + 1 < steps) {
         pr.unpack(stage[(n + 1) & 1], unit);
