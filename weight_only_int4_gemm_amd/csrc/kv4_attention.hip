@@ -195,8 +195,9 @@ struct Queries {
   float unit;  // product units to base-2 logits
   float sum;   // sum q in base-2 logits
   int lo, hi;  // keys seen: lo <= j <= hi
-  bool large;  // some row's logits may pass 2^kMostLogits (the same in all lanes):
-  float up;    // this column's are then `up` times what unit and sum make
+  float up;    // logits over what unit and sum make, 1 but for large rows, which
+               // only the path that moves the reference provides for:
+  float most_sum;  // kMostSum, or -1 if some row is large
 };
 
 // One tile.  `edge`: some of its tokens are not seen by some row.  What the
@@ -274,12 +275,11 @@ __device__ __forceinline__ void attend(const TileData<D, ROWS>& d, const Queries
     for (int i = 0; i < N; i += 2) most = fmaxf(fmaxf(most, w[i]), w[i + 1]);
   };
   weigh(logit_less_m);
-  if (q.large || __any(most > kMostWeight || sum > kMostSum)) {
+  if (__any(most > kMostWeight || sum > q.most_sum)) {
     // Move the reference: the largest weight becomes 2^8, unless that lets
     // a probability exceed 2^40 (values of scale 0).  Each logit is formed
     // once: the reference comes from the same numbers that it is then taken
     // off, so however coarse FP32 is at their size the largest keeps its weight.
-    // (Large rows come here with every tile.)
     float x[N], top = kNone;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -421,7 +421,7 @@ __device__ __forceinline__ void load_queries(Queries<D>& q, const KvAttentionArg
   e = e < -100 ? -100 : e;
   const float up = power_of_two(13 - e);
   const int by = large_by(a.scale, e);
-  q.large = __any(by > 0);
+  q.most_sum = __any(by > 0) ? -1.f : kMostSum;
   q.up = power_of_two(by < 127 ? by : 127);
   const float logits = a.scale * (kLog2e * power_of_two(e - 13 - by));
   q.unit = logits * 0x1p22f;

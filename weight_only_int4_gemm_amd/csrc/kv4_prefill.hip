@@ -216,7 +216,8 @@ __device__ __forceinline__ float logit(float ks, float product, float kz, float 
 // some token is not seen by some row; what the cache holds for it may be
 // anything, so it is taken out, not multiplied by zero.  (Rows of very unlike
 // sizes go this way too, with `back`, so that it costs the usual way nothing.)
-// AGAIN: after the reference has moved.
+// AGAIN: after the reference has moved.  most_sum: kMostSum, or -1 where the
+// logits are large and only the rare path, which moves it, provides for them.
 template <bool BF16>
 struct Weights {
   uint4v w[2];                   // [unit]
@@ -228,7 +229,8 @@ struct Weights {
 template <int D, bool BF16, bool EDGE, bool AGAIN = false>
 __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int tile,
                                       const float16v& raw, float sum_q, float back, float up,
-                                      float m, uint32_t there, int t, int lo, int hi) {
+                                      float most_sum, float m, uint32_t there, int t, int lo,
+                                      int hi) {
   const int h = (threadIdx.x & 63) >> 5;
   // known here only: the usual path must not compute masks or products
   if constexpr (EDGE) {
@@ -275,22 +277,22 @@ __device__ __forceinline__ void weigh(Weights<BF16>& o, const Stage<D>& st, int 
             pack_halves(less_low_half(w[2 * k], x), less_high_half(w[2 * k + 1], x));
     }
   }
-  o.over = most[0] > kMostHalf || most[1] > kMostHalf || o.sum > kMostSum;
+  o.over = most[0] > kMostHalf || most[1] > kMostHalf || o.sum > most_sum;
 }
 
 template <int D, bool BF16>
 __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const uint4v* q,
-                                            float sum_q, float back, bool large, float up,
+                                            float sum_q, float back, float up, float most_sum,
                                             RowSums<D>& s, uint32_t there, int t, bool edge,
                                             int lo, int hi) {
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const float16v raw = scores<D>(st, tile, q);
   Weights<BF16> o;
   if (edge)
-    weigh<D, BF16, true>(o, st, tile, raw, sum_q, back, up, s.m, there, t, lo, hi);
+    weigh<D, BF16, true>(o, st, tile, raw, sum_q, back, up, most_sum, s.m, there, t, lo, hi);
   else
-    weigh<D, BF16, false>(o, st, tile, raw, sum_q, back, up, s.m, there, t, lo, hi);
-  if (large || __any(o.over)) {
+    weigh<D, BF16, false>(o, st, tile, raw, sum_q, back, up, most_sum, s.m, there, t, lo, hi);
+  if (__any(o.over)) {
     // Move the reference, as the other kernel does, from the same logits that
     // `weigh` then takes it off.
     float top = kNone;
@@ -319,7 +321,7 @@ __device__ __forceinline__ void attend_rows(const Stage<D>& st, int tile, const 
     s.z *= f;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) s.acc[c] *= f;
-    weigh<D, BF16, true, true>(o, st, tile, raw, sum_q, back, up, s.m, there, t, lo, hi);
+    weigh<D, BF16, true, true>(o, st, tile, raw, sum_q, back, up, most_sum, s.m, there, t, lo, hi);
   }
   s.l += o.sum;
   s.z += o.z;
@@ -396,10 +398,10 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
   // of its own, and its products are brought back by it.  (The unit of the
   // logits then goes by 2^20 or the largest row, if that is smaller: both it
   // and every row's way back are numbers FP32 holds.)  Rows whose logits may
-  // be `large` go that way too, formed 2^`by` times smaller.
+  // be large go that way too, formed 2^`by` times smaller.
   uint4v q[F];
-  float sum_q = 0.f, unit, back = 1.f, up_logits;
-  bool wide, large;
+  float sum_q = 0.f, unit, back = 1.f, up_logits, most_sum;
+  bool wide;
   {
     uint4v raw[F];
     uint32_t most = 0;
@@ -441,8 +443,8 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
     }
     const int most_e = __builtin_amdgcn_readfirstlane(exponent(top));
     const int by = large_by(a.scale, most_e);
-    large = by > 0;
-    wide = large || __builtin_amdgcn_readfirstlane(low < top * 0x1p-10f);
+    most_sum = by > 0 ? -1.f : kMostSum;
+    wide = by > 0 || __builtin_amdgcn_readfirstlane(low < top * 0x1p-10f);
     const int e = wide ? exponent(mine) : most_e, base = wide && most_e > 20 ? 20 : most_e;
     const float up = power_of_two(13 - e);
     up_logits = power_of_two(by < 127 ? by : 127);
@@ -486,7 +488,8 @@ __global__ __launch_bounds__(kThreads, (D == 256 ? 1 : 2)) void kv_rows_kernel(
         if (idle || t >= range.end || t > pos_last || t + kTile <= lo_first) continue;
         const uint32_t there = st.there[2 * k] | (uint32_t)st.there[2 * k + 1] << 16;
         const bool edge = t < lo_last || t + kTile > pos_first + 1 || there != 0xffffffffu || wide;
-        attend_rows<D, BF16>(st, k, q, sum_q, back, large, up_logits, s, there, t, edge, lo, pos);
+        attend_rows<D, BF16>(st, k, q, sum_q, back, up_logits, most_sum, s, there, t, edge, lo,
+                             pos);
       }
       if (n + 1 < steps) {
         pr.unpack(stage[(n + 1) & 1], unit);
