@@ -124,7 +124,7 @@ int kv4_tables(const int32_t* lens, const int32_t* want, int32_t* table, int max
  * aligned.  Y may be X (the same strides).  positions (device, read) int32
  * [axes][T], row a at positions + a * pos_stride.  inv_freq (device, read)
  * FP64 [rot/2].  sections: host array of `axes` counts.  rot a positive
- * multiple of 16, at most D.
+ * multiple of 16, at most D.  T at most 2^26 - 4, here and in both appends.
  */
 int kv4_rope(const uint16_t* X, int64_t x_token, int64_t x_head, uint16_t* Y, int64_t y_token,
              int64_t y_head, const int32_t* positions, int64_t pos_stride,
@@ -195,7 +195,10 @@ int kv4_dequant_debug(const int32_t* slots, const uint8_t* cache, uint16_t* K, u
  * (below 0 counts as 0, above max_pages * page as that), q_start int32
  * [B + 1], ascending, within [0, T]; device, read.  scale > 0.
  *
- * max_q: no request has more queries (rows beyond are not computed).
+ * max_q: no request has more queries (rows beyond are not computed).  Sizes
+ * that come to 2^24 or more workgroups (requests times key/value heads times
+ * tiles of 128 query rows of max_q, of 16 or 8 where those are few) are
+ * refused.
  * max_len: the length the work is planned for; longer requests are right
  * too, only slower.  workspace as in w4a16_workspace_bytes: at least
  * kv4_attention_workspace_bytes, zero-filled once, left ready for the next

@@ -13,6 +13,13 @@ namespace w4a16 {
 constexpr int kKvUnit = 16;
 constexpr int kKvMinPage = 16, kKvMaxPage = 1024;
 
+// Workgroups of 256 threads that a launch takes: it has fewer than 2^32 threads.
+constexpr int64_t kKvMaxGroups = (1 << 24) - 1;
+// Tokens of a workgroup of the append kernel, where there are many, and so of
+// a call.
+constexpr int kKvAppendTokensLog = 2;
+constexpr int64_t kKvMaxAppendTokens = kKvMaxGroups << kKvAppendTokensLog;
+
 // Byte offsets inside a unit.
 template <int D>
 struct KvUnit {

@@ -129,10 +129,17 @@ int check_attention(int B, int Hq, int H, int D, int max_q, int max_len, int win
   if (B < 0 || H <= 0 || Hq <= 0 || Hq > 65535 || Hq % H) return W4A16_ERR_SHAPE;
   if (max_q < 0 || max_len < 0 || window < 0) return W4A16_ERR_SHAPE;
   if (max_q > kMaxTokens || max_len > kMaxTokens) return W4A16_ERR_SHAPE;
-  // query rows of a request, and workgroups of the grid
+  // query rows of a request, and what a plan may count
   if ((int64_t)(Hq / H) * max_q > kMaxTokens) return W4A16_ERR_SHAPE;
   if ((int64_t)B * Hq * ((max_q + 15) / 16 + 1) > kMaxTokens) return W4A16_ERR_SHAPE;
   return W4A16_OK;
+}
+
+// The plan of such a call; false if no launch takes its workgroups.
+bool plan_attention(int B, int Hq, int H, int D, int max_q, int max_len, int window, int cus,
+                    KvAttentionPlan* p) {
+  *p = make_kv_attention_plan(B, Hq, H, D, max_q, max_len, window, cus);
+  return (int64_t)B * H * p->tiles * p->splits <= kKvMaxGroups;
 }
 
 }  // namespace
@@ -189,7 +196,7 @@ int kv4_rope(const uint16_t* X, int64_t x_token, int64_t x_head, uint16_t* Y, in
              const double* inv_freq, const int* sections, int axes, int pairs, int T, int H,
              int D, int dtype, void* stream) {
   if (!good_dtype(dtype)) return W4A16_ERR_DTYPE;
-  if (T < 0 || T > kMaxTokens || H < 0 || H > 65535) return W4A16_ERR_SHAPE;
+  if (T < 0 || T > kKvMaxAppendTokens || H < 0 || H > 65535) return W4A16_ERR_SHAPE;
   if (D != 64 && D != 128 && D != 256) return W4A16_ERR_SHAPE;
   if (T == 0 || H == 0) return W4A16_OK;
   KvAppendArgs a{};
@@ -215,7 +222,7 @@ int kv4_append(const uint16_t* K, int64_t k_token, int64_t k_head, const uint16_
                int64_t v_token, int64_t v_head, const int32_t* slots, uint8_t* cache, int T,
                int H, int D, int pages, int page, int dtype, void* stream) {
   if (!good_dtype(dtype)) return W4A16_ERR_DTYPE;
-  if (T < 0 || T > kMaxTokens) return W4A16_ERR_SHAPE;
+  if (T < 0 || T > kKvMaxAppendTokens) return W4A16_ERR_SHAPE;
   int rc = check_cache(pages, H, D, page);
   if (rc != W4A16_OK) return rc;
   if (T == 0) return W4A16_OK;
@@ -243,7 +250,7 @@ int kv4_rope_append(const uint16_t* Q, int64_t q_token, int64_t q_head, const ui
                     uint8_t* cache, int T, int Hq, int H, int D, int pages, int page, int dtype,
                     void* stream) {
   if (!good_dtype(dtype)) return W4A16_ERR_DTYPE;
-  if (T < 0 || T > kMaxTokens || Hq < 0 || Hq > 65535) return W4A16_ERR_SHAPE;
+  if (T < 0 || T > kKvMaxAppendTokens || Hq < 0 || Hq > 65535) return W4A16_ERR_SHAPE;
   int rc = check_cache(pages, H, D, page);
   if (rc != W4A16_OK) return rc;
   if (T == 0) return W4A16_OK;
@@ -311,7 +318,8 @@ size_t kv4_attention_workspace_bytes(int B, int Hq, int H, int D, int max_q, int
   if (B == 0 || max_q == 0) return 0;
   const int cus = current_cus(nullptr);
   if (cus <= 0) return 0;
-  return make_kv_attention_plan(B, Hq, H, D, max_q, max_len, window, cus).workspace_bytes;
+  KvAttentionPlan p;
+  return plan_attention(B, Hq, H, D, max_q, max_len, window, cus, &p) ? p.workspace_bytes : 0;
 }
 
 int kv4_attention_describe(int B, int Hq, int H, int D, int max_q, int max_len, int window,
@@ -323,7 +331,8 @@ int kv4_attention_describe(int B, int Hq, int H, int D, int max_q, int max_len, 
   if (B == 0 || max_q == 0 || cus < 0) return W4A16_ERR_SHAPE;
   if (cus == 0) cus = current_cus(nullptr);
   if (cus <= 0) return W4A16_ERR_DEVICE;
-  const KvAttentionPlan p = make_kv_attention_plan(B, Hq, H, D, max_q, max_len, window, cus);
+  KvAttentionPlan p;
+  if (!plan_attention(B, Hq, H, D, max_q, max_len, window, cus, &p)) return W4A16_ERR_SHAPE;
   snprintf(buf, len, "kv_attention<%d,%d,%s> grid=%lld block=%d tiles=%d splits=%d chunk=%d workspace=%zu",
            D, p.row_tile, p.rows ? "rows" : "tokens", (long long)B * H * p.tiles * p.splits,
            64 * p.waves, p.tiles, p.splits, p.chunk, p.workspace_bytes);
@@ -364,7 +373,8 @@ int kv4_attention(const uint16_t* Q, int64_t q_token, int64_t q_head, const uint
   if (lse && overlap(O, out, lse, lse_bytes)) return W4A16_ERR_SHAPE;
   const int cus = current_cus(nullptr);
   if (cus <= 0) return W4A16_ERR_DEVICE;
-  const KvAttentionPlan p = make_kv_attention_plan(B, Hq, H, D, max_q, max_len, window, cus);
+  KvAttentionPlan p;
+  if (!plan_attention(B, Hq, H, D, max_q, max_len, window, cus, &p)) return W4A16_ERR_SHAPE;
   if (p.workspace_bytes > 0) {
     if (!workspace) return W4A16_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return W4A16_ERR_ALIGN;

@@ -26,7 +26,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokensLog = 2, kMaxTokens = 1 << kMaxTokensLog;  // of a workgroup
+constexpr int kMaxTokensLog = kKvAppendTokensLog, kMaxTokens = 1 << kMaxTokensLog;  // of a workgroup
 constexpr float kFifteenth = 1.0f / 15.0f;
 constexpr float kMaxHalf = 65504.0f;
 
