@@ -11,6 +11,10 @@
  * every call can be captured into a HIP graph.  Status codes are those of
  * enum w4a16_status.  `dtype` is W4A16_DTYPE_F16 or W4A16_DTYPE_BF16 and
  * covers every 16-bit tensor of a call; the cache does not depend on it.
+ * What a call writes shares no element with what else it reads or writes,
+ * save where an argument "may be" another; strided tensors may be parts of
+ * one buffer, side by side or interleaved by head or token (with strides
+ * alike, or rows apart within equal token strides).
  *
  * The stored form.  One token's keys (or values) of one head are a row
  * x[0..D).  With all arithmetic in FP32, round half to even, no contraction:

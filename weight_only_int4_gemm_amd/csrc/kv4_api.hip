@@ -63,20 +63,40 @@ size_t extent(int64_t token, int64_t head, int T, int heads, int D) {
   return ((size_t)(T - 1) * token + (size_t)(heads - 1) * head + D) * 2;
 }
 
-// Whether two such tensors of T tokens share memory.  Parts of one buffer
-// with the same token stride, such as the three parts of a fused product,
-// are told apart by where their rows lie within it.
+// Whether two such tensors of T tokens share elements.  Exact where their
+// strides are alike, as in parts of one buffer; otherwise told apart by where
+// they lie, and by where their rows lie within equal token strides.
 bool rows_overlap(const uint16_t* x, int64_t x_token, int64_t x_head, int x_heads,
                   const uint16_t* y, int64_t y_token, int64_t y_head, int y_heads, int T, int D) {
   if (!overlap(x, extent(x_token, x_head, T, x_heads, D), y,
                extent(y_token, y_head, T, y_heads, D)))
     return false;
+  // strides of dimensions of one element mean nothing
+  if (T == 1) x_token = y_token = 0;
+  if (x_heads == 1) x_head = y_head;
+  if (y_heads == 1) y_head = x_head;
+  if (x_token != y_token) return true;
+  const int64_t by =
+      (int64_t)(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x)) / 2;
   const int64_t wx = (x_heads - 1) * x_head + D, wy = (y_heads - 1) * y_head + D;
-  if (x_token != y_token || wx > x_token || wy > y_token) return true;
-  int64_t at = ((int64_t)(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x)) / 2) %
-               x_token;
-  if (at < 0) at += x_token;
-  return at < wx || at + wy > x_token;
+  if (wx <= x_token && wy <= y_token) {
+    int64_t at = by % x_token;
+    if (at < 0) at += x_token;
+    if (at >= wx && at + wy <= x_token) return false;
+  }
+  if (x_head != y_head) return true;
+  // Two rows are by + h heads + t tokens apart; for every h the nearest t.
+  for (int64_t h = -(int64_t)(x_heads - 1); h < y_heads; ++h) {
+    const int64_t off = by + h * x_head;
+    int64_t t = x_token > 0 ? -off / x_token : 0;  // towards zero: the other
+    for (int i = 0; i < 2; ++i) {                  // neighbour is further from it
+      const int64_t at = t < -(int64_t)(T - 1) ? -(int64_t)(T - 1) : t < T - 1 ? t : T - 1;
+      const int64_t apart = off + at * x_token;
+      if (apart > -D && apart < D) return true;
+      t += off < 0 ? 1 : -1;
+    }
+  }
+  return false;
 }
 
 // Fills *r; positions and inv_freq must be there.
@@ -367,9 +387,10 @@ int kv4_attention(const uint16_t* Q, int64_t q_token, int64_t q_head, const uint
       {Q, in}, {cache, bytes}, {table, (size_t)B * max_pages * 4}, {lens, (size_t)B * 4},
       {q_start, q_start ? (size_t)(B + 1) * 4 : 0}};
   for (const auto& r : read) {
-    if (r.bytes && overlap(O, out, r.p, r.bytes)) return W4A16_ERR_SHAPE;
+    if (&r != read && r.bytes && overlap(O, out, r.p, r.bytes)) return W4A16_ERR_SHAPE;
     if (lse && r.bytes && overlap(lse, lse_bytes, r.p, r.bytes)) return W4A16_ERR_SHAPE;
   }
+  if (rows_overlap(Q, q_token, q_head, Hq, O, o_token, o_head, Hq, T, D)) return W4A16_ERR_SHAPE;
   if (lse && overlap(O, out, lse, lse_bytes)) return W4A16_ERR_SHAPE;
   const int cus = current_cus(nullptr);
   if (cus <= 0) return W4A16_ERR_DEVICE;
