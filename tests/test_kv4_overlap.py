@@ -82,3 +82,15 @@ def test_rotation_is_refused_where_elements_are_shared(seed):
         accepted += rc == DEVICE
         refused += rc == SHAPE
     assert accepted > 200 and refused > 200
+
+
+def test_outputs_over_the_small_inputs():
+    """Positions, frequencies and slots are read while rows are written."""
+    lib = w4.load()
+    for name, out in (("positions", "Y"), ("inv_freq", "Y")):
+        assert lib.kv4_rope(*{**ROPE, name: ROPE[out] + 64}.values()) == SHAPE, name
+    for name in ("positions", "inv_freq", "slots"):
+        for out in ("Qout", "cache"):
+            assert lib.kv4_rope_append(*{**FUSED, name: FUSED[out] + 64}.values()) == SHAPE, name
+    assert lib.kv4_rope(*ROPE.values()) == DEVICE
+    assert lib.kv4_rope_append(*FUSED.values()) == DEVICE

@@ -124,6 +124,13 @@ int check_rope(const int32_t* positions, int64_t pos_stride, const double* inv_f
   return W4A16_OK;
 }
 
+// Whether the n bytes at p hold a position or frequency of a call of T tokens.
+bool over_rope(const void* p, size_t n, const RopeArgs& r, int axes, int T) {
+  for (int a = 0; a < axes; ++a)
+    if (overlap(p, n, r.positions + a * r.pos_stride, (size_t)T * 4)) return true;
+  return overlap(p, n, r.inv_freq, (size_t)r.half * 8);
+}
+
 int done(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_LAUNCH; }
 
 // The cache half of the append entry points.
@@ -227,6 +234,7 @@ int kv4_rope(const uint16_t* X, int64_t x_token, int64_t x_head, uint16_t* Y, in
   if (!(X == Y && x_token == y_token && x_head == y_head) &&
       rows_overlap(X, x_token, x_head, H, Y, y_token, y_head, H, T, D))
     return W4A16_ERR_SHAPE;
+  if (over_rope(Y, extent(y_token, y_head, T, H, D), a.rope, axes, T)) return W4A16_ERR_SHAPE;
   if (current_cus(nullptr) <= 0) return W4A16_ERR_DEVICE;
   a.q = Rows{X, x_token, x_head};
   a.k = a.v = a.q;
@@ -283,6 +291,8 @@ int kv4_rope_append(const uint16_t* Q, int64_t q_token, int64_t q_head, const ui
     if (rc == W4A16_OK) rc = check_out(Qout, qo_token, qo_head, T, Hq, D);
   }
   if (rc != W4A16_OK) return rc;
+  const size_t bytes = kv4_cache_bytes(pages, H, D, page);
+  if (over_rope(cache, bytes, a.rope, axes, T)) return W4A16_ERR_SHAPE;
   if (Hq > 0) {
     if (!(Q == Qout && q_token == qo_token && q_head == qo_head) &&
         rows_overlap(Q, q_token, q_head, Hq, Qout, qo_token, qo_head, Hq, T, D))
@@ -291,8 +301,8 @@ int kv4_rope_append(const uint16_t* Q, int64_t q_token, int64_t q_head, const ui
         rows_overlap(V, v_token, v_head, H, Qout, qo_token, qo_head, Hq, T, D))
       return W4A16_ERR_SHAPE;
     const size_t out = extent(qo_token, qo_head, T, Hq, D);
-    const size_t bytes = kv4_cache_bytes(pages, H, D, page);
-    if (overlap(cache, bytes, Qout, out) ||
+    if (over_rope(Qout, out, a.rope, axes, T) || overlap(Qout, out, slots, (size_t)T * 4) ||
+        overlap(cache, bytes, Qout, out) ||
         overlap(cache, bytes, Q, extent(q_token, q_head, T, Hq, D)))
       return W4A16_ERR_SHAPE;
   }
