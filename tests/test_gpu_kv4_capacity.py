@@ -97,3 +97,30 @@ def test_attention_after_a_step_that_did_not_fit_reads_stored_tokens_only(short)
                      w4.alloc_kv4_workspace(B, Hq, H, D, 1, 64))
     torch.cuda.synchronize()
     assert torch.isfinite(O.float()).all() and torch.isfinite(L).all()
+
+
+def test_the_most_requests_of_a_call_under_a_graph():
+    """4096 requests, whose sums take more shared memory than a launch gets
+    unasked, replayed in place."""
+    import torch
+    say("tables graph 4096")
+    B, page, width, capacity = w4.KV4_MAX_REQUESTS, 16, 4, 6000
+    pages = B * width
+    rng = np.random.default_rng(12)
+    table, ring, state = w4.alloc_kv4_pages(pages, B, width)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens, want = torch.zeros(B, **i32), torch.zeros(B, **i32)
+    rest = [torch.zeros(n, **i32) for n in (B + 1, capacity, capacity)]
+    held = [x.cpu().numpy() for x in (lens, table, ring, state)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w4.kv4_tables(lens, want, table, ring, state, lens, state, *rest, page)
+    for i in range(6):
+        w = np.clip(held[0] + rng.integers(-6, 4, B), 0, 64).astype(np.int32)
+        want.copy_(torch.from_numpy(w))
+        graph.replay()
+        torch.cuda.synchronize()
+        expect = ref.tables(held[0], w, *held[1:], capacity, page)
+        for name, g, e in zip(NAMES, (lens, table, ring, state, *rest), expect):
+            assert np.array_equal(g.cpu().numpy(), e), (i, name)
+        held = expect[:4]
