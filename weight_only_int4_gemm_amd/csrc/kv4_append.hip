@@ -16,8 +16,9 @@
 // What bounds it: HBM for prefills, the launch and one trip to memory for
 // decode steps.  Rotation of 16384 x 32 rows of 128, 47 us (5.7 TB/s; 54 with
 // temporal loads); 8192 tokens of 64 + 2 x 8 heads rotated and stored, 69 us (4.5);
-// 4001 x 2 x 32 heads stored, 27 us (3.7: about 120 vector instructions
-// per 16 bytes are close to the bound there); 32 tokens, 4.0 us.
+// 4001 x 2 x 32 heads stored, 27 us (3.7: by the counters a wave issues 197
+// vector instructions for its four rows, 49 thousand cycles per SIMD, 23 of
+// the 27 us); 32 tokens, 4.0 us.
 #include "../../include/w4a16_kv4.h"
 #include "format.hpp"
 #include "kv4.hpp"

@@ -44,7 +44,7 @@
 // What bounds it (D = 128): HBM in decode steps, 64 requests of 4096 tokens
 // and 32 heads 129 us (6.1 TB/s), one of 131072 tokens and 8 heads 31 us (4.6
 // TB/s: the start and the join take about 8 us); eight dependent trips to
-// memory in short calls, one of 1000 tokens and 32 heads 8.3 us; vector and
+// memory in short calls, one of 1000 tokens and 32 heads 8.5 us; vector and
 // matrix instructions, which hardly overlap, with more rows: 24 requests of 5
 // queries on windows of 4096 tokens, 32 heads on 8, D = 64, 32 us.
 #include "kv4_attention.hpp"
@@ -679,6 +679,9 @@ constexpr int64_t kMostPartBytes = ((int64_t)192 << 20) - (int64_t)kCounterHeade
 // 131072 tokens, 8 heads, 32 ranges, 31 us, 208 with 3; 500 queries over
 // 8192 tokens, 4, 137 us, 268 with one; 24 x 476 over 6597, 595 with 2, 478
 // with one.)
+// A request that holds far less than planned gets only the ranges its length
+// fills: one of 4000 tokens on 8 heads takes 9.5 us planned for 4000 tokens, 23
+// planned for 131072.
 double plan_for(KvAttentionPlan* p, int row_tile, int B, int H, int64_t rows, int D,
                 int64_t keys, int cus) {
   constexpr double kStart = 5, kJoin = 1.4, kPartsRate = 1e6, kJoinRate = 64e3;  // bytes per us
@@ -731,8 +734,10 @@ double plan_for(KvAttentionPlan* p, int row_tile, int B, int H, int64_t rows, in
 // Up to eight rows pair columns.  Beyond that tiles of 16 rows have the
 // waits of two workgroups per compute unit overlap and waste few rows; tiles
 // of 128 unpack the codes once for all, which pays when they are full and the
-// chip is (2 x 2048 queries: 0.74 ms; 32 x 128 queries over 1024 tokens, 32
+// chip is (2 x 2048 queries: 0.73 ms; 32 x 128 queries over 1024 tokens, 32
 // heads: 105 us against 187 in tiles of 16; 8 x 96 over 2048: 78 against 48).
+// Between them, at 65 to a few hundred rows per head, both are three to five
+// times off what the bytes and flops take.
 KvAttentionPlan make_kv_attention_plan(int B, int Hq, int H, int D, int max_q, int max_len,
                                        int window, int cus) {
   const int64_t rows = (int64_t)(Hq / H) * max_q;

@@ -16,13 +16,18 @@
 // take 0.34 us per wave together, 0.22 and 0.17 alone), so a tile of 32 x 32
 // scores costs their sum, 512 + about 880 cycles with D = 128, and the kernel
 // runs at 0.92 of that: 2 x 2048 queries over up to 8192 keys, 64 heads of
-// 128, BF16: 0.84 ms under the profiler, 0.72 to 0.75 without, 760 to 800
-// TFLOP/s (a 16384^3 product of the matrix library: 1364).  For
-// the same reason these did not help: two groups of waves that change places
-// between softmax and products at barriers (0.91), eight waves per workgroup
-// (0.85), the next tile's products between the softmax's instructions (0.87
-// of the time before the masks left the usual path, spills), steps of 32
-// tokens (0.93), wave priorities around the products (0.85).
+// 128, BF16: 0.81 to 0.86 ms under the profiler, 0.72 to 0.75 without, 760 to
+// 800 TFLOP/s (a 16384^3 product of the matrix library: 1364).  FP16 calls
+// have the remainders' products too, 24 for 16, and form them: 555 TFLOP/s of
+// the formula's (1.33 ms for prompts of 1.3 times the work).  BF16 with D = 64
+// reaches 440, where a score's vector instructions serve half the products,
+// and with D = 256 and one workgroup per compute unit 475.
+// For the same reason these did not help, in ms for the BF16 case: two groups
+// of waves that change places between softmax and products at barriers (0.91),
+// eight waves per workgroup (0.85), the next tile's products between the
+// softmax's instructions (0.87 of the time before the masks left the usual
+// path, spills), steps of 32 tokens (0.93), wave priorities around the products
+// (0.85).
 //
 // Operands.  Scores: keys first (rows = 32 tokens), queries second (columns =
 // 32 query rows); lane l has column l % 32 and, for i in 0..15, token
