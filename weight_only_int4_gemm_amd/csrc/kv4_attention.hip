@@ -679,6 +679,10 @@ constexpr int64_t kMostPartBytes = ((int64_t)192 << 20) - (int64_t)kCounterHeade
 // 131072 tokens, 8 heads, 32 ranges, 31 us, 208 with 3; 500 queries over
 // 8192 tokens, 4, 137 us, 268 with one; 24 x 476 over 6597, 595 with 2, 478
 // with one.)
+// The 0.65 is a guess that uneven batches need and equal ones bear: 32 requests
+// of 8192 tokens, 8 heads, take 50.1 us with it and 50.6 with 1, 8 of 32768
+// 53.1 and 51.9; a quarter to all of those lengths 40.6 and 44.6, 43.7 and 48.1;
+// 24 x 5 drafted tokens 30 and 37; 9 x 10 over 2636, 32 heads, 26 and 22.
 // A request that holds far less than planned gets only the ranges its length
 // fills: one of 4000 tokens on 8 heads takes 9.5 us planned for 4000 tokens, 23
 // planned for 131072.
