@@ -34,7 +34,9 @@ stream.  The functions carry the C interface's names (include/w4a16.h):
     w4a16_set_forced_plan(spec)          (tuning and testing only)
 
 The paged 4-bit key/value cache (``kv4_*``, include/w4a16_kv4.h) is bound in
-``kv4.py`` and exported here under the same names.
+``kv4.py`` and exported here under the same names; the products in 8-bit
+floating point (``w8a8_*``, include/w8a8.h) and the expert layers (``moe_*``,
+``*_moe_gemm``, include/w4a16_moe.h) are bound in ``moe.py``.
 
 A missing library is an error (``LibraryNotBuilt``); there is no fallback.
 """
@@ -45,10 +47,12 @@ import ctypes
 import os
 
 from . import kv4 as _kv4
+from . import moe as _moe
 from .kv4 import *  # noqa: F401,F403  (the paged 4-bit key/value cache)
+from .moe import *  # noqa: F401,F403  (8-bit products and expert layers)
 
 __all__ = [
-    *_kv4.__all__,
+    *_kv4.__all__, *_moe.__all__,
     "W4A16Error", "LibraryNotBuilt", "library_path", "load",
     "w4a16_repack", "w4a16_gemm", "w4a16_gemm_fused", "w4a16_dequant_debug",
     "W4A16_ACT_NONE", "W4A16_ACT_RELU", "W4A16_ACT_SILU",
@@ -169,6 +173,7 @@ def load():
     lib.w4a16_set_forced_plan.argtypes = [ctypes.c_char_p]
     lib.w4a16_set_forced_plan.restype = i
     _kv4.declare(lib)
+    _moe.declare(lib)
     _lib = lib
     return lib
 

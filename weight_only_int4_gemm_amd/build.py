@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libw4a16.so")
 PROBES_LIB = os.path.join(PKG, "libw4a16_probes.so")
 SOURCES = ["api.hip", "gemm.hip", "gemm_lds.hip", "gemm_sk.hip", "gemm_sk_fmt.hip", "repack.hip", "dequant.hip",
            "kv4_api.hip", "kv4_tables.hip", "kv4_append.hip", "kv4_attention.hip",
-           "kv4_prefill.hip"]
+           "kv4_prefill.hip", "moe_api.hip", "moe_route.hip", "w8a8.hip", "w4a16_moe.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

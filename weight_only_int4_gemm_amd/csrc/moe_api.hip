@@ -1,0 +1,398 @@
+// The C interface of the expert layers and of products in 8-bit floating
+// point (include/w4a16_moe.h, include/w8a8.h): argument checks, plans and
+// launches.  Nothing here allocates, prints or synchronises.
+#include <hip/hip_runtime.h>
+
+#include <cstdio>
+
+#include "internal.hpp"
+#include "moe.hpp"
+#include "product.hpp"
+#include "w4a16_moe.h"
+#include "w8a8.h"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kW8a8LayoutVersion = 1;
+constexpr int kMaxRows = 1 << 24;        // rows of one call
+constexpr int64_t kMaxGroups = 1 << 24;  // workgroups of one launch dimension
+constexpr int64_t kMaxStride = 1ll << 32;
+
+bool aligned(const void* p, int to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+struct Part {
+  const void* p;
+  size_t bytes;
+};
+
+// Whether one of the `written` first parts shares memory with another part.
+bool share(const Part* part, int written, int n) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(part[i].p),
+                      y = reinterpret_cast<uintptr_t>(part[j].p);
+      if (part[i].bytes && part[j].bytes && x < y + part[j].bytes && y < x + part[i].bytes)
+        return true;
+    }
+  return false;
+}
+
+bool good_dtype(int dtype) { return dtype == W4A16_DTYPE_F16 || dtype == W4A16_DTYPE_BF16; }
+
+// Sizes of weights: K and the columns W of one matrix.
+bool good_weights(int K, int64_t W) {
+  return K > 0 && K % kBlockK == 0 && W > 0 && W % kBlockN == 0 && W <= 0x7fffffff;
+}
+
+int done(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_LAUNCH; }
+
+int check_product(int rows, int K, int N, int E, bool gate, bool f8) {
+  if (rows < 0 || rows > kMaxRows || N < 0 || E < 1 || E > MOE_MAX_EXPERTS) return W4A16_ERR_SHAPE;
+  if (N % (gate && f8 ? 32 : 16)) return W4A16_ERR_SHAPE;
+  if (!good_weights(K, N > 0 ? (int64_t)N * (gate ? 2 : 1) : 16)) return W4A16_ERR_SHAPE;
+  return W4A16_OK;
+}
+
+bool good_plan(const ProductPlan& p) {
+  return (int64_t)p.tiles_m * p.tiles_n <= kMaxGroups;
+}
+
+int describe(int format, int rows, int K, int N, int E, bool gate, int cus, char* buf,
+             size_t len) {
+  if (!buf || len == 0) return W4A16_ERR_NULL;
+  buf[0] = 0;
+  if (rows == 0 || N == 0) return W4A16_ERR_SHAPE;
+  const int rc = check_product(rows, K, N, E > 0 ? E : 1, gate, format == kProdF8);
+  if (rc != W4A16_OK) return rc;
+  if (cus == 0) cus = current_cus(nullptr);
+  if (cus <= 0) return W4A16_ERR_DEVICE;
+  const ProductPlan p = make_product_plan(format, rows, K, N, E, gate, cus);
+  if (!good_plan(p)) return W4A16_ERR_SHAPE;
+  std::snprintf(buf, len, "%s<%d,%d,%d,%d,%d> tile=%dx%d grid=%dx%d splits=%d workspace=%zu",
+                p.tile ? "product_tile_kernel" : "product_stream_kernel", p.mb, p.nb, p.wm, p.wn,
+                p.depth, p.tm, p.tn, p.tiles_m, p.tiles_n, p.splits, p.workspace_bytes);
+  return W4A16_OK;
+}
+
+// The expert products' shared part: everything but the operands' types.
+int check_experts(const void* A, int a_rows, const int32_t* order, int k, const int32_t* starts,
+                  const void* Bpacked, const void* scales, const uint16_t* C, int rows, int K,
+                  int N, int E, int activation, int dtype, bool f8) {
+  if (!good_dtype(dtype)) return W4A16_ERR_DTYPE;
+  if (activation != MOE_ACT_NONE && activation != MOE_ACT_SILU_GATE) return W4A16_ERR_EPILOGUE;
+  const int rc = check_product(rows, K, N, E, activation == MOE_ACT_SILU_GATE, f8);
+  if (rc != W4A16_OK) return rc;
+  if (rows == 0 || N == 0) return W4A16_OK;
+  if (k < 1 || a_rows < 1 || a_rows > kMaxRows) return W4A16_ERR_SHAPE;
+  if (!A || !starts || !Bpacked || !scales || !C) return W4A16_ERR_NULL;
+  if (!aligned(A, 16) || !aligned(Bpacked, 16) || !aligned(scales, 16) || !aligned(C, 16) ||
+      !aligned(starts, 4) || !aligned(order, 4))
+    return W4A16_ERR_ALIGN;
+  return W4A16_OK;
+}
+
+}  // namespace
+
+ProductPlan make_product_plan(int format, int rows, int K, int N, int E, bool gate, int cus) {
+  ProductPlan p{};
+  const int experts = E > 0 ? E : 1;
+  const int used = rows < experts ? rows : experts;
+  const int mean = (rows + used - 1) / used;
+  p.splits = 1;
+  p.wm = 1;
+  if (mean <= 48) {
+    p.tile = 0;
+    p.wn = 8;
+    p.nb = 2;
+    p.mb = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
+    p.depth = p.mb == 4 ? 2 : 3;
+    p.tm = 16 * p.mb;
+    p.tn = 16 * p.nb;
+  } else {
+    p.tile = 1;
+    if (mean <= 64) {
+      p.mb = 4, p.nb = 2, p.wm = 1, p.wn = 4, p.depth = 4;
+    } else if (mean <= 1024) {
+      p.mb = 4, p.nb = 4, p.wm = 2, p.wn = 2, p.depth = 4;
+    } else {
+      p.mb = 8, p.nb = 4, p.wm = 2, p.wn = 4, p.depth = 2;
+    }
+    p.tm = 16 * p.mb * p.wm;
+    p.tn = 16 * p.nb * p.wn;
+  }
+  if (gate) p.tn /= 2;
+  p.tiles_n = (N + p.tn - 1) / p.tn;
+  // sum over used experts of ceil(rows / tm)
+  p.tiles_m = (int)(((int64_t)rows + (int64_t)used * (p.tm - 1)) / p.tm);
+  if (E == 0 && p.tile == 1) {
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    const int KB = K / kBlockK;
+    int splits = tiles < cus ? (int)(cus / tiles) : 1;
+    if (splits > KB / 8) splits = KB / 8;
+    if (splits > 16) splits = 16;
+    if (splits > 1 && tiles <= kMaxSplitTiles) {
+      p.splits = splits;
+      p.workspace_bytes = kCounterHeaderBytes +
+                          (size_t)tiles * splits * (16 * p.mb * p.wm) * (16 * p.nb * p.wn) * 4;
+    }
+  }
+  return p;
+}
+
+}  // namespace w4a16
+
+using namespace w4a16;
+
+extern "C" {
+
+int w8a8_layout_version(void) { return kW8a8LayoutVersion; }
+
+size_t w8a8_packed_bytes(int K, int N) { return good_weights(K, N) ? (size_t)K * N : 0; }
+
+int w8a8_repack(const uint8_t* B, uint8_t* Bpacked, int K, int N, void* stream) {
+  if (!good_weights(K, N) || (int64_t)K * N / 4096 > kMaxGroups * 16) return W4A16_ERR_SHAPE;
+  if (!B || !Bpacked) return W4A16_ERR_NULL;
+  if (!aligned(B, 16) || !aligned(Bpacked, 16)) return W4A16_ERR_ALIGN;
+  const size_t n = (size_t)K * N;
+  const Part part[] = {{Bpacked, n}, {B, n}};
+  if (share(part, 1, 2)) return W4A16_ERR_SHAPE;
+  if (current_cus(nullptr) <= 0) return W4A16_ERR_DEVICE;
+  return done(launch_w8a8_repack(B, Bpacked, K, N, static_cast<hipStream_t>(stream)));
+}
+
+int w8a8_quantize(const uint16_t* X, int64_t x_row, uint8_t* Xq, float* Xs, int T, int K,
+                  int dtype, void* stream) {
+  if (!good_dtype(dtype)) return W4A16_ERR_DTYPE;
+  if (T < 0 || T > kMaxRows || K <= 0 || K % kBlockK) return W4A16_ERR_SHAPE;
+  if (T == 0) return W4A16_OK;
+  if (T > 1 && (x_row < K || x_row > kMaxStride)) return W4A16_ERR_SHAPE;
+  if (!X || !Xq || !Xs) return W4A16_ERR_NULL;
+  if (!aligned(X, 16) || !aligned(Xq, 16) || !aligned(Xs, 16)) return W4A16_ERR_ALIGN;
+  if (T > 1 && x_row % 8) return W4A16_ERR_ALIGN;
+  if (T == 1) x_row = K;
+  const Part part[] = {{Xq, (size_t)T * K}, {Xs, (size_t)T * (K / kBlockK) * 4},
+                       {X, ((size_t)(T - 1) * x_row + K) * 2}};
+  if (share(part, 2, 3)) return W4A16_ERR_SHAPE;
+  if (current_cus(nullptr) <= 0) return W4A16_ERR_DEVICE;
+  return done(
+      launch_w8a8_quantize(X, x_row, Xq, Xs, T, K, dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t w8a8_workspace_bytes(int M, int K, int N) {
+  if (M <= 0 || N <= 0 || check_product(M, K, N, 1, false, true) != W4A16_OK) return 0;
+  const int cus = current_cus(nullptr);
+  if (cus <= 0) return 0;
+  return make_product_plan(kProdF8, M, K, N, 0, false, cus).workspace_bytes;
+}
+
+int w8a8_describe(int M, int K, int N, int cus, char* buf, size_t len) {
+  return describe(kProdF8, M, K, N, 0, false, cus, buf, len);
+}
+
+int w8a8_gemm(const uint8_t* A, const float* As, const uint8_t* Bpacked, const float* Bs,
+              uint16_t* C, int M, int K, int N, int dtype, void* workspace, void* stream) {
+  if (!good_dtype(dtype)) return W4A16_ERR_DTYPE;
+  const int rc = check_product(M, K, N, 1, false, true);
+  if (rc != W4A16_OK) return rc;
+  if (M == 0 || N == 0) return W4A16_OK;
+  if (!A || !As || !Bpacked || !Bs || !C) return W4A16_ERR_NULL;
+  const void* all[] = {A, As, Bpacked, Bs, C, workspace};
+  for (const void* q : all)
+    if (!aligned(q, 16)) return W4A16_ERR_ALIGN;
+  const size_t KB = K / kBlockK;
+  Part part[] = {{C, (size_t)M * N * 2}, {workspace, 0}, {A, (size_t)M * K},
+                 {As, (size_t)M * KB * 4}, {Bpacked, (size_t)K * N},
+                 {Bs, ((size_t)N + 127) / 128 * KB * 4}};
+  if (share(part, 2, 6)) return W4A16_ERR_SHAPE;
+  const int cus = current_cus(nullptr);
+  if (cus <= 0) return W4A16_ERR_DEVICE;
+  const ProductPlan plan = make_product_plan(kProdF8, M, K, N, 0, false, cus);
+  if (!good_plan(plan)) return W4A16_ERR_SHAPE;
+  if (plan.workspace_bytes) {
+    if (!workspace) return W4A16_ERR_WORKSPACE;
+    part[1].bytes = plan.workspace_bytes;
+    if (share(part, 2, 6)) return W4A16_ERR_SHAPE;
+  }
+  ProductArgs a{};
+  a.A = A;
+  a.As = As;
+  a.B = Bpacked;
+  a.S = Bs;
+  a.C = C;
+  a.a_rows = a.rows = M;
+  a.k = 1;
+  a.E = 1;
+  a.K = K;
+  a.N = a.W = N;
+  a.dtype = dtype;
+  a.tiles_n = plan.tiles_n;
+  a.splits = plan.splits;
+  if (plan.splits > 1) {
+    a.counters = static_cast<unsigned*>(workspace);
+    a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterHeaderBytes);
+  }
+  return done(launch_product_f8(plan, a, false, static_cast<hipStream_t>(stream)));
+}
+
+int moe_route(const void* logits, int64_t row, int logits_type, const float* bias, int32_t* ids,
+              float* weights, int T, int E, int k, int score, int groups, int top_groups,
+              int group_best, int renorm, float scale, void* stream) {
+  if (logits_type != MOE_LOGITS_F16 && logits_type != MOE_LOGITS_BF16 &&
+      logits_type != MOE_LOGITS_F32)
+    return W4A16_ERR_DTYPE;
+  if (score != MOE_SOFTMAX && score != MOE_SIGMOID) return W4A16_ERR_SHAPE;
+  if (T < 0 || T > kMaxRows || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOP || k > E)
+    return W4A16_ERR_SHAPE;
+  if (groups < 1 || groups > MOE_MAX_GROUPS || E % groups || top_groups < 1 ||
+      top_groups > groups || group_best < 1 || group_best > 2)
+    return W4A16_ERR_SHAPE;
+  if (T == 0) return W4A16_OK;
+  if (T > 1 && (row < E || row > kMaxStride)) return W4A16_ERR_SHAPE;
+  if (!logits || !ids || !weights) return W4A16_ERR_NULL;
+  const int size = logits_type == MOE_LOGITS_F32 ? 4 : 2;
+  if (!aligned(logits, size) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return W4A16_ERR_ALIGN;
+  if (T == 1) row = E;
+  const size_t out = (size_t)T * k * 4;
+  const Part part[] = {{ids, out}, {weights, out}, {logits, ((size_t)(T - 1) * row + E) * size},
+                       {bias, bias ? (size_t)E * 4 : 0}};
+  if (share(part, 2, 4)) return W4A16_ERR_SHAPE;
+  if (current_cus(nullptr) <= 0) return W4A16_ERR_DEVICE;
+  const RouteArgs a{logits, row, logits_type, bias, ids, weights, T, E, k, score,
+                    groups, top_groups, group_best, renorm, scale};
+  return done(launch_moe_route(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_tables(const int32_t* ids, int32_t* starts, int32_t* order, int32_t* where, int T, int k,
+               int E, void* stream) {
+  if (T < 0 || k < 1 || E < 1 || E > MOE_MAX_EXPERTS || (int64_t)T * k > kMaxRows)
+    return W4A16_ERR_SHAPE;
+  const size_t n = (size_t)T * k * 4;
+  if (!starts || (n && (!ids || !order || !where))) return W4A16_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(starts, 4) || !aligned(order, 4) || !aligned(where, 4))
+    return W4A16_ERR_ALIGN;
+  const Part part[] = {{starts, (size_t)(E + 1) * 4}, {order, n}, {where, n}, {ids, n}};
+  if (share(part, 3, 4)) return W4A16_ERR_SHAPE;
+  if (current_cus(nullptr) <= 0) return W4A16_ERR_DEVICE;
+  const TablesArgs a{ids, starts, order, where, T * k, E};
+  return done(launch_moe_tables(a, static_cast<hipStream_t>(stream)));
+}
+
+int w4a16_moe_gemm(const uint16_t* A, int a_rows, const int32_t* order, int k,
+                   const int32_t* starts, const uint32_t* Bpacked, const uint16_t* scales,
+                   uint16_t* C, int rows, int K, int N, int group, int E, int activation,
+                   int dtype, void* stream) {
+  int rc = check_experts(A, a_rows, order, k, starts, Bpacked, scales, C, rows, K, N, E,
+                         activation, dtype, false);
+  if (rc != W4A16_OK) return rc;
+  if (group <= 0 || group % kBlockK || K % group) return W4A16_ERR_GROUP;
+  if (rows == 0 || N == 0) return W4A16_OK;
+  const bool gate = activation == MOE_ACT_SILU_GATE;
+  const int W = N * (gate ? 2 : 1);
+  const size_t weights = (size_t)K * W / 2, scale_count = (size_t)(K / group) * W;
+  const Part part[] = {{C, (size_t)rows * N * 2}, {A, (size_t)a_rows * K * 2},
+                       {order, order ? (size_t)rows * 4 : 0}, {starts, (size_t)(E + 1) * 4},
+                       {Bpacked, weights * E}, {scales, scale_count * E * 2}};
+  if (share(part, 1, 6)) return W4A16_ERR_SHAPE;
+  const int cus = current_cus(nullptr);
+  if (cus <= 0) return W4A16_ERR_DEVICE;
+  const int format = dtype == W4A16_DTYPE_BF16 ? kProdI4Bf16 : kProdI4F16;
+  const ProductPlan plan = make_product_plan(format, rows, K, N, E, gate, cus);
+  if (!good_plan(plan)) return W4A16_ERR_SHAPE;
+  ProductArgs a{};
+  a.A = reinterpret_cast<const uint8_t*>(A);
+  a.order = order;
+  a.starts = starts;
+  a.B = reinterpret_cast<const uint8_t*>(Bpacked);
+  a.S = scales;
+  a.C = C;
+  a.b_expert = (int64_t)weights;
+  a.s_expert = (int64_t)scale_count;
+  a.a_rows = a_rows;
+  a.k = k;
+  a.E = E;
+  a.rows = rows;
+  a.K = K;
+  a.N = N;
+  a.W = W;
+  a.dtype = dtype;
+  const uint32_t per = (uint32_t)(group / kBlockK);
+  a.gmagic = ((1ull << 32) + per - 1) / per;
+  a.tiles_n = plan.tiles_n;
+  a.splits = 1;
+  return done(launch_product_i4(plan, a, gate, static_cast<hipStream_t>(stream)));
+}
+
+int w8a8_moe_gemm(const uint8_t* A, const float* As, int a_rows, const int32_t* order, int k,
+                  const int32_t* starts, const uint8_t* Bpacked, const float* Bs, uint16_t* C,
+                  int rows, int K, int N, int E, int activation, int dtype, void* stream) {
+  int rc = check_experts(A, a_rows, order, k, starts, Bpacked, Bs, C, rows, K, N, E, activation,
+                         dtype, true);
+  if (rc != W4A16_OK || rows == 0 || N == 0) return rc;
+  if (!As) return W4A16_ERR_NULL;
+  if (!aligned(As, 16)) return W4A16_ERR_ALIGN;
+  const bool gate = activation == MOE_ACT_SILU_GATE;
+  const int W = N * (gate ? 2 : 1);
+  const size_t KB = K / kBlockK, scale_count = ((size_t)W + 127) / 128 * KB;
+  const Part part[] = {{C, (size_t)rows * N * 2}, {A, (size_t)a_rows * K},
+                       {As, (size_t)a_rows * KB * 4}, {order, order ? (size_t)rows * 4 : 0},
+                       {starts, (size_t)(E + 1) * 4}, {Bpacked, (size_t)K * W * E},
+                       {Bs, scale_count * E * 4}};
+  if (share(part, 1, 7)) return W4A16_ERR_SHAPE;
+  const int cus = current_cus(nullptr);
+  if (cus <= 0) return W4A16_ERR_DEVICE;
+  const ProductPlan plan = make_product_plan(kProdF8, rows, K, N, E, gate, cus);
+  if (!good_plan(plan)) return W4A16_ERR_SHAPE;
+  ProductArgs a{};
+  a.A = A;
+  a.As = As;
+  a.order = order;
+  a.starts = starts;
+  a.B = Bpacked;
+  a.S = Bs;
+  a.C = C;
+  a.b_expert = (int64_t)K * W;
+  a.s_expert = (int64_t)scale_count;
+  a.a_rows = a_rows;
+  a.k = k;
+  a.E = E;
+  a.rows = rows;
+  a.K = K;
+  a.N = N;
+  a.W = W;
+  a.dtype = dtype;
+  a.tiles_n = plan.tiles_n;
+  a.splits = 1;
+  return done(launch_product_f8(plan, a, gate, static_cast<hipStream_t>(stream)));
+}
+
+int moe_gemm_describe(int form, int rows, int K, int N, int E, int activation, int cus, char* buf,
+                      size_t len) {
+  if (form != 4 && form != 8) return W4A16_ERR_SHAPE;
+  if (activation != MOE_ACT_NONE && activation != MOE_ACT_SILU_GATE) return W4A16_ERR_EPILOGUE;
+  if (E < 1) return W4A16_ERR_SHAPE;
+  return describe(form == 4 ? kProdI4F16 : kProdF8, rows, K, N, E,
+                  activation == MOE_ACT_SILU_GATE, cus, buf, len);
+}
+
+int moe_combine(const uint16_t* Y, int rows, const int32_t* where, const float* weights,
+                uint16_t* out, int T, int k, int N, int dtype, void* stream) {
+  if (!good_dtype(dtype)) return W4A16_ERR_DTYPE;
+  if (T < 0 || T > kMaxRows || k < 1 || k > MOE_MAX_TOP || N < 0 || N % 8 || rows < 0 ||
+      rows > kMaxRows)
+    return W4A16_ERR_SHAPE;
+  if (T == 0 || N == 0) return W4A16_OK;
+  if ((!Y && rows > 0) || !where || !weights || !out) return W4A16_ERR_NULL;
+  if (!aligned(Y, 16) || !aligned(out, 16) || !aligned(where, 4) || !aligned(weights, 4))
+    return W4A16_ERR_ALIGN;
+  const size_t n = (size_t)T * k * 4;
+  const Part part[] = {{out, (size_t)T * N * 2}, {Y, (size_t)rows * N * 2}, {where, n},
+                       {weights, n}};
+  if (share(part, 1, 4)) return W4A16_ERR_SHAPE;
+  if (current_cus(nullptr) <= 0) return W4A16_ERR_DEVICE;
+  const CombineArgs a{Y, where, weights, out, rows, T, k, N, dtype};
+  return done(launch_moe_combine(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
