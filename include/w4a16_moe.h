@@ -132,7 +132,8 @@ int moe_tables(const int32_t* ids, int32_t* starts, int32_t* order, int32_t* whe
  *         range keep what they hold.
  * rows    >= 0, K a positive multiple of 128, N >= 0 a multiple of 16 (0 rows
  *         or columns: nothing is launched), group a multiple of 128 that
- *         divides K, E 1..MOE_MAX_EXPERTS, k >= 1, a_rows >= 1.
+ *         divides K, E 1..MOE_MAX_EXPERTS, k >= 1, a_rows >= 1.  At most 2^24
+ *         rows and a_rows, K 2^20, W 2^24, K * W 2^36.
  * Numerics: products accumulate in FP32; weights are the exact (q - 8) with
  *         the scale on the FP32 sums of 128, or rounded once to `dtype` from
  *         (q - 8) * s, by the shape (both are the product up to rounding);

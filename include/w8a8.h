@@ -44,7 +44,8 @@ size_t w8a8_packed_bytes(int K, int N);
  * Bpacked (device, write) K * N bytes, layout version 1: code (n, k) is byte
  *                           ((n/16 * K/128 + k/128) * 2 + k%128/64) * 1024
  *                           + (n%16 + 16 * (k%64/16)) * 16 + k%16.
- * K       positive multiple of 128.   N  positive multiple of 16.
+ * K       positive multiple of 128, at most 2^20.   N  positive multiple of 16,
+ *         at most 2^24.   K * N at most 2^36.
  * Errors: W4A16_ERR_NULL, _SHAPE (sizes, or B and Bpacked overlapping),
  *         _ALIGN, _DEVICE, _LAUNCH.
  */
@@ -89,7 +90,8 @@ int w8a8_describe(int M, int K, int N, int cus, char* buf, size_t len);
  * Bs        (device, read)  FP32 [ceil(N/128)][K/128].
  * C         (device, write) `dtype` [M][N].
  * M         >= 0, N >= 0 a multiple of 16 (0 of either: nothing is launched),
- *           K a positive multiple of 128.
+ *           K a positive multiple of 128; K and N as w8a8_repack takes them, M at
+ *           most 2^24.
  * workspace (device, read/write) see w8a8_workspace_bytes; may be NULL only
  *           where that returns 0.
  * Numerics: the products of a block are summed by the matrix instruction in

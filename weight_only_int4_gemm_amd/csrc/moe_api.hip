@@ -40,9 +40,12 @@ bool share(const Part* part, int written, int n) {
 
 bool good_dtype(int dtype) { return dtype == W4A16_DTYPE_F16 || dtype == W4A16_DTYPE_BF16; }
 
-// Sizes of weights: K and the columns W of one matrix.
+// Sizes of weights: K and the columns W of one matrix.  Offsets in the
+// kernels are 32 bits from a wave's first column block (K) and over the scales
+// of one matrix.
 bool good_weights(int K, int64_t W) {
-  return K > 0 && K % kBlockK == 0 && W > 0 && W % kBlockN == 0 && W <= 0x7fffffff;
+  return K > 0 && K % kBlockK == 0 && K <= (1 << 20) && W > 0 && W % kBlockN == 0 &&
+         W <= (1ll << 36) / K && W <= (1 << 24);
 }
 
 int done(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_LAUNCH; }
@@ -113,10 +116,12 @@ ProductPlan make_product_plan(int format, int rows, int K, int N, int E, bool ga
     p.tile = 1;
     if (mean <= 64) {
       p.mb = 4, p.nb = 2, p.wm = 1, p.wn = 4, p.depth = 4;
-    } else if (mean <= 1024) {
+    } else if (format != kProdF8) {
+      p.mb = 8, p.nb = 2, p.wm = 1, p.wn = 8, p.depth = 2;
+    } else if (mean <= 400) {
       p.mb = 4, p.nb = 4, p.wm = 2, p.wn = 2, p.depth = 4;
     } else {
-      p.mb = 8, p.nb = 4, p.wm = 2, p.wn = 4, p.depth = 2;
+      p.mb = 8, p.nb = 4, p.wm = 2, p.wn = 4, p.depth = 4;
     }
     p.tm = 16 * p.mb * p.wm;
     p.tn = 16 * p.nb * p.wn;

@@ -125,7 +125,10 @@ __device__ __forceinline__ RowTile row_tile(const ProductArgs& p, const RowTiles
   for (;; ++e) {
     const int lo = start_of(p, e), hi = start_of(p, e + 1);
     const int n = hi > lo ? (hi - lo + tm - 1) / tm : 0;
-    if (left < n || e + 1 >= p.E) return RowTile{e, lo + left * tm, hi};
+    if (left < n || e + 1 >= p.E)
+      return RowTile{__builtin_amdgcn_readfirstlane(e),
+                     __builtin_amdgcn_readfirstlane(lo + left * tm),
+                     __builtin_amdgcn_readfirstlane(hi)};
     left -= n;
   }
 }
@@ -385,18 +388,12 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
   constexpr int TM = 16 * MB * WM;
   constexpr int OB = GATE ? NB / 2 : NB;        // output column blocks of a wave
   constexpr int SUB = P::kRowBlock / 128;       // 128-byte slices of a row's K block
-  constexpr int CHUNKS = SUB * TM / 8;          // wave-loads (1 KiB) of activations
-  constexpr int ALOADS = (CHUNKS + WAVES - 1) / WAVES;
-  constexpr int SROWS = P::kF8 ? (TM < 64 ? 64 : TM) : 64;
-  constexpr int SLOADS = P::kF8 ? 1 : 0;        // every wave issues one
-  constexpr int LOADS = ALOADS + SLOADS;
+  constexpr int ALOADS = SUB * ((TM / 8 + WAVES - 1) / WAVES);  // 1 KiB loads of a wave
   static_assert(NS == 2 || NS == 4, "two or four stages");
-  static_assert(SROWS / 64 <= WAVES, "one scale load a wave");
   // piece c of row r of a slice at slot c ^ (r & 7): a fragment read's lanes
   // spread over all banks
   struct Stage {
     uint4 a[SUB * TM * 8];
-    float as[SROWS];
   };
   // one LDS object per stage: the compiler sees that a load into one stage
   // does not touch the others
@@ -404,6 +401,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
   __shared__ Stage st1;
   __shared__ typename std::conditional<(NS > 2), Stage, char>::type st2;
   __shared__ typename std::conditional<(NS > 2), Stage, char>::type st3;
+  // e4m3: the rows' scales of four K blocks, and of the next four
+  __shared__ float4_t row_scales[2][P::kF8 ? TM : 1];
 
   const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -422,68 +421,102 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
   const int kb0 = (int)((int64_t)KB * split / p.splits);
   const int kb1 = (int)((int64_t)KB * (split + 1) / p.splits);
 
-  // Activation loads: chunk (wave + WAVES i) of a stage, 8 rows of a slice.
-  const uint8_t* asrc[ALOADS];
+  // Activation loads: eight rows of a slice each.
+  constexpr int RLOADS = (TM / 8 + WAVES - 1) / WAVES;  // of one slice
+  const uint8_t* asrc[RLOADS];
 #pragma unroll
-  for (int i = 0; i < ALOADS; ++i) {
-    const int chunk = (wave + WAVES * i) % CHUNKS;
-    const int slice = chunk / (TM / 8), r = chunk % (TM / 8) * 8 + (lane >> 3);
+  for (int i = 0; i < RLOADS; ++i) {
+    const int r = (wave + WAVES * i) % (TM / 8) * 8 + (lane >> 3);
     const int q = rt.row0 + r;
     const int src = source_row(p, q < rt.end ? q : rt.end - 1);
-    asrc[i] = p.A + (int64_t)src * KB * P::kRowBlock + slice * 128 + ((lane & 7) ^ (r & 7)) * 16;
+    asrc[i] = p.A + (int64_t)src * KB * P::kRowBlock + ((lane & 7) ^ (r & 7)) * 16;
   }
+  // Row scales come four K blocks at a time (a lane reads 16 bytes of its
+  // row): loaded block by block, each 4-byte access of a scattered row takes
+  // the cache path as long as 64 contiguous bytes (8192 x 28672 at M = 4096:
+  // 998 -> 981 us, and 934 with four stages).  TM / WAVES lanes of a wave load one row each; the last group,
+  // where the row may end, goes through registers.
+  constexpr int SROWS = TM / WAVES;
   const float* scale_src = nullptr;
   if constexpr (P::kF8) {
-    const int r = wave % (SROWS / 64) * 64 + lane;
-    const int q = rt.row0 + (r < TM ? r : TM - 1);
+    const int q = rt.row0 + wave * SROWS + (lane < SROWS ? lane : SROWS - 1);
     scale_src = p.As + (int64_t)source_row(p, q < rt.end ? q : rt.end - 1) * KB;
   }
-  auto load_stage = [&](Stage& sg, int kb) {
+  auto load_scales = [&](int buffer, int kb) {
+    if constexpr (P::kF8) {
+      if (kb + 4 <= KB) {
+        if (lane < SROWS)
+          __builtin_amdgcn_global_load_lds((global_ptr_t)(scale_src + kb),
+                                           (lds_ptr_t)&row_scales[buffer][wave * SROWS], 16, 0, 0);
+      } else if (kb < KB) {
+        float4_t v;
 #pragma unroll
-    for (int i = 0; i < ALOADS; ++i) {
-      const int chunk = (wave + WAVES * i) % CHUNKS;
-      __builtin_amdgcn_global_load_lds((global_ptr_t)(asrc[i] + kb * P::kRowBlock),
-                                       (lds_ptr_t)&sg.a[64 * chunk], 16, 0, 0);
+        for (int i = 0; i < 4; ++i) v[i] = scale_src[kb + i < KB ? kb + i : KB - 1];
+        if (lane < SROWS) row_scales[buffer][wave * SROWS + lane] = v;
+      }
     }
-    if constexpr (P::kF8)
-      __builtin_amdgcn_global_load_lds((global_ptr_t)(scale_src + kb),
-                                       (lds_ptr_t)&sg.as[64 * (wave % (SROWS / 64))], 4, 0, 0);
+  };
+  // Load i < ALOADS of a stage.
+  auto load_rows = [&](Stage& sg, int kb, int i) {
+    const uint8_t* src = asrc[i / SUB] + kb * P::kRowBlock + (i % SUB) * 128;
+    uint4* const to = &sg.a[(i % SUB) * TM * 8 + 64 * ((wave + WAVES * (i / SUB)) % (TM / 8))];
+    __builtin_amdgcn_global_load_lds((global_ptr_t)src, (lds_ptr_t)to, 16, 0, 0);
   };
 
-  // Weights of a wave: blocks past the last re-read it (never stored).
+  // Weights of a wave: blocks past the last re-read it (never stored).  Their
+  // addresses are the wave's own but for the lane's 16 bytes, so buffer loads
+  // keep them in scalar registers; one resource for the gate columns, one for
+  // the up columns, both from the wave's first block.
   const int ob0 = (tile_n * WN + wn) * OB;  // first output column block
-  int block[NB];
-  const uint8_t* bsrc[NB];
+  const int blocks = p.N / 16, first = ob0 < blocks ? ob0 : blocks - 1;
+  constexpr int HALVES = GATE ? 2 : 1;
+  const uint32_t lane16 = lane * 16;
+  __amdgpu_buffer_rsrc_t bsrc[HALVES];
+  int boff[OB];
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int ob = ob0 + nb % OB, last = p.N / 16 - 1;
-    block[nb] = (ob < last ? ob : last) + (nb >= OB ? p.N / 16 : 0);
-    bsrc[nb] = p.B + rt.e * p.b_expert + (int64_t)block[nb] * KB * P::kBBlock + lane * 16;
+  for (int i = 0; i < HALVES; ++i)
+    bsrc[i] = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(p.B) + rt.e * p.b_expert +
+            (int64_t)(first + i * blocks) * KB * P::kBBlock,
+        (short)0, 0x7fffffff, 0x00020000);
+#pragma unroll
+  for (int i = 0; i < OB; ++i)
+    boff[i] = ((first + i < blocks ? first + i : blocks - 1) - first) * KB * P::kBBlock;
+  // e4m3: a wave's columns lie in one 128-column block of scales (with GATE,
+  // one of each half).  4 bits: the scale of the lane's column.
+  constexpr int SCALES = P::kF8 ? HALVES : NB;
+  const float* fsrc[HALVES];
+  const __amdgpu_buffer_rsrc_t ssrc = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(static_cast<const uint16_t*>(p.S)) + rt.e * p.s_expert, (short)0,
+      0x7fffffff, 0x00020000);
+  if constexpr (P::kF8) {
+#pragma unroll
+    for (int i = 0; i < HALVES; ++i)
+      fsrc[i] = static_cast<const float*>(p.S) + rt.e * p.s_expert +
+                (int64_t)((first + i * blocks) >> 3) * KB;
   }
-  constexpr int SCALES = P::kF8 ? (GATE ? 2 : 1) : NB;
   struct Weights {
     uint4 b[NB][P::kBPieces];
-    float bs[SCALES];
-    uint16_t s[SCALES];
+    uint32_t s[SCALES];  // FP32 bits, or 16 bits
   };
-  auto load_weights = [&](Weights& w, int kb) {
+  // Load i < WLOADS of a K block's weights: a column block's, or a scale.
+  constexpr int WLOADS = NB + SCALES;
+  auto load_weights = [&](Weights& w, int kb, int i) {
+    if (i < NB) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < P::kBPieces; ++i)
-        w.b[nb][i] = *reinterpret_cast<const uint4*>(bsrc[nb] + (int64_t)kb * P::kBBlock + i * 1024);
-    if constexpr (P::kF8) {
-      // A wave's columns lie in one 128-column block of scales (with GATE,
-      // one of each half).
-      const float* S = static_cast<const float*>(p.S) + rt.e * p.s_expert;
-#pragma unroll
-      for (int i = 0; i < SCALES; ++i) w.bs[i] = S[(block[i * OB] >> 3) * KB + kb];
+      for (int piece = 0; piece < P::kBPieces; ++piece)
+        w.b[i][piece] = __builtin_bit_cast(
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(bsrc[i / OB], lane16 + piece * 1024,
+                                                         boff[i % OB] + kb * P::kBBlock, 0));
+    } else if constexpr (P::kF8) {
+      const int h = i - NB;
+      w.s[h] = __builtin_bit_cast(uint32_t, fsrc[h][kb]);
     } else {
+      const int nb = i - NB;
       const int group = (int)(((uint64_t)(uint32_t)kb * p.gmagic) >> 32);
-      const uint16_t* S = static_cast<const uint16_t*>(p.S) + rt.e * p.s_expert +
-                          (int64_t)group * p.W;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) w.s[nb] = S[16 * block[nb] + l16];
+      const int ob = first + nb % OB < blocks ? first + nb % OB : blocks - 1;
+      w.s[nb] = __builtin_amdgcn_raw_buffer_load_b16(
+          ssrc, l16 * 2, (group * p.W + 16 * (ob + (nb >= OB ? blocks : 0))) * 2, 0);
     }
   };
 
@@ -494,71 +527,162 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = float4_t{0.f, 0.f, 0.f, 0.f};
   const float4_t zero = {0.f, 0.f, 0.f, 0.f};
 
-  auto multiply = [&](const Stage& sg, const Weights& w) {
+  constexpr int LOADS = WLOADS + ALOADS;
+  // Rows of a wave are 16 apart, so a lane's swizzle is one number.
+  const int l7 = l16 & 7, arow0 = (wm * MB * 16 + l16) * 8;
+  const int swz0 = arow0 + (quarter ^ l7), swz1 = arow0 + ((quarter + 4) ^ l7);
+  // u: the K block's place in its group of four; sc: the group's row scales;
+  // issue(i): the i-th of the loads for later K blocks.  They are spread over
+  // the matrix instructions: issued together, the waves' loads queue for the
+  // address unit before any of them multiplies (8192 x 28672 at M = 4096: 999
+  // -> 873 us).
+  auto multiply = [&](const Stage& sg, Weights& w, int u, const float4_t* sc, auto&& issue) {
     if constexpr (P::kF8) {
+      // Every K block has its own scales, so each matrix instruction starts
+      // from zero and its sums are added with one multiply-add each.  These
+      // follow LAG instructions later, when the sums are there; row block
+      // mb + 1 is read while mb is multiplied.
+      constexpr int LAG = 2, RING = 4;
+      uint4 a[2][2];
+      float as[2], f[2][SCALES];
+      float4_t d[RING];
+      auto read = [&](int mb) {
+        a[mb & 1][0] = sg.a[swz0 + mb * 128];
+        a[mb & 1][1] = sg.a[swz1 + mb * 128];
+        as[mb & 1] = reinterpret_cast<const float*>(sc + wm * MB * 16 + l16 + mb * 16)[u];
+      };
+      auto add = [&](int i) {
+        const int mb = i / NB, nb = i % NB;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[mb][nb][e] = __builtin_fmaf(d[i % RING][e], f[mb & 1][nb / OB], acc[mb][nb][e]);
+        asm volatile("" : "+v"(acc[mb][nb]));  // here, not where the loop ends
+      };
+      read(0);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
-        const int r = (wm * MB + mb) * 16 + l16;
-        const uint4 a0 = sg.a[r * 8 + (quarter ^ (r & 7))];
-        const uint4 a1 = sg.a[r * 8 + ((quarter + 4) ^ (r & 7))];
-        const float as = sg.as[r];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const float4_t d = mma_f8(w.b[nb][0], w.b[nb][1], a0, a1, zero);
-          const float f = as * w.bs[nb / OB];
+          const int i = mb * NB + nb;
+          d[i % RING] = mma_f8(w.b[nb][0], w.b[nb][1], a[mb & 1][0], a[mb & 1][1], zero);
+          __builtin_amdgcn_sched_barrier(0);
+          if (nb == LAG - 1)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[mb][nb][i] = __builtin_fmaf(d[i], f, acc[mb][nb][i]);
+            for (int s = 0; s < SCALES; ++s) f[mb & 1][s] = as[mb & 1] * __builtin_bit_cast(float, w.s[s]);
+          if (i >= LAG) add(i - LAG);
+          if (nb == 0 && mb + 1 < MB) read(mb + 1);
+          constexpr int EVERY = MB * NB / LOADS > 0 ? MB * NB / LOADS : 1;
+          if (i % EVERY == EVERY - 1 && i / EVERY < LOADS) issue(i / EVERY);
+          __builtin_amdgcn_sched_barrier(0);  // in this order
         }
       }
+#pragma unroll
+      for (int i = MB * NB - LAG; i < MB * NB; ++i) add(i);
+#pragma unroll
+      for (int i = MB * NB; i < LOADS; ++i) issue(i);
     } else {
       ColParams c[NB];
 #pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const _Float16 s = __builtin_bit_cast(_Float16, (uint16_t)w.s[nb]);
+        c[nb] = make_col<P::kFmt>(half2_t{s, s}, 8);
+      }
+      // While slice j is multiplied, slice j + 1 is unpacked; fragments are
+      // read AHEAD row blocks before their use.
+      constexpr int AHEAD = 3;
+      half8_t wt[2][NB];
+      half8_t a[AHEAD + 1];
+      auto read = [&](int i) {  // row block i % MB of slice i / MB
+        const int j = i / MB, mb = i % MB;
+        a[i % (AHEAD + 1)] = __builtin_bit_cast(
+            half8_t, sg.a[(j >> 1) * TM * 8 + ((j & 1) ? swz1 : swz0) + mb * 128]);
+      };
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) read(i);
+#pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-        c[nb] = make_col<P::kFmt>(
-            __builtin_bit_cast(half2_t, (uint32_t)w.s[nb] | ((uint32_t)w.s[nb] << 16)), 8);
+        wt[0][nb] = unpack_col<P::kFmt>(word_of(w.b[nb][0], 0), c[nb]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        half8_t wt[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) wt[nb] = unpack_col<P::kFmt>(word_of(w.b[nb][0], j), c[nb]);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-          const int r = (wm * MB + mb) * 16 + l16;
-          const half8_t a = __builtin_bit_cast(
-              half8_t, sg.a[(j >> 1) * TM * 8 + r * 8 + ((4 * (j & 1) + quarter) ^ (r & 7))]);
+          const int i = j * MB + mb;
+          if (i + AHEAD < 4 * MB) read(i + AHEAD);
+          if (j < 3 && mb * NB % MB == 0) {
+            const int nb = mb * NB / MB;
+            wt[(j + 1) & 1][nb] = unpack_col<P::kFmt>(word_of(w.b[nb][0], j + 1), c[nb]);
+          }
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mma16<P::kFmt>(wt[nb], a, acc[mb][nb]);
+          for (int nb = 0; nb < NB; ++nb)
+            acc[mb][nb] = mma16<P::kFmt>(wt[j & 1][nb], a[i % (AHEAD + 1)], acc[mb][nb]);
+          // activations in the first three slices, weights (whose registers
+          // the last unpacking frees) in the last
+          if (j < 3) {
+            constexpr int EVERY = 3 * MB / ALOADS > 0 ? 3 * MB / ALOADS : 1;
+            if (i % EVERY == EVERY - 1 && i / EVERY < ALOADS) issue(i / EVERY);
+          } else {
+            constexpr int EACH = (WLOADS + MB - 1) / MB;
+#pragma unroll
+            for (int n = mb * EACH; n < (mb + 1) * EACH && n < WLOADS; ++n) issue(ALOADS + n);
+          }
+          if ((mb + 1) * NB % MB == 0) __builtin_amdgcn_sched_barrier(0);
         }
       }
+#pragma unroll
+      for (int i = 3 * MB; i < ALOADS; ++i) issue(i);
     }
   };
 
-  // Weights of K block kb + 1 are loaded into registers and the stage of
-  // kb + NS - 1 into LDS, in this order, while block kb is multiplied: what
-  // block kb waits for is older than the newest stage's loads.
-  Stage* stages[4] = {&st0, &st1, reinterpret_cast<Stage*>(&st2), reinterpret_cast<Stage*>(&st3)};
-  Weights weights[2];
+  // While K block kb is multiplied, the stage of kb + NS - 1 is loaded into
+  // LDS and the weights of kb + 1 into registers.  e4m3: the weights first, so
+  // that what block kb + 1 waits for is older than the newest stage's loads.
+  // 4 bits: the weights last, when the registers of block kb's are free.
+  auto stage = [&](int i) -> Stage& {
+    if constexpr (NS > 2)
+      return i == 0 ? st0 : i == 1 ? st1 : i == 2 ? st2 : st3;
+    else
+      return i == 0 ? st0 : st1;
+  };
+  constexpr int SETS = P::kF8 ? 2 : 1;
+  constexpr int UNROLL = P::kF8 ? 4 : NS;
+  Weights weights[SETS];
   auto upto = [&](int kb) { return kb < kb1 ? kb : kb1 - 1; };
+  auto load_stage = [&](Stage& sg, int kb) {
 #pragma unroll
-  for (int i = 0; i < NS - 2; ++i) load_stage(*stages[i], upto(kb0 + i));
-  load_weights(weights[0], kb0);
+    for (int i = 0; i < ALOADS; ++i) load_rows(sg, kb, i);
+  };
+  load_scales(0, kb0);
+#pragma unroll
+  for (int i = 0; i < NS - 2; ++i) load_stage(stage(i), upto(kb0 + i));
   keep_load_order();
-  load_stage(*stages[NS - 2], upto(kb0 + NS - 2));
+#pragma unroll
+  for (int i = 0; i < WLOADS; ++i) load_weights(weights[0], kb0, i);
+  keep_load_order();
+  load_stage(stage(NS - 2), upto(kb0 + NS - 2));
+  int buffer = 0;
   auto step = [&](int u, int kb) {
-    stage_barrier<(NS > 2 ? LOADS : 0)>();
-    load_weights(weights[(u + 1) & 1], upto(kb + 1));
-    keep_load_order();
-    load_stage(*stages[(u + NS - 1) % NS], upto(kb + NS - 1));
-    keep_load_order();
-    multiply(*stages[u], weights[u & 1]);
+    stage_barrier<(P::kF8 && NS > 2 ? ALOADS : 0)>();
+    if (P::kF8 && u == 0) load_scales(buffer ^ 1, kb + 4);
+    const int kb_w = upto(kb + 1), kb_a = upto(kb + NS - 1);
+    multiply(stage(u % NS), weights[u % SETS], u, row_scales[buffer], [&](int i) {
+      const bool rows = P::kF8 ? i >= WLOADS : i < ALOADS;
+      if (rows)
+        load_rows(stage((u + NS - 1) % NS), kb_a, P::kF8 ? i - WLOADS : i);
+      else
+        load_weights(weights[(u + 1) % SETS], kb_w, P::kF8 ? i : i - ALOADS);
+      keep_load_order();
+    });
   };
   int kb = kb0;
-  for (; kb + NS <= kb1; kb += NS) {
+  for (; kb + UNROLL <= kb1; kb += UNROLL) {
 #pragma unroll
-    for (int u = 0; u < NS; ++u) step(u, kb + u);
+    for (int u = 0; u < UNROLL; ++u) step(u, kb + u);
+    buffer ^= 1;
   }
 #pragma unroll
-  for (int u = 0; u < NS - 1; ++u)
+  for (int u = 0; u < UNROLL - 1; ++u)
     if (kb + u < kb1) step(u, kb + u);
   // no direct load may still be landing in LDS when the workgroup ends
   __builtin_amdgcn_s_waitcnt(0);

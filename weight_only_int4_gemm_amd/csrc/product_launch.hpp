@@ -10,7 +10,8 @@ namespace w4a16 {
 // columns share a workgroup.
 #define W4A16_STREAM_VARIANTS(X) X(1, 2, 8, 3) X(2, 2, 8, 3) X(4, 2, 8, 2)
 // Tile kernel: (MB, NB, WM, WN, NS).
-#define W4A16_TILE_VARIANTS(X) X(4, 2, 1, 4, 4) X(4, 4, 2, 2, 4) X(8, 4, 2, 4, 2)
+#define W4A16_TILE_F8(X) X(4, 2, 1, 4, 4) X(4, 4, 2, 2, 4) X(8, 4, 2, 4, 4)
+#define W4A16_TILE_I4(X) X(4, 2, 1, 4, 4) X(8, 2, 1, 8, 2)
 
 template <int F>
 hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool gate,
@@ -43,7 +44,11 @@ hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool ga
                          stream, a);                                                             \
     return hipGetLastError();                                                                    \
   }
-  W4A16_TILE_VARIANTS(W4A16_CASE)
+  if constexpr (F == kProdF8) {
+    W4A16_TILE_F8(W4A16_CASE)
+  } else {
+    W4A16_TILE_I4(W4A16_CASE)
+  }
 #undef W4A16_CASE
   return hipErrorInvalidValue;
 }
