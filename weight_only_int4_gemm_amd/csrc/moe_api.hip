@@ -97,51 +97,121 @@ int check_experts(const void* A, int a_rows, const int32_t* order, int k, const 
 
 }  // namespace
 
-ProductPlan make_product_plan(int format, int rows, int K, int N, int E, bool gate, int cus) {
+namespace {
+
+// A compiled shape of the tile kernel, and what a matrix product in it takes,
+// measured at 4096 and 11008 x 4096 and 4096 x 22016 with 16 to 2048 rows:
+// `alone` microseconds a K block for a workgroup that has its compute unit to
+// itself, `shared` for each of several, `once` for the rest of a workgroup.
+struct Tile {
+  int mb, nb, wm, wn, depth;
+  float alone, shared, once;
+};
+constexpr Tile kTilesF8[] = {
+    {2, 1, 1, 4, 4, 0.30f, 0.19f, 1.5f}, {4, 1, 1, 4, 4, 0.36f, 0.26f, 1.5f},
+    {4, 2, 1, 4, 4, 0.49f, 0.37f, 2.f},  {8, 2, 1, 4, 4, 0.62f, 0.56f, 7.f},
+    {8, 2, 1, 8, 4, 0.90f, 1.08f, 11.f}, {8, 4, 2, 4, 4, 1.45f, 1.84f, 18.f}};
+
+ProductPlan stream_plan(int mb, int nb, int waves, int depth) {
   ProductPlan p{};
+  p.mb = mb;
+  p.nb = nb;
+  p.wm = 1;
+  p.wn = waves;
+  p.depth = depth;
+  p.tm = 16 * mb;
+  p.tn = 16 * nb;
+  p.splits = 1;
+  return p;
+}
+
+ProductPlan tile_plan(int mb, int nb, int wm, int wn, int depth) {
+  ProductPlan p{};
+  p.tile = 1;
+  p.mb = mb;
+  p.nb = nb;
+  p.wm = wm;
+  p.wn = wn;
+  p.depth = depth;
+  p.tm = 16 * mb * wm;
+  p.tn = 16 * nb * wn;
+  p.splits = 1;
+  return p;
+}
+
+// A matrix product.  Up to 16 rows the streaming kernel, with one column block
+// a workgroup while two of them a compute unit cover the columns (4096 x 4096,
+// 16 rows: 6.1 us against 8.1 in tiles; 4096 x 12288: 16.6, but 13.7 with two
+// blocks).  Up to 32 rows too while K is short (2048 x 4096: 5.8 against 6.4;
+// 11008 x 4096: 18.6 against 15.3).  Beyond, the tile and the number of K
+// ranges whose predicted time is least: a compute unit takes its workgroups'
+// K blocks one after another, a join of s ranges takes s trips of the tile's
+// sums (64 x 64, 11008 x 4096 at 64 rows: 32.5, 21.2 and 17.8 us in 1, 2 and 4
+// ranges).
+ProductPlan plan_matrix(int M, int K, int N, int cus) {
+  const int KB = K / kBlockK;
+  if (M <= 16 || (M <= 32 && KB <= 24 && N / 16 <= 2 * cus)) {
+    if (M > 16) return stream_plan(2, 1, 8, 3);
+    return N / 16 <= 2 * cus ? stream_plan(1, 1, 8, 4) : stream_plan(1, 2, 4, 4);
+  }
+  ProductPlan best{};
+  float least = 0.f;
+  for (const Tile& t : kTilesF8) {
+    ProductPlan p = tile_plan(t.mb, t.nb, t.wm, t.wn, t.depth);
+    const int64_t tiles = (int64_t)((M + p.tm - 1) / p.tm) * ((N + p.tn - 1) / p.tn);
+    for (int s = 1; s <= 8; s *= 2) {
+      if (s > 1 && (KB < 8 * s || tiles * s > 2 * cus || tiles > kMaxSplitTiles)) break;
+      const int64_t each = (tiles * s + cus - 1) / cus;
+      const float block = each * t.shared > t.alone ? each * t.shared : t.alone;
+      const float join = s == 1 ? 0.f : s * (1.9f + 0.5f * p.tm * p.tn / 4096.f);
+      const float us = t.once + (KB + s - 1) / s * block + join;
+      if (best.tm == 0 || us < least) {
+        least = us;
+        best = p;
+        best.splits = s;
+      }
+    }
+  }
+  return best;
+}
+
+// Rows of experts, by the mean number of rows of an expert that can have any.
+// Measured with 8 experts of 4096 x 5632 (4 bits) and 64 of 2048 x 2816 (e4m3),
+// in us:
+//   mean       4            16           32           64           128          256
+//   4 bits     74.6 : 84.9  33.3 : 28.7  38.5 : 36.8  73.8 : 69.0  ...          104
+//   e4m3       59.7 : 59.0  82.2 : 65.5  74.3 : 69.4  80.5 : 86.6  115 : 97.7   149 : 148
+// the streaming kernel against tiles of 32 rows (4, with 4096 x 22016 for 4
+// bits, and 16), 32 rows against 64 (32), 64 in four waves against wider ones
+// (64, 128), 128 x 256 against 256 x 256 (256).
+// 4 bits stream four column blocks a workgroup: 16 tokens through 8 experts of
+// 4096 x 22016 93.2 us with two, 74.6 with four; with fewer workgroups than
+// compute units two, and eight waves (one token, 11008 x 4096: 25.6 and 19.4).
+ProductPlan plan_experts(bool f8, int mean, int used, int W, int cus) {
+  if (f8 && mean <= 6) return stream_plan(1, 2, 4, 4);
+  if (!f8 && mean <= 8)
+    return (int64_t)used * (W / 64) >= cus ? stream_plan(1, 4, 4, 3) : stream_plan(1, 2, 8, 3);
+  if (mean <= 24) return tile_plan(2, 2, 1, 4, 4);
+  if (mean <= 96) return tile_plan(4, 2, 1, 4, 4);
+  if (f8) return mean <= 240 ? tile_plan(8, 2, 1, 8, 4) : tile_plan(8, 4, 2, 4, 4);
+  return mean <= 192 ? tile_plan(4, 2, 1, 8, 2) : tile_plan(8, 2, 1, 8, 2);
+}
+
+}  // namespace
+
+ProductPlan make_product_plan(int format, int rows, int K, int N, int E, bool gate, int cus) {
   const int experts = E > 0 ? E : 1;
   const int used = rows < experts ? rows : experts;
-  const int mean = (rows + used - 1) / used;
-  p.splits = 1;
-  p.wm = 1;
-  if (mean <= 48) {
-    p.tile = 0;
-    p.wn = 8;
-    p.nb = 2;
-    p.mb = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
-    p.depth = p.mb == 4 ? 2 : 3;
-    p.tm = 16 * p.mb;
-    p.tn = 16 * p.nb;
-  } else {
-    p.tile = 1;
-    if (mean <= 64) {
-      p.mb = 4, p.nb = 2, p.wm = 1, p.wn = 4, p.depth = 4;
-    } else if (format != kProdF8) {
-      p.mb = 8, p.nb = 2, p.wm = 1, p.wn = 8, p.depth = 2;
-    } else if (mean <= 400) {
-      p.mb = 4, p.nb = 4, p.wm = 2, p.wn = 2, p.depth = 4;
-    } else {
-      p.mb = 8, p.nb = 4, p.wm = 2, p.wn = 4, p.depth = 4;
-    }
-    p.tm = 16 * p.mb * p.wm;
-    p.tn = 16 * p.nb * p.wn;
-  }
+  ProductPlan p = E == 0 ? plan_matrix(rows, K, N, cus)
+                         : plan_experts(format == kProdF8, (rows + used - 1) / used, used,
+                                        gate ? 2 * N : N, cus);
   if (gate) p.tn /= 2;
   p.tiles_n = (N + p.tn - 1) / p.tn;
-  // sum over used experts of ceil(rows / tm)
+  // the most that the used experts' rows can make: sum of ceil(rows / tm)
   p.tiles_m = (int)(((int64_t)rows + (int64_t)used * (p.tm - 1)) / p.tm);
-  if (E == 0 && p.tile == 1) {
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    const int KB = K / kBlockK;
-    int splits = tiles < cus ? (int)(cus / tiles) : 1;
-    if (splits > KB / 8) splits = KB / 8;
-    if (splits > 16) splits = 16;
-    if (splits > 1 && tiles <= kMaxSplitTiles) {
-      p.splits = splits;
-      p.workspace_bytes = kCounterHeaderBytes +
-                          (size_t)tiles * splits * (16 * p.mb * p.wm) * (16 * p.nb * p.wn) * 4;
-    }
-  }
+  if (p.splits > 1)
+    p.workspace_bytes = kCounterHeaderBytes +
+                        (size_t)p.tiles_m * p.tiles_n * p.splits * p.tm * p.tn * 4;
   return p;
 }
 

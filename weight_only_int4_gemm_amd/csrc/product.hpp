@@ -248,7 +248,7 @@ __global__ __launch_bounds__(64 * WAVES) void product_stream_kernel(ProductArgs 
     uint4 a[MB][P::kAPieces];
     float bs[P::kF8 ? NB : 1];
     float as[P::kF8 ? MB : 1];
-    uint2 s[P::kF8 ? 1 : NB];  // four columns' scales, or the lane's column's
+    uint2 s[P::kF8 ? 1 : NB];  // the lane's four columns' scales
   };
   auto load = [&](Step& t, int kb) {
 #pragma unroll
@@ -268,10 +268,7 @@ __global__ __launch_bounds__(64 * WAVES) void product_stream_kernel(ProductArgs 
                           (int64_t)group * p.W;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        if constexpr (F == kProdI4F16)
-          t.s[nb] = *reinterpret_cast<const uint2*>(S + 16 * block[nb] + 4 * quarter);
-        else
-          t.s[nb].x = S[16 * block[nb] + l16];
+        t.s[nb] = *reinterpret_cast<const uint2*>(S + 16 * block[nb] + 4 * quarter);
       }
     }
 #pragma unroll
@@ -298,37 +295,53 @@ __global__ __launch_bounds__(64 * WAVES) void product_stream_kernel(ProductArgs 
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[mb][nb][i] = __builtin_fmaf(d[i], f, acc[mb][nb][i]);
         }
-    } else if constexpr (F == kProdI4F16) {
+    } else {
+      // The sums of the exact integers q - 8 take the scale.  FP16 gets them by
+      // subtraction.  BF16 has no packed one: there the codes enter as 128 + q
+      // (exact: seven fraction bits) and the sums start from -136 times the
+      // rows' sums, one more matrix instruction a slice; 7 vector instructions
+      // a word where converting and scaling takes 29 (one token through two
+      // experts of 4096 x 22016: 32.0 -> 24.5 us).
+      constexpr bool kOffset = F == kProdI4Bf16;
+      float4_t base[MB];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        base[mb] = zero;
+        if constexpr (kOffset) {
+          Half8 minus;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) minus.u[i] = 0xC308C308u;  // BF16 -136
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            base[mb] =
+                mma16<P::kFmt>(minus.v, __builtin_bit_cast(half8_t, t.a[mb][j]), base[mb]);
+        }
+      }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float4_t d[MB];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const half8_t w = codes_minus_eight(word_of(t.b[nb][0], j)).v;
+          const uint32_t word = word_of(t.b[nb][0], j);
+          Half8 w;
+          if constexpr (kOffset) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w.u[i] = and_or(i ? word >> (4 * i) : word, 0x000F000Fu, 0x43004300u);
+          } else {
+            w = codes_minus_eight(word);
+          }
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
-            d[mb] = mma16<P::kFmt>(w, __builtin_bit_cast(half8_t, t.a[mb][j]),
-                                   j == 0 ? zero : d[mb]);
+            d[mb] = mma16<P::kFmt>(w.v, __builtin_bit_cast(half8_t, t.a[mb][j]),
+                                   j == 0 ? base[mb] : d[mb]);
         }
-        typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
-        const half4_t s = __builtin_bit_cast(half4_t, t.s[nb]);
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pair = i < 2 ? t.s[nb].x : t.s[nb].y;
+          const float s = scale16((uint16_t)(pair >> (16 * (i & 1))), kOffset);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[mb][nb][i] = __builtin_fmaf(d[mb][i], (float)s[i], acc[mb][nb][i]);
-      }
-    } else {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const ColParams c = make_col<P::kFmt>(
-            __builtin_bit_cast(half2_t, t.s[nb].x | (t.s[nb].x << 16)), 8);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const half8_t w = unpack_col<P::kFmt>(word_of(t.b[nb][0], j), c);
-#pragma unroll
-          for (int mb = 0; mb < MB; ++mb)
-            acc[mb][nb] = mma16<P::kFmt>(w, __builtin_bit_cast(half8_t, t.a[mb][j]), acc[mb][nb]);
+          for (int mb = 0; mb < MB; ++mb) acc[mb][nb][i] = __builtin_fmaf(d[mb][i], s, acc[mb][nb][i]);
         }
       }
     }
@@ -382,7 +395,7 @@ constexpr int kTileRun = 4;
 
 // WM x WN waves, each 16 MB rows by NB blocks of 16 weight columns; NS stages.
 template <int F, int MB, int NB, int WM, int WN, int NS, bool GATE>
-__global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs p) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductArgs p) {
   typedef Product<F> P;
   constexpr int WAVES = WM * WN;
   constexpr int TM = 16 * MB * WM;
@@ -401,8 +414,14 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
   __shared__ Stage st1;
   __shared__ typename std::conditional<(NS > 2), Stage, char>::type st2;
   __shared__ typename std::conditional<(NS > 2), Stage, char>::type st3;
-  // e4m3: the rows' scales of four K blocks, and of the next four
-  __shared__ float4_t row_scales[2][P::kF8 ? TM : 1];
+  // e4m3: the rows' scales of four K blocks, and of the next four; two objects
+  // for the same reason (as one, every fourth block began with a wait for all
+  // loads in flight: 4096 x 4096 at M = 256 16.1 -> 13.9 us)
+  struct RowScales {
+    float4_t of[P::kF8 ? TM : 1];
+  };
+  __shared__ RowScales rs0;
+  __shared__ RowScales rs1;
 
   const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -442,17 +461,17 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
     const int q = rt.row0 + wave * SROWS + (lane < SROWS ? lane : SROWS - 1);
     scale_src = p.As + (int64_t)source_row(p, q < rt.end ? q : rt.end - 1) * KB;
   }
-  auto load_scales = [&](int buffer, int kb) {
+  auto load_scales = [&](RowScales& to, int kb) {
     if constexpr (P::kF8) {
       if (kb + 4 <= KB) {
         if (lane < SROWS)
           __builtin_amdgcn_global_load_lds((global_ptr_t)(scale_src + kb),
-                                           (lds_ptr_t)&row_scales[buffer][wave * SROWS], 16, 0, 0);
+                                           (lds_ptr_t)&to.of[wave * SROWS], 16, 0, 0);
       } else if (kb < KB) {
         float4_t v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = scale_src[kb + i < KB ? kb + i : KB - 1];
-        if (lane < SROWS) row_scales[buffer][wave * SROWS + lane] = v;
+        if (lane < SROWS) to.of[wave * SROWS + lane] = v;
       }
     }
   };
@@ -527,7 +546,11 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = float4_t{0.f, 0.f, 0.f, 0.f};
   const float4_t zero = {0.f, 0.f, 0.f, 0.f};
 
+  constexpr bool kLate = !P::kF8 && NS == 2;
+  constexpr int SETS = kLate ? 1 : NS > 2 && NB <= 2 && MB <= 8 ? NS : 2;
   constexpr int LOADS = WLOADS + ALOADS;
+  constexpr int WINSTRS = NB * P::kBPieces + SCALES;  // load instructions of the weights
+  constexpr int NEWER = NS == 2 ? 0 : SETS == NS ? (NS - 2) * (WINSTRS + ALOADS) : ALOADS;
   // Rows of a wave are 16 apart, so a lane's swizzle is one number.
   const int l7 = l16 & 7, arow0 = (wm * MB * 16 + l16) * 8;
   const int swz0 = arow0 + (quarter ^ l7), swz1 = arow0 + ((quarter + 4) ^ l7);
@@ -543,42 +566,47 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
       // follow LAG instructions later, when the sums are there; row block
       // mb + 1 is read while mb is multiplied.
       constexpr int LAG = 2, RING = 4;
-      uint4 a[2][2];
-      float as[2], f[2][SCALES];
+      constexpr int PRE = NB >= 4 ? 1 : NB == 2 ? 2 : 3;  // row blocks read ahead
+      constexpr int AS = NB == 1 ? 8 : 4;                 // their scales live LAG longer
+      uint4 a[PRE + 1][2];
+      float as[AS], f[2][SCALES];
       float4_t d[RING];
       auto read = [&](int mb) {
-        a[mb & 1][0] = sg.a[swz0 + mb * 128];
-        a[mb & 1][1] = sg.a[swz1 + mb * 128];
-        as[mb & 1] = reinterpret_cast<const float*>(sc + wm * MB * 16 + l16 + mb * 16)[u];
+        a[mb % (PRE + 1)][0] = sg.a[swz0 + mb * 128];
+        a[mb % (PRE + 1)][1] = sg.a[swz1 + mb * 128];
+        as[mb % AS] = reinterpret_cast<const float*>(sc + wm * MB * 16 + l16 + mb * 16)[u];
       };
       auto add = [&](int i) {
         const int mb = i / NB, nb = i % NB;
+        if (nb == 0)
+#pragma unroll
+          for (int s = 0; s < SCALES; ++s)
+            f[mb & 1][s] = as[mb % AS] * __builtin_bit_cast(float, w.s[s]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           acc[mb][nb][e] = __builtin_fmaf(d[i % RING][e], f[mb & 1][nb / OB], acc[mb][nb][e]);
         asm volatile("" : "+v"(acc[mb][nb]));  // here, not where the loop ends
       };
-      read(0);
+#pragma unroll
+      for (int mb = 0; mb < PRE && mb < MB; ++mb) read(mb);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const int i = mb * NB + nb;
-          d[i % RING] = mma_f8(w.b[nb][0], w.b[nb][1], a[mb & 1][0], a[mb & 1][1], zero);
+          d[i % RING] = mma_f8(w.b[nb][0], w.b[nb][1], a[mb % (PRE + 1)][0], a[mb % (PRE + 1)][1],
+                               zero);
           __builtin_amdgcn_sched_barrier(0);
-          if (nb == LAG - 1)
-#pragma unroll
-            for (int s = 0; s < SCALES; ++s) f[mb & 1][s] = as[mb & 1] * __builtin_bit_cast(float, w.s[s]);
           if (i >= LAG) add(i - LAG);
-          if (nb == 0 && mb + 1 < MB) read(mb + 1);
+          if (nb == 0 && mb + PRE < MB) read(mb + PRE);
           constexpr int EVERY = MB * NB / LOADS > 0 ? MB * NB / LOADS : 1;
           if (i % EVERY == EVERY - 1 && i / EVERY < LOADS) issue(i / EVERY);
           __builtin_amdgcn_sched_barrier(0);  // in this order
         }
       }
 #pragma unroll
-      for (int i = MB * NB - LAG; i < MB * NB; ++i) add(i);
+      for (int i = MB * NB < LAG ? 0 : MB * NB - LAG; i < MB * NB; ++i) add(i);
 #pragma unroll
       for (int i = MB * NB; i < LOADS; ++i) issue(i);
     } else {
@@ -590,7 +618,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
       }
       // While slice j is multiplied, slice j + 1 is unpacked; fragments are
       // read AHEAD row blocks before their use.
-      constexpr int AHEAD = 3;
+      constexpr int AHEAD = kLate && F == kProdI4Bf16 ? 2 : 3;  // within 128 registers
+      static_assert(4 * MB > AHEAD, "fragments ahead");
       half8_t wt[2][NB];
       half8_t a[AHEAD + 1];
       auto read = [&](int i) {  // row block i % MB of slice i / MB
@@ -610,16 +639,20 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
         for (int mb = 0; mb < MB; ++mb) {
           const int i = j * MB + mb;
           if (i + AHEAD < 4 * MB) read(i + AHEAD);
-          if (j < 3 && mb * NB % MB == 0) {
-            const int nb = mb * NB / MB;
-            wt[(j + 1) & 1][nb] = unpack_col<P::kFmt>(word_of(w.b[nb][0], j + 1), c[nb]);
-          }
+          if (j < 3)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              if (nb * MB / NB == mb)
+                wt[(j + 1) & 1][nb] = unpack_col<P::kFmt>(word_of(w.b[nb][0], j + 1), c[nb]);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
             acc[mb][nb] = mma16<P::kFmt>(wt[j & 1][nb], a[i % (AHEAD + 1)], acc[mb][nb]);
-          // activations in the first three slices, weights (whose registers
-          // the last unpacking frees) in the last
-          if (j < 3) {
+          if constexpr (!kLate) {
+            constexpr int EVERY = 4 * MB / LOADS > 0 ? 4 * MB / LOADS : 1;
+            if (i % EVERY == EVERY - 1 && i / EVERY < LOADS) issue(i / EVERY);
+          } else if (j < 3) {
+            // activations in the first three slices, weights (whose registers
+            // the last unpacking frees) in the last
             constexpr int EVERY = 3 * MB / ALOADS > 0 ? 3 * MB / ALOADS : 1;
             if (i % EVERY == EVERY - 1 && i / EVERY < ALOADS) issue(i / EVERY);
           } else {
@@ -627,51 +660,63 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
 #pragma unroll
             for (int n = mb * EACH; n < (mb + 1) * EACH && n < WLOADS; ++n) issue(ALOADS + n);
           }
-          if ((mb + 1) * NB % MB == 0) __builtin_amdgcn_sched_barrier(0);
+          if ((mb + 1) * NB % MB < NB) __builtin_amdgcn_sched_barrier(0);
         }
       }
 #pragma unroll
-      for (int i = 3 * MB; i < ALOADS; ++i) issue(i);
+      for (int i = kLate ? 3 * MB : 4 * MB; i < (kLate ? ALOADS : LOADS); ++i) issue(i);
     }
   };
 
   // While K block kb is multiplied, the stage of kb + NS - 1 is loaded into
-  // LDS and the weights of kb + 1 into registers.  e4m3: the weights first, so
-  // that what block kb + 1 waits for is older than the newest stage's loads.
-  // 4 bits: the weights last, when the registers of block kb's are free.
+  // LDS and the weights of kb + SETS - 1 into registers, weights first.  With
+  // as many sets as stages, what block kb waits for is older than the loads of
+  // the NS - 2 blocks before it; with fewer, than the newest stage's.
+  // kLate (wide 4-bit tiles): one set, loaded again when the last slice is
+  // unpacked; it leaves registers for twice the waves.
   auto stage = [&](int i) -> Stage& {
-    if constexpr (NS > 2)
+    if constexpr (NS == 4)
       return i == 0 ? st0 : i == 1 ? st1 : i == 2 ? st2 : st3;
     else
       return i == 0 ? st0 : st1;
   };
-  constexpr int SETS = P::kF8 ? 2 : 1;
-  constexpr int UNROLL = P::kF8 ? 4 : NS;
+  constexpr int UNROLL = P::kF8 ? 8 : NS;
   Weights weights[SETS];
   auto upto = [&](int kb) { return kb < kb1 ? kb : kb1 - 1; };
   auto load_stage = [&](Stage& sg, int kb) {
 #pragma unroll
     for (int i = 0; i < ALOADS; ++i) load_rows(sg, kb, i);
   };
-  load_scales(0, kb0);
+  load_scales(rs0, kb0);
+  auto load_set = [&](int i) {
 #pragma unroll
-  for (int i = 0; i < NS - 2; ++i) load_stage(stage(i), upto(kb0 + i));
-  keep_load_order();
+    for (int n = 0; n < WLOADS; ++n) load_weights(weights[i], upto(kb0 + i), n);
+    keep_load_order();
+  };
+  if constexpr (kLate) {
+    load_stage(stage(0), kb0);
+    load_set(0);
+  } else {
+    // in the order of the steps that would have issued them
 #pragma unroll
-  for (int i = 0; i < WLOADS; ++i) load_weights(weights[0], kb0, i);
-  keep_load_order();
-  load_stage(stage(NS - 2), upto(kb0 + NS - 2));
-  int buffer = 0;
+    for (int i = 0; i < NS - 1; ++i) {
+      const int set = i - (NS - 1) + (SETS - 1);
+      if (set >= 0) load_set(set);
+      load_stage(stage(i), upto(kb0 + i));
+      keep_load_order();
+    }
+  }
   auto step = [&](int u, int kb) {
-    stage_barrier<(P::kF8 && NS > 2 ? ALOADS : 0)>();
-    if (P::kF8 && u == 0) load_scales(buffer ^ 1, kb + 4);
-    const int kb_w = upto(kb + 1), kb_a = upto(kb + NS - 1);
-    multiply(stage(u % NS), weights[u % SETS], u, row_scales[buffer], [&](int i) {
-      const bool rows = P::kF8 ? i >= WLOADS : i < ALOADS;
+    stage_barrier<NEWER>();
+    if (P::kF8 && u % 4 == 0) load_scales(u == 0 ? rs1 : rs0, kb + 4);
+    const int kb_w = upto(kb + (kLate ? 1 : SETS - 1)), kb_a = upto(kb + NS - 1);
+    multiply(stage(u % NS), weights[u % SETS], u % 4,
+             (u < 4 ? rs0 : rs1).of, [&](int i) {
+      const bool rows = kLate ? i < ALOADS : i >= WLOADS;
       if (rows)
-        load_rows(stage((u + NS - 1) % NS), kb_a, P::kF8 ? i - WLOADS : i);
+        load_rows(stage((u + NS - 1) % NS), kb_a, kLate ? i : i - WLOADS);
       else
-        load_weights(weights[(u + 1) % SETS], kb_w, P::kF8 ? i : i - ALOADS);
+        load_weights(weights[kLate ? 0 : (u + SETS - 1) % SETS], kb_w, kLate ? i - ALOADS : i);
       keep_load_order();
     });
   };
@@ -679,7 +724,6 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
   for (; kb + UNROLL <= kb1; kb += UNROLL) {
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) step(u, kb + u);
-    buffer ^= 1;
   }
 #pragma unroll
   for (int u = 0; u < UNROLL - 1; ++u)
@@ -687,7 +731,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
   // no direct load may still be landing in LDS when the workgroup ends
   __builtin_amdgcn_s_waitcnt(0);
 
-  if (p.splits > 1) {
+  if (P::kF8 && p.splits > 1) {  // 4-bit products never split
     // As in the other kernels' split K: partials published, the arrival
     // counted, the last workgroup of the tile adds them in split order.
     constexpr int TE = WAVES * MB * NB * 256;
@@ -711,15 +755,30 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(ProductArgs 
     }
     __syncthreads();
     if (!*flag) return;
-    for (int s = 0; s < p.splits; ++s) {
-      const __amdgpu_buffer_rsrc_t ps = coherent_rsrc(base + (int64_t)s * TE);
+    // Several partials are loaded before the first of them is added: one
+    // by one each costs a trip to memory.
+    constexpr int AT_ONCE = MB * NB <= 4 ? 4 : MB * NB <= 8 ? 2 : 1;
+    for (int s0 = 0; s0 < p.splits; s0 += AT_ONCE) {
+      float4_t x[AT_ONCE][MB][NB];
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
+      for (int s = 0; s < AT_ONCE; ++s) {
+        const int from = s0 + s < p.splits ? s0 + s : p.splits - 1;
+        const __amdgpu_buffer_rsrc_t ps = coherent_rsrc(base + (int64_t)from * TE);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const float4_t x = load_coherent(ps, frag0 + (mb * NB + nb) * 64);
-          acc[mb][nb] = s == 0 ? x : acc[mb][nb] + x;
-        }
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            x[s][mb][nb] = load_coherent(ps, frag0 + (mb * NB + nb) * 64);
+      }
+#pragma unroll
+      for (int s = 0; s < AT_ONCE; ++s) {
+        if (s0 + s >= p.splits) break;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            acc[mb][nb] = s0 + s == 0 ? x[s][mb][nb] : acc[mb][nb] + x[s][mb][nb];
+      }
     }
     if (threadIdx.x == 0)
       __hip_atomic_store(p.counters + t, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -7,11 +7,14 @@
 namespace w4a16 {
 
 // Streaming kernel: (MB, NB, WAVES, DEPTH); NB is even where gate and up
-// columns share a workgroup.
-#define W4A16_STREAM_VARIANTS(X) X(1, 2, 8, 3) X(2, 2, 8, 3) X(4, 2, 8, 2)
+// columns share a workgroup.  e4m3, 4 bits (experts only).
+#define W4A16_STREAM_F8(X) X(1, 1, 8, 4) X(1, 2, 4, 4) X(2, 1, 8, 3)
+#define W4A16_STREAM_I4(X) X(1, 2, 8, 3) X(1, 4, 4, 3)
 // Tile kernel: (MB, NB, WM, WN, NS).
-#define W4A16_TILE_F8(X) X(4, 2, 1, 4, 4) X(4, 4, 2, 2, 4) X(8, 4, 2, 4, 4)
-#define W4A16_TILE_I4(X) X(4, 2, 1, 4, 4) X(8, 2, 1, 8, 2)
+#define W4A16_TILE_F8(X)                                                           \
+  X(2, 1, 1, 4, 4) X(2, 2, 1, 4, 4) X(4, 1, 1, 4, 4) X(4, 2, 1, 4, 4) X(8, 2, 1, 4, 4) \
+  X(8, 2, 1, 8, 4) X(8, 4, 2, 4, 4)
+#define W4A16_TILE_I4(X) X(2, 2, 1, 4, 4) X(4, 2, 1, 4, 4) X(4, 2, 1, 8, 2) X(8, 2, 1, 8, 2)
 
 template <int F>
 hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool gate,
@@ -20,15 +23,22 @@ hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool ga
     const dim3 grid((unsigned)((int64_t)plan.tiles_m * plan.tiles_n)), block(64 * plan.wn);
 #define W4A16_CASE(MB_, NB_, WAVES_, DEPTH_)                                                      \
   if (plan.mb == MB_ && plan.nb == NB_ && plan.wn == WAVES_ && plan.depth == DEPTH_) {            \
-    if (gate)                                                                                     \
-      hipLaunchKernelGGL((product_stream_kernel<F, MB_, NB_, WAVES_, DEPTH_, true>), grid, block, \
-                         0, stream, a);                                                           \
-    else                                                                                          \
+    if (gate) {                                                                                   \
+      if constexpr (NB_ % 2 == 0)                                                                 \
+        hipLaunchKernelGGL((product_stream_kernel<F, MB_, NB_, WAVES_, DEPTH_, true>), grid,      \
+                           block, 0, stream, a);                                                  \
+      else                                                                                        \
+        return hipErrorInvalidValue;                                                              \
+    } else                                                                                        \
       hipLaunchKernelGGL((product_stream_kernel<F, MB_, NB_, WAVES_, DEPTH_, false>), grid,       \
                          block, 0, stream, a);                                                    \
     return hipGetLastError();                                                                     \
   }
-    W4A16_STREAM_VARIANTS(W4A16_CASE)
+    if constexpr (F == kProdF8) {
+      W4A16_STREAM_F8(W4A16_CASE)
+    } else {
+      W4A16_STREAM_I4(W4A16_CASE)
+    }
 #undef W4A16_CASE
     return hipErrorInvalidValue;
   }
@@ -36,10 +46,13 @@ hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool ga
   const dim3 block(64 * plan.wm * plan.wn);
 #define W4A16_CASE(MB_, NB_, WM_, WN_, NS_)                                                      \
   if (plan.mb == MB_ && plan.nb == NB_ && plan.wm == WM_ && plan.wn == WN_ && plan.depth == NS_) { \
-    if (gate)                                                                                    \
-      hipLaunchKernelGGL((product_tile_kernel<F, MB_, NB_, WM_, WN_, NS_, true>), grid, block, 0, \
-                         stream, a);                                                             \
-    else                                                                                         \
+    if (gate) {                                                                                  \
+      if constexpr (NB_ % 2 == 0)                                                                \
+        hipLaunchKernelGGL((product_tile_kernel<F, MB_, NB_, WM_, WN_, NS_, true>), grid, block, \
+                           0, stream, a);                                                        \
+      else                                                                                       \
+        return hipErrorInvalidValue;                                                             \
+    } else                                                                                       \
       hipLaunchKernelGGL((product_tile_kernel<F, MB_, NB_, WM_, WN_, NS_, false>), grid, block, 0, \
                          stream, a);                                                             \
     return hipGetLastError();                                                                    \
