@@ -134,10 +134,9 @@ int moe_tables(const int32_t* ids, int32_t* starts, int32_t* order, int32_t* whe
  *         or columns: nothing is launched), group a multiple of 128 that
  *         divides K, E 1..MOE_MAX_EXPERTS, k >= 1, a_rows >= 1.  At most 2^24
  *         rows and a_rows, K 2^20, W 2^24, K * W 2^36.
- * Numerics: products accumulate in FP32; weights are the exact (q - 8) with
- *         the scale on the FP32 sums of 128, or rounded once to `dtype` from
- *         (q - 8) * s, by the shape (both are the product up to rounding);
- *         the activation is in FP32, C rounded once.
+ * Numerics: products accumulate in FP32; the exact (q - 8) are multiplied and
+ *         the scales go onto the FP32 sums of 128; the activation is in FP32,
+ *         C rounded once.
  * Errors: W4A16_ERR_NULL, _SHAPE (sizes, overlaps), _GROUP, _ALIGN (16 bytes;
  *         order and starts 4), _DTYPE, _EPILOGUE (activation), _DEVICE,
  *         _LAUNCH.

@@ -176,25 +176,34 @@ ProductPlan plan_matrix(int M, int K, int N, int cus) {
 }
 
 // Rows of experts, by the mean number of rows of an expert that can have any.
-// Measured with 8 experts of 4096 x 5632 (4 bits) and 64 of 2048 x 2816 (e4m3),
-// in us:
-//   mean       4            16           32           64           128          256
-//   4 bits     74.6 : 84.9  33.3 : 28.7  38.5 : 36.8  73.8 : 69.0  ...          104
-//   e4m3       59.7 : 59.0  82.2 : 65.5  74.3 : 69.4  80.5 : 86.6  115 : 97.7   149 : 148
-// the streaming kernel against tiles of 32 rows (4, with 4096 x 22016 for 4
-// bits, and 16), 32 rows against 64 (32), 64 in four waves against wider ones
-// (64, 128), 128 x 256 against 256 x 256 (256).
+// 4 bits, us with 8 experts of 4096 x 22016 (FP16):
+//   mean                     4      8      12     16     48     64     96
+//   streaming kernel         74.6   89.8   91.5   112
+//   tiles of 32 x 128        84.9   83.7   87.1   89.5   129    160    228
+//   64 x 256                                             129    155    169
+//   (64 x 128 between or above: 135, 167, 198; 256 rows: 64 x 256 389,
+//   128 x 128 437, 256 x 256 522; 1024 rows: 1409, 1379, 1393)
+// e4m3, us with 64 experts of 2048 x 2816:
+//   mean                     4      16     32     64     128    256
+//   streaming kernel         59.7   82.2
+//   tiles of 32 x 128        59.0   65.5   74.3
+//   64 x 128                               69.4   80.5   115
+//   128 x 256                                     86.6   97.7   149
+//   256 x 256                                                   148
 // 4 bits stream four column blocks a workgroup: 16 tokens through 8 experts of
 // 4096 x 22016 93.2 us with two, 74.6 with four; with fewer workgroups than
 // compute units two, and eight waves (one token, 11008 x 4096: 25.6 and 19.4).
-ProductPlan plan_experts(bool f8, int mean, int used, int W, int cus) {
-  if (f8 && mean <= 6) return stream_plan(1, 2, 4, 4);
-  if (!f8 && mean <= 8)
+ProductPlan plan_experts(bool f8, int rows, int used, int W, int cus) {
+  const int mean = (rows + used - 1) / used;
+  if (f8) {
+    if (mean <= 6) return stream_plan(1, 2, 4, 4);
+    if (mean <= 24) return tile_plan(2, 2, 1, 4, 4);
+    if (mean <= 96) return tile_plan(4, 2, 1, 4, 4);
+    return mean <= 240 ? tile_plan(8, 2, 1, 8, 4) : tile_plan(8, 4, 2, 4, 4);
+  }
+  if (mean <= 7)
     return (int64_t)used * (W / 64) >= cus ? stream_plan(1, 4, 4, 3) : stream_plan(1, 2, 8, 3);
-  if (mean <= 24) return tile_plan(2, 2, 1, 4, 4);
-  if (mean <= 96) return tile_plan(4, 2, 1, 4, 4);
-  if (f8) return mean <= 240 ? tile_plan(8, 2, 1, 8, 4) : tile_plan(8, 4, 2, 4, 4);
-  return mean <= 192 ? tile_plan(4, 2, 1, 8, 2) : tile_plan(8, 2, 1, 8, 2);
+  return mean <= 48 ? tile_plan(2, 2, 1, 4, 4) : tile_plan(4, 4, 1, 4, 4);
 }
 
 }  // namespace
@@ -203,8 +212,7 @@ ProductPlan make_product_plan(int format, int rows, int K, int N, int E, bool ga
   const int experts = E > 0 ? E : 1;
   const int used = rows < experts ? rows : experts;
   ProductPlan p = E == 0 ? plan_matrix(rows, K, N, cus)
-                         : plan_experts(format == kProdF8, (rows + used - 1) / used, used,
-                                        gate ? 2 * N : N, cus);
+                         : plan_experts(format == kProdF8, rows, used, gate ? 2 * N : N, cus);
   if (gate) p.tn /= 2;
   p.tiles_n = (N + p.tn - 1) / p.tn;
   // the most that the used experts' rows can make: sum of ceil(rows / tm)

@@ -152,6 +152,7 @@ typedef int int8_vt __attribute__((ext_vector_type(8)));
 template <int F>
 struct Product {
   static constexpr bool kF8 = F == kProdF8;
+  static constexpr bool kOffset = F == kProdI4Bf16;  // codes(): 136 too much
   static constexpr int kFmt = F == kProdI4Bf16 ? kFmtBf16 : kFmtF16;
   static constexpr int kRowBlock = kF8 ? 128 : 256;  // bytes of a row's K block
   static constexpr int kAPieces = kRowBlock / 64;    // 16-byte pieces of a lane
@@ -170,6 +171,30 @@ __device__ __forceinline__ float4_t mma_f8(uint4 b0, uint4 b1, uint4 a0, uint4 a
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
   return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+}
+
+// Eight 4-bit codes as exact numbers of the type: FP16 q - 8; BF16, which has
+// no packed subtraction, 128 + q (seven fraction bits) in 7 vector
+// instructions, where (q - 8) s takes 29.  Sums of the latter start from
+// minus_offset() times the row, one more matrix instruction a slice.
+template <int F>
+__device__ __forceinline__ half8_t codes(uint32_t word) {
+  if constexpr (Product<F>::kOffset) {
+    Half8 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w.u[i] = and_or(i ? word >> (4 * i) : word, 0x000F000Fu, 0x43004300u);
+    return w.v;
+  } else {
+    return codes_minus_eight(word).v;
+  }
+}
+
+__device__ __forceinline__ half8_t minus_offset() {  // BF16 -136
+  Half8 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w.u[i] = 0xC308C308u;
+  return w.v;
 }
 
 __device__ __forceinline__ float scale16(uint16_t bits, int bf16) {
@@ -296,50 +321,33 @@ __global__ __launch_bounds__(64 * WAVES) void product_stream_kernel(ProductArgs 
           for (int i = 0; i < 4; ++i) acc[mb][nb][i] = __builtin_fmaf(d[i], f, acc[mb][nb][i]);
         }
     } else {
-      // The sums of the exact integers q - 8 take the scale.  FP16 gets them by
-      // subtraction.  BF16 has no packed one: there the codes enter as 128 + q
-      // (exact: seven fraction bits) and the sums start from -136 times the
-      // rows' sums, one more matrix instruction a slice; 7 vector instructions
-      // a word where converting and scaling takes 29 (one token through two
-      // experts of 4096 x 22016: 32.0 -> 24.5 us).
-      constexpr bool kOffset = F == kProdI4Bf16;
+      // The sums of the exact integers q - 8 take the scale (BF16: one token
+      // through two experts of 4096 x 22016, weights scaled 32.0 us, sums 24.5).
       float4_t base[MB];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         base[mb] = zero;
-        if constexpr (kOffset) {
-          Half8 minus;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) minus.u[i] = 0xC308C308u;  // BF16 -136
+        if constexpr (P::kOffset)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            base[mb] =
-                mma16<P::kFmt>(minus.v, __builtin_bit_cast(half8_t, t.a[mb][j]), base[mb]);
-        }
+            base[mb] = mma16<P::kFmt>(minus_offset(), __builtin_bit_cast(half8_t, t.a[mb][j]),
+                                      base[mb]);
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float4_t d[MB];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t word = word_of(t.b[nb][0], j);
-          Half8 w;
-          if constexpr (kOffset) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w.u[i] = and_or(i ? word >> (4 * i) : word, 0x000F000Fu, 0x43004300u);
-          } else {
-            w = codes_minus_eight(word);
-          }
+          const half8_t w = codes<F>(word_of(t.b[nb][0], j));
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
-            d[mb] = mma16<P::kFmt>(w.v, __builtin_bit_cast(half8_t, t.a[mb][j]),
+            d[mb] = mma16<P::kFmt>(w, __builtin_bit_cast(half8_t, t.a[mb][j]),
                                    j == 0 ? base[mb] : d[mb]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t pair = i < 2 ? t.s[nb].x : t.s[nb].y;
-          const float s = scale16((uint16_t)(pair >> (16 * (i & 1))), kOffset);
+          const float s = scale16((uint16_t)(pair >> (16 * (i & 1))), P::kOffset);
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb) acc[mb][nb][i] = __builtin_fmaf(d[mb][i], s, acc[mb][nb][i]);
         }
@@ -453,8 +461,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   // Row scales come four K blocks at a time (a lane reads 16 bytes of its
   // row): loaded block by block, each 4-byte access of a scattered row takes
   // the cache path as long as 64 contiguous bytes (8192 x 28672 at M = 4096:
-  // 998 -> 981 us, and 934 with four stages).  TM / WAVES lanes of a wave load one row each; the last group,
-  // where the row may end, goes through registers.
+  // 998 -> 981 us, and 934 with four stages).  TM / WAVES lanes of a wave load
+  // one row each; the last group, where the row may end, goes through registers.
   constexpr int SROWS = TM / WAVES;
   const float* scale_src = nullptr;
   if constexpr (P::kF8) {
@@ -502,7 +510,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   for (int i = 0; i < OB; ++i)
     boff[i] = ((first + i < blocks ? first + i : blocks - 1) - first) * KB * P::kBBlock;
   // e4m3: a wave's columns lie in one 128-column block of scales (with GATE,
-  // one of each half).  4 bits: the scale of the lane's column.
+  // one of each half).  4 bits: the scales of the lane's four output columns.
   constexpr int SCALES = P::kF8 ? HALVES : NB;
   const float* fsrc[HALVES];
   const __amdgpu_buffer_rsrc_t ssrc = __builtin_amdgcn_make_buffer_rsrc(
@@ -516,7 +524,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   }
   struct Weights {
     uint4 b[NB][P::kBPieces];
-    uint32_t s[SCALES];  // FP32 bits, or 16 bits
+    float s[P::kF8 ? SCALES : 1];
+    uint2 s4[P::kF8 ? 1 : NB];  // four columns' scales
   };
   // Load i < WLOADS of a K block's weights: a column block's, or a scale.
   constexpr int WLOADS = NB + SCALES;
@@ -529,13 +538,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
                                                          boff[i % OB] + kb * P::kBBlock, 0));
     } else if constexpr (P::kF8) {
       const int h = i - NB;
-      w.s[h] = __builtin_bit_cast(uint32_t, fsrc[h][kb]);
+      w.s[h] = fsrc[h][kb];
     } else {
       const int nb = i - NB;
       const int group = (int)(((uint64_t)(uint32_t)kb * p.gmagic) >> 32);
       const int ob = first + nb % OB < blocks ? first + nb % OB : blocks - 1;
-      w.s[nb] = __builtin_amdgcn_raw_buffer_load_b16(
-          ssrc, l16 * 2, (group * p.W + 16 * (ob + (nb >= OB ? blocks : 0))) * 2, 0);
+      const int at = (group * p.W + 16 * (ob + (nb >= OB ? blocks : 0))) * 2;
+      w.s4[nb] = __builtin_bit_cast(
+          uint2, __builtin_amdgcn_raw_buffer_load_b64(ssrc, quarter * 8, at, 0));
     }
   };
 
@@ -546,8 +556,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = float4_t{0.f, 0.f, 0.f, 0.f};
   const float4_t zero = {0.f, 0.f, 0.f, 0.f};
 
-  constexpr bool kLate = !P::kF8 && NS == 2;
-  constexpr int SETS = kLate ? 1 : NS > 2 && NB <= 2 && MB <= 8 ? NS : 2;
+  constexpr int SETS = NS > 2 && NB <= 2 && MB <= 8 ? NS : 2;
   constexpr int LOADS = WLOADS + ALOADS;
   constexpr int WINSTRS = NB * P::kBPieces + SCALES;  // load instructions of the weights
   constexpr int NEWER = NS == 2 ? 0 : SETS == NS ? (NS - 2) * (WINSTRS + ALOADS) : ALOADS;
@@ -581,7 +590,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
         if (nb == 0)
 #pragma unroll
           for (int s = 0; s < SCALES; ++s)
-            f[mb & 1][s] = as[mb % AS] * __builtin_bit_cast(float, w.s[s]);
+            f[mb & 1][s] = as[mb % AS] * w.s[s];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           acc[mb][nb][e] = __builtin_fmaf(d[i % RING][e], f[mb & 1][nb / OB], acc[mb][nb][e]);
@@ -610,61 +619,62 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 #pragma unroll
       for (int i = MB * NB; i < LOADS; ++i) issue(i);
     } else {
-      ColParams c[NB];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const _Float16 s = __builtin_bit_cast(_Float16, (uint16_t)w.s[nb]);
-        c[nb] = make_col<P::kFmt>(half2_t{s, s}, 8);
-      }
-      // While slice j is multiplied, slice j + 1 is unpacked; fragments are
-      // read AHEAD row blocks before their use.
-      constexpr int AHEAD = kLate && F == kProdI4Bf16 ? 2 : 3;  // within 128 registers
-      static_assert(4 * MB > AHEAD, "fragments ahead");
-      half8_t wt[2][NB];
+      // The exact integers are multiplied and the scales go onto the FP32 sums
+      // of 128, so no weight is rounded.  All of a K block's words are unpacked
+      // while its first row block is multiplied; the sums of one row block are
+      // scaled and added while the next is.  Against weights scaled and rounded
+      // first, 8 experts of 4096 x 22016, FP16 and BF16, in us: 16 rows each
+      // 89.5 : 90.9 and 92.8 : 130; 32 rows 115 : 117 and 120 : 155; 256 rows
+      // 389 : 410 and 419 : 429; 1024 rows 1400 : 1245 and 1490 : 1500, with
+      // a tenth of the error (FP16).
+      // fragments are read AHEAD slices before their use, within 256 registers
+      constexpr int AHEAD = P::kOffset && NB == 4 ? 3 : 4;
+      half8_t wt[4][NB];
       half8_t a[AHEAD + 1];
-      auto read = [&](int i) {  // row block i % MB of slice i / MB
-        const int j = i / MB, mb = i % MB;
+      float4_t d[NB], base = zero;
+      auto read = [&](int i) {  // slice i % 4 of row block i / 4
+        const int j = i % 4, mb = i / 4;
         a[i % (AHEAD + 1)] = __builtin_bit_cast(
             half8_t, sg.a[(j >> 1) * TM * 8 + ((j & 1) ? swz1 : swz0) + mb * 128]);
       };
+      auto unpack = [&](int j) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) wt[j][nb] = codes<F>(word_of(w.b[nb][0], j));
+      };
+      auto add = [&](int mb, int nb) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t pair = e < 2 ? w.s4[nb].x : w.s4[nb].y;
+          acc[mb][nb][e] = __builtin_fmaf(P::kOffset ? d[nb][e] + base[e] : d[nb][e],
+                                          scale16((uint16_t)(pair >> (16 * (e & 1))), P::kOffset),
+                                          acc[mb][nb][e]);
+        }
+        asm volatile("" : "+v"(acc[mb][nb]));  // here, not where the loop ends
+      };
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) read(i);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        wt[0][nb] = unpack_col<P::kFmt>(word_of(w.b[nb][0], 0), c[nb]);
+      unpack(0);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int i = 0; i < 4 * MB; ++i) {
+        const int j = i % 4;
+        if (i + AHEAD < 4 * MB) read(i + AHEAD);
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          const int i = j * MB + mb;
-          if (i + AHEAD < 4 * MB) read(i + AHEAD);
-          if (j < 3)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              if (nb * MB / NB == mb)
-                wt[(j + 1) & 1][nb] = unpack_col<P::kFmt>(word_of(w.b[nb][0], j + 1), c[nb]);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            acc[mb][nb] = mma16<P::kFmt>(wt[j & 1][nb], a[i % (AHEAD + 1)], acc[mb][nb]);
-          if constexpr (!kLate) {
-            constexpr int EVERY = 4 * MB / LOADS > 0 ? 4 * MB / LOADS : 1;
-            if (i % EVERY == EVERY - 1 && i / EVERY < LOADS) issue(i / EVERY);
-          } else if (j < 3) {
-            // activations in the first three slices, weights (whose registers
-            // the last unpacking frees) in the last
-            constexpr int EVERY = 3 * MB / ALOADS > 0 ? 3 * MB / ALOADS : 1;
-            if (i % EVERY == EVERY - 1 && i / EVERY < ALOADS) issue(i / EVERY);
-          } else {
-            constexpr int EACH = (WLOADS + MB - 1) / MB;
-#pragma unroll
-            for (int n = mb * EACH; n < (mb + 1) * EACH && n < WLOADS; ++n) issue(ALOADS + n);
-          }
-          if ((mb + 1) * NB % MB < NB) __builtin_amdgcn_sched_barrier(0);
+        for (int nb = 0; nb < NB; ++nb) {
+          if (j == 0 && i > 0) add(i / 4 - 1, nb);
+          d[nb] = mma16<P::kFmt>(wt[j][nb], a[i % (AHEAD + 1)], j == 0 ? zero : d[nb]);
         }
+        if constexpr (P::kOffset)
+          base = mma16<P::kFmt>(minus_offset(), a[i % (AHEAD + 1)], j == 0 ? zero : base);
+        if (i < 3) unpack(i + 1);
+        constexpr int EVERY = 4 * MB / LOADS > 0 ? 4 * MB / LOADS : 1;
+        if (i % EVERY == EVERY - 1 && i / EVERY < LOADS) issue(i / EVERY);
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int i = kLate ? 3 * MB : 4 * MB; i < (kLate ? ALOADS : LOADS); ++i) issue(i);
+      for (int nb = 0; nb < NB; ++nb) add(MB - 1, nb);
+#pragma unroll
+      for (int i = 4 * MB; i < LOADS; ++i) issue(i);
     }
   };
 
@@ -672,8 +682,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   // LDS and the weights of kb + SETS - 1 into registers, weights first.  With
   // as many sets as stages, what block kb waits for is older than the loads of
   // the NS - 2 blocks before it; with fewer, than the newest stage's.
-  // kLate (wide 4-bit tiles): one set, loaded again when the last slice is
-  // unpacked; it leaves registers for twice the waves.
   auto stage = [&](int i) -> Stage& {
     if constexpr (NS == 4)
       return i == 0 ? st0 : i == 1 ? st1 : i == 2 ? st2 : st3;
@@ -693,30 +701,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     for (int n = 0; n < WLOADS; ++n) load_weights(weights[i], upto(kb0 + i), n);
     keep_load_order();
   };
-  if constexpr (kLate) {
-    load_stage(stage(0), kb0);
-    load_set(0);
-  } else {
-    // in the order of the steps that would have issued them
+  // in the order of the steps that would have issued them
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) {
-      const int set = i - (NS - 1) + (SETS - 1);
-      if (set >= 0) load_set(set);
-      load_stage(stage(i), upto(kb0 + i));
-      keep_load_order();
-    }
+  for (int i = 0; i < NS - 1; ++i) {
+    const int set = i - (NS - 1) + (SETS - 1);
+    if (set >= 0) load_set(set);
+    load_stage(stage(i), upto(kb0 + i));
+    keep_load_order();
   }
   auto step = [&](int u, int kb) {
     stage_barrier<NEWER>();
     if (P::kF8 && u % 4 == 0) load_scales(u == 0 ? rs1 : rs0, kb + 4);
-    const int kb_w = upto(kb + (kLate ? 1 : SETS - 1)), kb_a = upto(kb + NS - 1);
-    multiply(stage(u % NS), weights[u % SETS], u % 4,
-             (u < 4 ? rs0 : rs1).of, [&](int i) {
-      const bool rows = kLate ? i < ALOADS : i >= WLOADS;
-      if (rows)
-        load_rows(stage((u + NS - 1) % NS), kb_a, kLate ? i : i - WLOADS);
+    const int kb_w = upto(kb + SETS - 1), kb_a = upto(kb + NS - 1);
+    multiply(stage(u % NS), weights[u % SETS], u % 4, (u < 4 ? rs0 : rs1).of, [&](int i) {
+      if (i >= WLOADS)
+        load_rows(stage((u + NS - 1) % NS), kb_a, i - WLOADS);
       else
-        load_weights(weights[kLate ? 0 : (u + SETS - 1) % SETS], kb_w, kLate ? i - ALOADS : i);
+        load_weights(weights[(u + SETS - 1) % SETS], kb_w, i);
       keep_load_order();
     });
   };

@@ -14,7 +14,7 @@ namespace w4a16 {
 #define W4A16_TILE_F8(X)                                                           \
   X(2, 1, 1, 4, 4) X(2, 2, 1, 4, 4) X(4, 1, 1, 4, 4) X(4, 2, 1, 4, 4) X(8, 2, 1, 4, 4) \
   X(8, 2, 1, 8, 4) X(8, 4, 2, 4, 4)
-#define W4A16_TILE_I4(X) X(2, 2, 1, 4, 4) X(4, 2, 1, 4, 4) X(4, 2, 1, 8, 2) X(8, 2, 1, 8, 2)
+#define W4A16_TILE_I4(X) X(2, 2, 1, 4, 4) X(4, 4, 1, 4, 4)
 
 template <int F>
 hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool gate,
