@@ -136,7 +136,10 @@ int moe_tables(const int32_t* ids, int32_t* starts, int32_t* order, int32_t* whe
  *         rows and a_rows, K 2^20, W 2^24, K * W 2^36.
  * Numerics: products accumulate in FP32; the exact (q - 8) are multiplied and
  *         the scales go onto the FP32 sums of 128; the activation is in FP32,
- *         C rounded once.
+ *         C rounded once.  BF16 codes enter as 128 + q, 136 times the row's
+ *         sum taken off: a row of A that holds an infinity gives NaN where
+ *         the product would be infinite too, and one with values of 2^112
+ *         and more may.
  * Errors: W4A16_ERR_NULL, _SHAPE (sizes, overlaps), _GROUP, _ALIGN (16 bytes;
  *         order and starts 4), _DTYPE, _EPILOGUE (activation), _DEVICE,
  *         _LAUNCH.

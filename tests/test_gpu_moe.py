@@ -5,7 +5,9 @@ Tolerances, derived from the arithmetic (U = 2^-24, an FP32 rounding; S the sum
 of the magnitudes that are added; h half a step of the output's type):
 * a product: every one of the K products and sums of an output can be off by
   one rounding towards zero (2 U) of at most S, scales and joins by a few more:
-  (K + 64) 2 U S;  4-bit weights may be rounded to the type first: h S;
+  (K + 64) 2 U S;  4-bit weights with BF16 enter as 128 + q, at most 143, and
+  136 times the row comes off: each block of 128 adds 256 numbers and a few sums
+  whose partial sums are at most 279 s |a| summed: 320 2 U 279 sum(|a| s) more;
   the output's own rounding: h |y|, at least half its smallest step;
 * the gate: silu has slope within +-1.1 and |silu(x)| <= |x|, exp and
   reciprocal are within 2^-21: 1.1 dx |u| + |silu(x)| du + dx du 1.1 + 2^-20 |y|;
@@ -358,7 +360,8 @@ def test_tables(T, k, E):
 # ---------------------------------------------------------------------------
 
 def _weights(form, E, K, W, group, name, rng):
-    """(packed, scales) on the device and the exact [E, K, W]."""
+    """(packed, scales) on the device, the exact [E, K, W] and, of 4 bits, the
+    scale of each."""
     torch = _torch()
     if form == 8:
         packed = w4.alloc_w8a8_packed(K, W, E)
@@ -368,16 +371,17 @@ def _weights(form, E, K, W, group, name, rng):
             q = _e4m3(rng, (W, K))
             w4.w8a8_repack(cuda(q), packed[e])
             exact[e] = ref.weights8(q, sb[e]).T
-        return packed, cuda(sb), exact
+        return packed, cuda(sb), exact, None
     packed = torch.empty((E, K * W // 8), dtype=torch.int32, device="cuda")
     s, exact_s = to16(rng.uniform(0.005, 0.02, (E, K // group, W)), name)
+    steps = np.repeat(exact_s, group, 1)
     exact = np.empty((E, K, W))
     for e in range(E):
         words = rng.integers(0, 2 ** 32, (K // 8, W), dtype=np.uint64).astype(np.uint32)
         w4.w4a16_repack(cuda(words.view(np.int32)), packed[e], K, W)
         codes = (words[:, None, :] >> (4 * np.arange(8, dtype=np.uint32))[None, :, None]) & 15
-        exact[e] = (codes.reshape(K, W).astype(float) - 8) * np.repeat(exact_s[e], group, 0)
-    return packed, s, exact
+        exact[e] = (codes.reshape(K, W).astype(float) - 8) * steps[e]
+    return packed, s, exact, steps
 
 
 def _loads(kind, T, k, E, rng):
@@ -396,7 +400,7 @@ def _run_experts(form, T, k, E, K, N, name, up, kind, group=128, seed=0):
     torch = _torch()
     rng = np.random.default_rng(seed + T + E + N)
     W = 2 * N if up else N
-    packed, scales, exact_w = _weights(form, E, K, W, group, name, rng)
+    packed, scales, exact_w, steps = _weights(form, E, K, W, group, name, rng)
     ids = _loads(kind, T, k, E, rng)
     starts, order, where = ref.tables(ids, E)
     rows = T * k
@@ -417,7 +421,10 @@ def _run_experts(form, T, k, E, K, N, name, up, kind, group=128, seed=0):
     n = starts[E]
     got, x, S = got[:n], x[:n], S[:n]
     h = half_step(name)
-    d = ((K + 64) * 2 * U + (h if form == 4 else 0)) * S
+    d = (K + 64) * 2 * U * S
+    if form == 4 and name == "bfloat16":
+        more = ref.expert_rows(np.abs(A), order if up else None, starts, steps, k, rows)[0][:n]
+        d = d + 320 * 2 * U * 279 * more
     if up:
         g, u, dg, du = x[:, :N], x[:, N:], d[:, :N], d[:, N:]
         s = ref.silu(g)
@@ -460,6 +467,37 @@ def test_experts_columns_of_16_and_long_groups(T, N):
     _run_experts(8, T, 2, 2, 512, N, "float16", False, "skew")
 
 
+@pytest.mark.parametrize("name", ["float16", "bfloat16"])
+@pytest.mark.parametrize("T", [2, 70, 300])                  # streamed, and both tiles
+def test_experts_non_finite_rows_stay_alone(T, name):
+    """Infinities and NaN in rows of A and in an expert's scales reach those
+    rows and that expert's rows, and nothing else."""
+    torch = _torch()
+    rng = np.random.default_rng(T)
+    k, E, K, N = 1, 2, 384, 288
+    packed, scales, exact_w, _ = _weights(4, E, K, N, 128, name, rng)
+    a, A = to16(rng.standard_normal((T, K)), name)
+    ids = np.arange(T)[:, None].astype(np.int32) % 2
+    starts, order, _ = ref.tables(ids, E)
+    y = torch.empty((T, N), dtype=_dtype(name), device="cuda")
+    say("experts non-finite", T, name, w4.moe_gemm_describe(4, T, K, N, E, 0))
+    run = lambda: (w4.w4a16_moe_gemm(a, cuda(order), cuda(starts), packed, scales, y, k, 128),
+                   host(y))[1]
+    clean = run()
+    assert np.isfinite(clean).all()
+    a[0, 5], a[T - 1, K - 1] = float("nan"), float("inf")
+    bad = np.isin(order, [0, T - 1])
+    got = run()
+    assert np.isnan(got[order == 0]).all() and not np.isfinite(got[bad]).any()
+    assert np.array_equal(got[~bad], clean[~bad])
+    a.copy_(torch.from_numpy(A))
+    scales[1, 1, 7] = float("nan")                           # one column of one expert
+    got = run()
+    bad = np.zeros((T, N), bool)
+    bad[starts[1]:, 7] = True
+    assert np.isnan(got[bad]).all() and np.array_equal(got[~bad], clean[~bad])
+
+
 def test_experts_index_tensors_of_anything():
     """Orders and starts that hold nonsense: no row outside is touched, and
     rows whose entries are right are right."""
@@ -467,7 +505,7 @@ def test_experts_index_tensors_of_anything():
     say("experts nonsense")
     rng = np.random.default_rng(0)
     T, k, E, K, N = 50, 2, 4, 256, 96
-    packed, scales, exact_w = _weights(4, E, K, N, 128, "float16", rng)
+    packed, scales, exact_w, _ = _weights(4, E, K, N, 128, "float16", rng)
     a, A = to16(rng.standard_normal((T, K)), "float16")
     order = np.arange(100, dtype=np.int32)
     order[10], order[20], order[30] = -2 ** 31, 100, 2 ** 31 - 1
@@ -480,7 +518,7 @@ def test_experts_index_tensors_of_anything():
     for p in range(25):                                      # expert 0: rows 0 .. 24
         want = A[src[p]] @ exact_w[0]
         S = np.abs(A[src[p]]) @ np.abs(exact_w[0])
-        close(got[p], want, (2.0 ** -11 + (K + 64) * 2 * U) * S + 2.0 ** -11 * np.abs(want), p)
+        close(got[p], want, (K + 64) * 2 * U * S + 2.0 ** -11 * np.abs(want), p)
 
 
 @pytest.mark.parametrize("T,k,N,rows", [(1, 1, 8, 1), (7, 2, 96, 14), (33, 8, 2048, 264),
@@ -518,8 +556,8 @@ class Layer:
         torch = _torch()
         rng = np.random.default_rng(seed)
         self.form, self.k, self.E, self.K, self.N = form, k, E, K, N
-        self.w1, self.s1, self.x1 = _weights(form, E, K, 2 * N, 128, name, rng)
-        self.w2, self.s2, self.x2 = _weights(form, E, N, K, 128, name, rng)
+        self.w1, self.s1, self.x1, _ = _weights(form, E, K, 2 * N, 128, name, rng)
+        self.w2, self.s2, self.x2, _ = _weights(form, E, N, K, 128, name, rng)
         dt = _dtype(name)
         self.x = torch.zeros((T, K), dtype=dt, device="cuda")
         self.logits = torch.zeros((T, E), dtype=dt, device="cuda")

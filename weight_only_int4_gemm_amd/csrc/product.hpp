@@ -512,16 +512,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   // e4m3: a wave's columns lie in one 128-column block of scales (with GATE,
   // one of each half).  4 bits: the scales of the lane's four output columns.
   constexpr int SCALES = P::kF8 ? HALVES : NB;
-  const float* fsrc[HALVES];
+  // Buffer loads: the waits below count them, so none may become a scalar one.
   const __amdgpu_buffer_rsrc_t ssrc = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint16_t*>(static_cast<const uint16_t*>(p.S)) + rt.e * p.s_expert, (short)0,
+      static_cast<char*>(const_cast<void*>(p.S)) + rt.e * p.s_expert * (P::kF8 ? 4 : 2), (short)0,
       0x7fffffff, 0x00020000);
-  if constexpr (P::kF8) {
-#pragma unroll
-    for (int i = 0; i < HALVES; ++i)
-      fsrc[i] = static_cast<const float*>(p.S) + rt.e * p.s_expert +
-                (int64_t)((first + i * blocks) >> 3) * KB;
-  }
   struct Weights {
     uint4 b[NB][P::kBPieces];
     float s[P::kF8 ? SCALES : 1];
@@ -538,7 +532,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
                                                          boff[i % OB] + kb * P::kBBlock, 0));
     } else if constexpr (P::kF8) {
       const int h = i - NB;
-      w.s[h] = fsrc[h][kb];
+      w.s[h] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(
+                     ssrc, 0, (((first + h * blocks) >> 3) * KB + kb) * 4, 0));
     } else {
       const int nb = i - NB;
       const int group = (int)(((uint64_t)(uint32_t)kb * p.gmagic) >> 32);
