@@ -310,6 +310,20 @@ def test_route_masked_tied_and_infinite():
                 _check_route(cuda(x), b, 6, softmax=softmax, **kind)
 
 
+@pytest.mark.parametrize("name", ["float32", "float16"])
+@pytest.mark.parametrize("T", [5, 4200])                     # 64 and 16 lanes a token
+def test_route_zeros_of_both_signs_tie(T, name):
+    say("route zeros", T, name)
+    rng = np.random.default_rng(6)
+    x = np.where(rng.random((T, 96)) < 0.5, -0.0, 0.0)
+    x[:, ::7] = -1.0
+    x = _torch().from_numpy(x).to(_dtype(name)).cuda()
+    for kind in (dict(), dict(groups=8, top_groups=3), dict(groups=8, top_groups=3, group_best=2)):
+        for softmax in (True, False):
+            _check_route(x, None, 6, softmax=softmax, **kind)
+            _check_route(x, np.full(96, -0.0), 6, softmax=softmax, **kind)
+
+
 def test_route_near_ties_go_by_64_bits():
     """Scores a few FP32 roundings apart, where 32 bits would turn the order."""
     say("route near ties")

@@ -120,12 +120,48 @@ __device__ __forceinline__ void better_of(V& v, int& i, V ov, int oi) {
   v = better ? ov : v;
   i = better ? oi : i;
 }
+// Whole numbers that order as floats do (no NaN, no -0), and as doubles do but
+// for ties in their upper halves.
+__device__ __forceinline__ uint32_t upper_key(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint32_t upper_key(double v) {
+  const uint32_t u = (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 32);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_lane(float v, int l) {
+  return __builtin_bit_cast(float,
+                            __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+__device__ __forceinline__ double from_lane(double v, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
+  const uint64_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
+  return __builtin_bit_cast(double, hi << 32 | lo);
+}
+
+// A wave that has one token takes the largest key first; only where several
+// indices have it the values and indices themselves are joined (48 tokens, 256
+// experts in 8 groups: 10.4 us with every join of 64 bits,
+// 7.4 so, with chosen scores kept and the bias loaded beside the logits).
 template <int L, typename V>
 __device__ __forceinline__ void best_over_lanes(V& v, int& i) {
   if constexpr (std::is_same<V, uint32_t>::value) {
     v = over_lanes<L>(v, [](uint32_t p, uint32_t q) { return q > p ? q : p; });
     i = 0xffff - (int)(v & 0xffff);
   } else {
+    if constexpr (L == 64) {
+      const uint32_t key = upper_key(v);
+      const uint64_t on = __ballot(
+          key == over_lanes<L>(key, [](uint32_t p, uint32_t q) { return q > p ? q : p; }));
+      const int l = __builtin_ctzll(on), first = __builtin_amdgcn_readlane(i, l);
+      if ((on & ~__ballot(i == first)) == 0) {
+        v = from_lane(v, l);
+        i = first;
+        return;
+      }
+    }
     better_of(v, i, dpp<0xB1>(v), (int)dpp<0xB1>((uint32_t)i));
     better_of(v, i, dpp<0x4E>(v), (int)dpp<0x4E>((uint32_t)i));
     better_of(v, i, dpp<0x141>(v), (int)dpp<0x141>((uint32_t)i));
@@ -176,6 +212,7 @@ template <typename V, int L, int P>
 __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
   constexpr bool kPacked = std::is_same<V, uint32_t>::value;
   typedef typename std::conditional<std::is_same<V, double>::value, double, float>::type F;
+  constexpr bool kKeep = std::is_same<V, double>::value;
   constexpr int TOKENS = 256 / L;
   __shared__ V marks[TOKENS][L * P];
   const int lane = threadIdx.x & (L - 1), slot = threadIdx.x / L;
@@ -186,6 +223,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
 
   float x[P];
   V c[P];
+  float b[std::is_same<V, double>::value ? P : 1];  // loaded with the logits: one trip
   float top = -inf;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
@@ -196,24 +234,25 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
       c[i] = x[i] > -inf ? packed(h, e) : none<V>();
     } else {
       x[i] = e < a.E ? load_logit(a, row + e) : -inf;
+      if constexpr (sizeof(V) == 8) b[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
     }
     top = x[i] > top ? x[i] : top;  // NaN: not above
   }
   top = over_lanes<L>(top, [](float p, float q) { return q > p ? q : p; });
   F sum = 1;  // softmax: the scores' denominator
+  F s[kKeep ? P : 1];  // the scores' numerators
   const bool softmax = a.score == MOE_SOFTMAX;
   if constexpr (std::is_same<V, double>::value) {
     F own = 0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      c[i] = x[i] > -inf ? numerator<F>(a, x[i], top) : 0;
-      own += c[i];
+      s[i] = x[i] > -inf ? numerator<F>(a, x[i], top) : 0;
+      own += s[i];
     }
     if (softmax) sum = over_lanes<L>(own, sum_of<F>);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int e = lane + L * i;
-      const F v = (softmax ? c[i] / sum : c[i]) + (a.bias && e < a.E ? (F)a.bias[e] : (F)0);
+      const F v = (softmax ? s[i] / sum : s[i]) + (F)b[i];
       c[i] = x[i] > -inf && v > none<V>() ? v : none<V>();
     }
   } else {
@@ -225,7 +264,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
     }
     if constexpr (!kPacked)
 #pragma unroll
-      for (int i = 0; i < P; ++i) c[i] = x[i] > none<V>() ? x[i] : none<V>();
+      for (int i = 0; i < P; ++i) c[i] = x[i] > none<V>() ? x[i] + 0.f : none<V>();  // -0 is 0
   }
 
   if (a.groups > 1) {
@@ -250,12 +289,24 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
           second = v > first ? first : v > second ? v : second;
           first = v > first ? v : first;
         }
-      for (int d = 1; d < share; d *= 2) {
-        const V f = __shfl_xor(first, d), s = __shfl_xor(second, d);
+      // lanes join as in over_lanes: what was joined before is alike in them
+      auto join = [&](V f, V s) {
         const V least = f > first ? first : f;
         second = s > second ? s : second;
         second = least > second ? least : second;
         first = f > first ? f : first;
+      };
+      if (share > 1) join(dpp<0xB1>(first), dpp<0xB1>(second));
+      if (share > 2) join(dpp<0x4E>(first), dpp<0x4E>(second));
+      if (share > 4) join(dpp<0x141>(first), dpp<0x141>(second));
+      if (share > 8) join(dpp<0x140>(first), dpp<0x140>(second));
+      if constexpr (L == 64) {
+        V f, s;
+        if (share > 16) {
+          both_sides<16>(first, first, f);
+          both_sides<16>(second, second, s);
+          join(f, s);
+        }
       }
       if constexpr (kPacked)
         mark[m] = first ? (first & 0xffff0000u) | (0xffffu - g) : 0;
@@ -286,8 +337,12 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
 
   constexpr int MINE = MOE_MAX_TOP / L > 0 ? MOE_MAX_TOP / L : 1;
   int mine[MINE];  // lane l: choices l, l + L
+  F score[MINE];
 #pragma unroll
-  for (int m = 0; m < MINE; ++m) mine[m] = -1;
+  for (int m = 0; m < MINE; ++m) {
+    mine[m] = -1;
+    score[m] = 0;
+  }
   for (int j = 0; j < a.k; ++j) {
     V best = c[0];
     int at = lane;
@@ -300,14 +355,25 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
     if (!(best > none<V>())) at = -1;
 #pragma unroll
     for (int m = 0; m < MINE; ++m) mine[m] = lane + L * m == j ? at : mine[m];
+    if constexpr (kKeep && L == 64) {
+      // its score from the lane that has it: cheaper than once more a trip for
+      // the logit and an exponential
+      const int chosen = __builtin_amdgcn_readfirstlane(at);
+      F of = s[0];
+#pragma unroll
+      for (int i = 1; i < P; ++i) of = chosen / L == i ? s[i] : of;
+      of = from_lane(of, chosen & (L - 1));
+      score[0] = lane == j && chosen >= 0 ? of : score[0];
+    }
 #pragma unroll
     for (int i = 0; i < P; ++i) c[i] = at == lane + L * i ? none<V>() : c[i];
   }
 
-  F total = 0, score[MINE];
+  F total = 0;
 #pragma unroll
   for (int m = 0; m < MINE; ++m) {
-    score[m] = mine[m] < 0 ? (F)0 : numerator<F>(a, load_logit(a, row + mine[m]), top);
+    if constexpr (!(kKeep && L == 64))
+      if (mine[m] >= 0) score[m] = numerator<F>(a, load_logit(a, row + mine[m]), top);
     total += score[m];
   }
   if (a.renorm) sum = over_lanes<L>(total, sum_of<F>);
