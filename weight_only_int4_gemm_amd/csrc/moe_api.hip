@@ -184,12 +184,13 @@ ProductPlan plan_matrix(int M, int K, int N, int cus) {
 //   (64 x 128 between or above: 135, 167, 198; 256 rows: 64 x 256 389,
 //   128 x 128 437, 256 x 256 522; 1024 rows: 1409, 1379, 1393)
 // e4m3, us with 64 experts of 2048 x 2816:
-//   mean                     4      16     32     64     128    256
+//   mean                     4      16     32     64     96     128    192    256
 //   streaming kernel         59.7   82.2
 //   tiles of 32 x 128        59.0   65.5   74.3
-//   64 x 128                               69.4   80.5   115
-//   128 x 256                                     86.6   97.7   149
-//   256 x 256                                                   148
+//   64 x 128                               69.4   80.5   98.6   120
+//   128 x 128                                     86.6   95.7   111    135    171
+//   256 x 256                                                   130    150    161
+//   (128 x 256, eight waves: 104 at 96, 126, 153, 168)
 // 4 bits stream four column blocks a workgroup: 16 tokens through 8 experts of
 // 4096 x 22016 93.2 us with two, 74.6 with four; with fewer workgroups than
 // compute units two, and eight waves (one token, 11008 x 4096: 25.6 and 19.4).
@@ -199,7 +200,7 @@ ProductPlan plan_experts(bool f8, int rows, int used, int W, int cus) {
     if (mean <= 6) return stream_plan(1, 2, 4, 4);
     if (mean <= 24) return tile_plan(2, 2, 1, 4, 4);
     if (mean <= 96) return tile_plan(4, 2, 1, 4, 4);
-    return mean <= 240 ? tile_plan(8, 2, 1, 8, 4) : tile_plan(8, 4, 2, 4, 4);
+    return mean <= 224 ? tile_plan(8, 2, 1, 4, 4) : tile_plan(8, 4, 2, 4, 4);
   }
   if (mean <= 7)
     return (int64_t)used * (W / 64) >= cus ? stream_plan(1, 4, 4, 3) : stream_plan(1, 2, 8, 3);

@@ -10,11 +10,11 @@ namespace w4a16 {
 // columns share a workgroup.  e4m3, 4 bits (experts only).
 #define W4A16_STREAM_F8(X) X(1, 1, 8, 4) X(1, 2, 4, 4) X(2, 1, 8, 3)
 #define W4A16_STREAM_I4(X) X(1, 2, 8, 3) X(1, 4, 4, 3)
-// Tile kernel: (MB, NB, WM, WN, NS).
-#define W4A16_TILE_F8(X)                                                           \
-  X(2, 1, 1, 4, 4) X(2, 2, 1, 4, 4) X(4, 1, 1, 4, 4) X(4, 2, 1, 4, 4) X(8, 2, 1, 4, 4) \
-  X(8, 2, 1, 8, 4) X(8, 4, 2, 4, 4)
-#define W4A16_TILE_I4(X) X(2, 2, 1, 4, 4) X(4, 4, 1, 4, 4)
+// Tile kernel: (MB, NB, WM, WN, NS, whether experts take it, with the gate too).
+#define W4A16_TILE_F8(X)                                                                \
+  X(2, 1, 1, 4, 4, 0) X(2, 2, 1, 4, 4, 1) X(4, 1, 1, 4, 4, 0) X(4, 2, 1, 4, 4, 1)       \
+  X(8, 2, 1, 4, 4, 1) X(8, 2, 1, 8, 4, 0) X(8, 4, 2, 4, 4, 1)
+#define W4A16_TILE_I4(X) X(2, 2, 1, 4, 4, 1) X(4, 4, 1, 4, 4, 1)
 
 template <int F>
 hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool gate,
@@ -44,10 +44,10 @@ hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool ga
   }
   const dim3 grid((unsigned)((int64_t)plan.tiles_m * plan.tiles_n), (unsigned)plan.splits);
   const dim3 block(64 * plan.wm * plan.wn);
-#define W4A16_CASE(MB_, NB_, WM_, WN_, NS_)                                                      \
+#define W4A16_CASE(MB_, NB_, WM_, WN_, NS_, GATE_)                                               \
   if (plan.mb == MB_ && plan.nb == NB_ && plan.wm == WM_ && plan.wn == WN_ && plan.depth == NS_) { \
     if (gate) {                                                                                  \
-      if constexpr (NB_ % 2 == 0)                                                                \
+      if constexpr (GATE_)                                                                       \
         hipLaunchKernelGGL((product_tile_kernel<F, MB_, NB_, WM_, WN_, NS_, true>), grid, block, \
                            0, stream, a);                                                        \
       else                                                                                       \
