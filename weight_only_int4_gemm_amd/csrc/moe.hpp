@@ -13,12 +13,11 @@ struct ProductArgs;
 // How one product is cut into work.
 //  tile     0: the streaming kernel, 1: the tile kernel
 //  mb, nb   16-row and 16-column blocks of a wave
-//  wm, wn   tile kernel: waves along rows and columns
-//           streaming kernel: wm = 1, wn = waves that divide K
+//  waves    tile kernel: along columns; streaming kernel: that divide K
 //  tm, tn   rows of a workgroup and its output columns
 //  tiles_m  the most row tiles; splits: K ranges of a tile (tile kernel)
 struct ProductPlan {
-  int tile, mb, nb, wm, wn, depth;
+  int tile, mb, nb, waves, depth;
   int tm, tn, tiles_m, tiles_n, splits;
   size_t workspace_bytes;
 };

@@ -72,8 +72,8 @@ int describe(int format, int rows, int K, int N, int E, bool gate, int cus, char
   if (cus <= 0) return W4A16_ERR_DEVICE;
   const ProductPlan p = make_product_plan(format, rows, K, N, E, gate, cus);
   if (!good_plan(p)) return W4A16_ERR_SHAPE;
-  std::snprintf(buf, len, "%s<%d,%d,%d,%d,%d> tile=%dx%d grid=%dx%d splits=%d workspace=%zu",
-                p.tile ? "product_tile_kernel" : "product_stream_kernel", p.mb, p.nb, p.wm, p.wn,
+  std::snprintf(buf, len, "%s<%d,%d,%d,%d> tile=%dx%d grid=%dx%d splits=%d workspace=%zu",
+                p.tile ? "product_tile_kernel" : "product_stream_kernel", p.mb, p.nb, p.waves,
                 p.depth, p.tm, p.tn, p.tiles_m, p.tiles_n, p.splits, p.workspace_bytes);
   return W4A16_OK;
 }
@@ -104,20 +104,18 @@ namespace {
 // `alone` microseconds a K block for a workgroup that has its compute unit to
 // itself, `shared` for each of several, `once` for the rest of a workgroup.
 struct Tile {
-  int mb, nb, wm, wn, depth;
+  int mb, nb;
   float alone, shared, once;
 };
-constexpr Tile kTilesF8[] = {
-    {2, 1, 1, 4, 4, 0.30f, 0.19f, 1.5f}, {4, 1, 1, 4, 4, 0.36f, 0.26f, 1.5f},
-    {4, 2, 1, 4, 4, 0.49f, 0.37f, 2.f},  {8, 2, 1, 4, 4, 0.62f, 0.56f, 7.f},
-    {8, 2, 1, 8, 4, 0.90f, 1.08f, 11.f}, {8, 4, 2, 4, 4, 1.45f, 1.84f, 18.f}};
+constexpr Tile kTilesF8[] = {{2, 1, 0.30f, 0.19f, 1.5f}, {4, 1, 0.36f, 0.26f, 1.5f},
+                             {4, 2, 0.49f, 0.37f, 2.f},  {8, 2, 0.62f, 0.56f, 7.f},
+                             {8, 4, 1.33f, 0.90f, 12.f}};
 
 ProductPlan stream_plan(int mb, int nb, int waves, int depth) {
   ProductPlan p{};
   p.mb = mb;
   p.nb = nb;
-  p.wm = 1;
-  p.wn = waves;
+  p.waves = waves;
   p.depth = depth;
   p.tm = 16 * mb;
   p.tn = 16 * nb;
@@ -125,16 +123,15 @@ ProductPlan stream_plan(int mb, int nb, int waves, int depth) {
   return p;
 }
 
-ProductPlan tile_plan(int mb, int nb, int wm, int wn, int depth) {
+ProductPlan tile_plan(int mb, int nb) {
   ProductPlan p{};
   p.tile = 1;
   p.mb = mb;
   p.nb = nb;
-  p.wm = wm;
-  p.wn = wn;
-  p.depth = depth;
-  p.tm = 16 * mb * wm;
-  p.tn = 16 * nb * wn;
+  p.waves = 4;
+  p.depth = 4;
+  p.tm = 16 * mb;
+  p.tn = 16 * nb * p.waves;
   p.splits = 1;
   return p;
 }
@@ -157,7 +154,7 @@ ProductPlan plan_matrix(int M, int K, int N, int cus) {
   ProductPlan best{};
   float least = 0.f;
   for (const Tile& t : kTilesF8) {
-    ProductPlan p = tile_plan(t.mb, t.nb, t.wm, t.wn, t.depth);
+    ProductPlan p = tile_plan(t.mb, t.nb);
     const int64_t tiles = (int64_t)((M + p.tm - 1) / p.tm) * ((N + p.tn - 1) / p.tn);
     for (int s = 1; s <= 8; s *= 2) {
       if (s > 1 && (KB < 8 * s || tiles * s > 2 * cus || tiles > kMaxSplitTiles)) break;
@@ -184,13 +181,12 @@ ProductPlan plan_matrix(int M, int K, int N, int cus) {
 //   (64 x 128 between or above: 135, 167, 198; 256 rows: 64 x 256 389,
 //   128 x 128 437, 256 x 256 522; 1024 rows: 1409, 1379, 1393)
 // e4m3, us with 64 experts of 2048 x 2816:
-//   mean                     4      16     32     64     96     128    192    256
+//   mean                     4      16     32     64     96     128    192    384
 //   streaming kernel         59.7   82.2
 //   tiles of 32 x 128        59.0   65.5   74.3
-//   64 x 128                               69.4   80.5   98.6   120
-//   128 x 128                                     86.6   95.7   111    135    171
-//   256 x 256                                                   130    150    161
-//   (128 x 256, eight waves: 104 at 96, 126, 153, 168)
+//   64 x 128                               69.4   80.5   100    120    162
+//   128 x 256                                            96.3   102    120    184
+//   (128 x 128: 94.8 at 96, 112, 135, 229; 64 x 256: 86.4 at 72, 143 at 192)
 // 4 bits stream four column blocks a workgroup: 16 tokens through 8 experts of
 // 4096 x 22016 93.2 us with two, 74.6 with four; with fewer workgroups than
 // compute units two, and eight waves (one token, 11008 x 4096: 25.6 and 19.4).
@@ -198,13 +194,12 @@ ProductPlan plan_experts(bool f8, int rows, int used, int W, int cus) {
   const int mean = (rows + used - 1) / used;
   if (f8) {
     if (mean <= 6) return stream_plan(1, 2, 4, 4);
-    if (mean <= 24) return tile_plan(2, 2, 1, 4, 4);
-    if (mean <= 96) return tile_plan(4, 2, 1, 4, 4);
-    return mean <= 224 ? tile_plan(8, 2, 1, 4, 4) : tile_plan(8, 4, 2, 4, 4);
+    if (mean <= 24) return tile_plan(2, 2);
+    return mean <= 80 ? tile_plan(4, 2) : tile_plan(8, 4);
   }
   if (mean <= 7)
     return (int64_t)used * (W / 64) >= cus ? stream_plan(1, 4, 4, 3) : stream_plan(1, 2, 8, 3);
-  return mean <= 48 ? tile_plan(2, 2, 1, 4, 4) : tile_plan(4, 4, 1, 4, 4);
+  return mean <= 48 ? tile_plan(2, 2) : tile_plan(4, 4);
 }
 
 }  // namespace

@@ -214,15 +214,67 @@ __device__ __forceinline__ float silu_gate(float x, float u) {
   return x * __builtin_amdgcn_rcpf(1.f + __expf(-x)) * u;
 }
 
-// Four neighbouring columns of one row.
-__device__ __forceinline__ void store4(const ProductArgs& p, int64_t at, float4_t v) {
+// Four neighbouring columns of one row, rounded.
+__device__ __forceinline__ uint2 round4(const ProductArgs& p, float4_t v) {
   ushort4 h;
   if (p.dtype == W4A16_DTYPE_BF16)
     h = ushort4{round16(v[0], true), round16(v[1], true), round16(v[2], true), round16(v[3], true)};
   else
     h = ushort4{round16(v[0], false), round16(v[1], false), round16(v[2], false),
                 round16(v[3], false)};
-  *reinterpret_cast<ushort4*>(p.C + at) = h;
+  return __builtin_bit_cast(uint2, h);
+}
+
+__device__ __forceinline__ void store4(const ProductArgs& p, int64_t at, float4_t v) {
+  *reinterpret_cast<uint2*>(p.C + at) = round4(p, v);
+}
+
+// x's odd rows of 16 lanes change places with y's even ones (D = 16), x's
+// second half of the wave with y's first (D = 32).
+template <int D>
+__device__ __forceinline__ void swap_lanes(uint2& x, uint2& y) {
+  if constexpr (D == 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(x.x, y.x, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(x.y, y.y, false, false);
+    x = uint2{a[0], b[0]};
+    y = uint2{a[1], b[1]};
+  } else {
+    const auto a = __builtin_amdgcn_permlane32_swap(x.x, y.x, false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(x.y, y.y, false, false);
+    x = uint2{a[0], b[0]};
+    y = uint2{a[1], b[1]};
+  }
+}
+
+// OB blocks of 16 columns from column block ob0, a lane's x[ob] four columns of
+// its row in each.  The four lanes of a row exchange theirs, so that each
+// stores 16 bytes at a time (64 experts of 1408 x 2048, 768 rows each, and their
+// sum: 292 -> 269 us in 256 x 256 tiles).
+template <int OB>
+__device__ __forceinline__ void store_blocks(const ProductArgs& p, int r, int end, int ob0,
+                                             int quarter, uint2 (&x)[OB]) {
+  int ob = 0, column = 4 * quarter;
+  if constexpr (OB == 2) {
+    swap_lanes<16>(x[0], x[1]);  // quarters 2 (q / 2), + 1 of block q % 2
+    ob = quarter & 1;
+    column = 8 * (quarter >> 1);
+  } else if constexpr (OB == 4) {
+    swap_lanes<32>(x[0], x[2]);
+    swap_lanes<32>(x[1], x[3]);
+    swap_lanes<16>(x[0], x[1]);
+    swap_lanes<16>(x[2], x[3]);  // all of block q
+    ob = quarter;
+    column = 0;
+  }
+  static_assert(OB == 1 || OB == 2 || OB == 4, "blocks");
+  if (r >= end || 16 * (ob0 + ob) >= p.N) return;
+  uint16_t* const to = p.C + (int64_t)r * p.N + 16 * (ob0 + ob) + column;
+  if constexpr (OB == 1)
+    *reinterpret_cast<uint2*>(to) = x[0];
+  else
+#pragma unroll
+    for (int i = 0; i < OB; i += 2)
+      reinterpret_cast<uint4*>(to)[i / 2] = uint4{x[i].x, x[i].y, x[i + 1].x, x[i + 1].y};
 }
 
 // ---------------------------------------------------------------------------
@@ -401,16 +453,20 @@ __global__ __launch_bounds__(64 * WAVES) void product_stream_kernel(ProductArgs 
 // tiles in flight on a die share rows and columns.
 constexpr int kTileRun = 4;
 
-// WM x WN waves, each 16 MB rows by NB blocks of 16 weight columns; NS stages.
-template <int F, int MB, int NB, int WM, int WN, int NS, bool GATE>
-__global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductArgs p) {
+// 16 MB rows; WAVES waves, each NB blocks of 16 weight columns.  With four
+// waves two workgroups or more share a compute unit, so that one's first loads
+// and stores run beside the other's products: 128 x 256 e4m3 tiles so against
+// 256 x 256 in eight waves 816 : 826 us for 8192 x 28672 at M = 4096, 239 : 284
+// for 11008 x 12288 at 2048, 245 : 270 for 64 experts of 1408 x 2048, 768 rows
+// each (and their sum).
+template <int F, int MB, int NB, int WAVES, bool GATE>
+__global__ __launch_bounds__(64 * WAVES, 2) void product_tile_kernel(ProductArgs p) {
   typedef Product<F> P;
-  constexpr int WAVES = WM * WN;
-  constexpr int TM = 16 * MB * WM;
+  constexpr int TM = 16 * MB;
+  constexpr int NS = 4;  // stages of activations
   constexpr int OB = GATE ? NB / 2 : NB;        // output column blocks of a wave
   constexpr int SUB = P::kRowBlock / 128;       // 128-byte slices of a row's K block
   constexpr int ALOADS = SUB * ((TM / 8 + WAVES - 1) / WAVES);  // 1 KiB loads of a wave
-  static_assert(NS == 2 || NS == 4, "two or four stages");
   // piece c of row r of a slice at slot c ^ (r & 7): a fragment read's lanes
   // spread over all banks
   struct Stage {
@@ -420,8 +476,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   // does not touch the others
   __shared__ Stage st0;
   __shared__ Stage st1;
-  __shared__ typename std::conditional<(NS > 2), Stage, char>::type st2;
-  __shared__ typename std::conditional<(NS > 2), Stage, char>::type st3;
+  __shared__ Stage st2;
+  __shared__ Stage st3;
   // e4m3: the rows' scales of four K blocks, and of the next four; two objects
   // for the same reason (as one, every fourth block began with a wait for all
   // loads in flight: 4096 x 4096 at M = 256 16.1 -> 13.9 us)
@@ -433,7 +489,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 
   const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN;
 
   const RowTiles tiles = count_tiles(p, TM);
   const int split = blockIdx.y;
@@ -494,7 +549,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   // addresses are the wave's own but for the lane's 16 bytes, so buffer loads
   // keep them in scalar registers; one resource for the gate columns, one for
   // the up columns, both from the wave's first block.
-  const int ob0 = (tile_n * WN + wn) * OB;  // first output column block
+  const int ob0 = (tile_n * WAVES + wave) * OB;  // first output column block
   const int blocks = p.N / 16, first = ob0 < blocks ? ob0 : blocks - 1;
   constexpr int HALVES = GATE ? 2 : 1;
   const uint32_t lane16 = lane * 16;
@@ -552,12 +607,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = float4_t{0.f, 0.f, 0.f, 0.f};
   const float4_t zero = {0.f, 0.f, 0.f, 0.f};
 
-  constexpr int SETS = NS > 2 && NB <= 2 && MB <= 8 ? NS : 2;
+  constexpr int SETS = NB <= 2 ? NS : 2;
   constexpr int LOADS = WLOADS + ALOADS;
   constexpr int WINSTRS = NB * P::kBPieces + SCALES;  // load instructions of the weights
-  constexpr int NEWER = NS == 2 ? 0 : SETS == NS ? (NS - 2) * (WINSTRS + ALOADS) : ALOADS;
+  constexpr int NEWER = SETS == NS ? (NS - 2) * (WINSTRS + ALOADS) : ALOADS;
   // Rows of a wave are 16 apart, so a lane's swizzle is one number.
-  const int l7 = l16 & 7, arow0 = (wm * MB * 16 + l16) * 8;
+  const int l7 = l16 & 7, arow0 = l16 * 8;
   const int swz0 = arow0 + (quarter ^ l7), swz1 = arow0 + ((quarter + 4) ^ l7);
   // u: the K block's place in its group of four; sc: the group's row scales;
   // issue(i): the i-th of the loads for later K blocks.  They are spread over
@@ -579,7 +634,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
       auto read = [&](int mb) {
         a[mb % (PRE + 1)][0] = sg.a[swz0 + mb * 128];
         a[mb % (PRE + 1)][1] = sg.a[swz1 + mb * 128];
-        as[mb % AS] = reinterpret_cast<const float*>(sc + wm * MB * 16 + l16 + mb * 16)[u];
+        as[mb % AS] = reinterpret_cast<const float*>(sc + l16 + mb * 16)[u];
       };
       auto add = [&](int i) {
         const int mb = i / NB, nb = i % NB;
@@ -679,10 +734,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   // as many sets as stages, what block kb waits for is older than the loads of
   // the NS - 2 blocks before it; with fewer, than the newest stage's.
   auto stage = [&](int i) -> Stage& {
-    if constexpr (NS == 4)
-      return i == 0 ? st0 : i == 1 ? st1 : i == 2 ? st2 : st3;
-    else
-      return i == 0 ? st0 : st1;
+    return i == 0 ? st0 : i == 1 ? st1 : i == 2 ? st2 : st3;
   };
   constexpr int UNROLL = P::kF8 ? 8 : NS;
   Weights weights[SETS];
@@ -783,16 +835,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb) {
-    const int r = rt.row0 + (wm * MB + mb) * 16 + l16;
+    const int r = rt.row0 + mb * 16 + l16;
+    uint2 out[OB];
 #pragma unroll
     for (int ob = 0; ob < OB; ++ob) {
-      const int c = 16 * (ob0 + ob) + 4 * quarter;
       float4_t x = acc[mb][ob];
       if constexpr (GATE)
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = silu_gate(x[j], acc[mb][OB + ob][j]);
-      if (r < rt.end && c < p.N) store4(p, (int64_t)r * p.N + c, x);
+      out[ob] = round4(p, x);
     }
+    store_blocks<OB>(p, r, rt.end, ob0, quarter, out);
   }
 }
 

@@ -10,19 +10,18 @@ namespace w4a16 {
 // columns share a workgroup.  e4m3, 4 bits (experts only).
 #define W4A16_STREAM_F8(X) X(1, 1, 8, 4) X(1, 2, 4, 4) X(2, 1, 8, 3)
 #define W4A16_STREAM_I4(X) X(1, 2, 8, 3) X(1, 4, 4, 3)
-// Tile kernel: (MB, NB, WM, WN, NS, whether experts take it, with the gate too).
-#define W4A16_TILE_F8(X)                                                                \
-  X(2, 1, 1, 4, 4, 0) X(2, 2, 1, 4, 4, 1) X(4, 1, 1, 4, 4, 0) X(4, 2, 1, 4, 4, 1)       \
-  X(8, 2, 1, 4, 4, 1) X(8, 2, 1, 8, 4, 0) X(8, 4, 2, 4, 4, 1)
-#define W4A16_TILE_I4(X) X(2, 2, 1, 4, 4, 1) X(4, 4, 1, 4, 4, 1)
+// Tile kernel: (MB, NB, WAVES, whether experts take it, with the gate too).
+#define W4A16_TILE_F8(X) \
+  X(2, 1, 4, 0) X(2, 2, 4, 1) X(4, 1, 4, 0) X(4, 2, 4, 1) X(8, 2, 4, 0) X(8, 4, 4, 1)
+#define W4A16_TILE_I4(X) X(2, 2, 4, 1) X(4, 4, 4, 1)
 
 template <int F>
 hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool gate,
                           hipStream_t stream) {
   if (plan.tile == 0) {
-    const dim3 grid((unsigned)((int64_t)plan.tiles_m * plan.tiles_n)), block(64 * plan.wn);
+    const dim3 grid((unsigned)((int64_t)plan.tiles_m * plan.tiles_n)), block(64 * plan.waves);
 #define W4A16_CASE(MB_, NB_, WAVES_, DEPTH_)                                                      \
-  if (plan.mb == MB_ && plan.nb == NB_ && plan.wn == WAVES_ && plan.depth == DEPTH_) {            \
+  if (plan.mb == MB_ && plan.nb == NB_ && plan.waves == WAVES_ && plan.depth == DEPTH_) {            \
     if (gate) {                                                                                   \
       if constexpr (NB_ % 2 == 0)                                                                 \
         hipLaunchKernelGGL((product_stream_kernel<F, MB_, NB_, WAVES_, DEPTH_, true>), grid,      \
@@ -43,19 +42,19 @@ hipError_t launch_product(const ProductPlan& plan, const ProductArgs& a, bool ga
     return hipErrorInvalidValue;
   }
   const dim3 grid((unsigned)((int64_t)plan.tiles_m * plan.tiles_n), (unsigned)plan.splits);
-  const dim3 block(64 * plan.wm * plan.wn);
-#define W4A16_CASE(MB_, NB_, WM_, WN_, NS_, GATE_)                                               \
-  if (plan.mb == MB_ && plan.nb == NB_ && plan.wm == WM_ && plan.wn == WN_ && plan.depth == NS_) { \
-    if (gate) {                                                                                  \
-      if constexpr (GATE_)                                                                       \
-        hipLaunchKernelGGL((product_tile_kernel<F, MB_, NB_, WM_, WN_, NS_, true>), grid, block, \
-                           0, stream, a);                                                        \
-      else                                                                                       \
-        return hipErrorInvalidValue;                                                             \
-    } else                                                                                       \
-      hipLaunchKernelGGL((product_tile_kernel<F, MB_, NB_, WM_, WN_, NS_, false>), grid, block, 0, \
-                         stream, a);                                                             \
-    return hipGetLastError();                                                                    \
+  const dim3 block(64 * plan.waves);
+#define W4A16_CASE(MB_, NB_, WAVES_, GATE_)                                                     \
+  if (plan.mb == MB_ && plan.nb == NB_ && plan.waves == WAVES_) {                               \
+    if (gate) {                                                                                 \
+      if constexpr (GATE_)                                                                      \
+        hipLaunchKernelGGL((product_tile_kernel<F, MB_, NB_, WAVES_, true>), grid, block, 0,    \
+                           stream, a);                                                          \
+      else                                                                                      \
+        return hipErrorInvalidValue;                                                            \
+    } else                                                                                      \
+      hipLaunchKernelGGL((product_tile_kernel<F, MB_, NB_, WAVES_, false>), grid, block, 0,     \
+                         stream, a);                                                            \
+    return hipGetLastError();                                                                   \
   }
   if constexpr (F == kProdF8) {
     W4A16_TILE_F8(W4A16_CASE)
