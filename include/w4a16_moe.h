@@ -120,7 +120,7 @@ int moe_tables(const int32_t* ids, int32_t* starts, int32_t* order, int32_t* whe
  *   C[p] = act(A[row(p)] . dequant(expert e)),  starts[e] <= p < starts[e + 1]
  *   row(p) = order[p] / k, or p where order is NULL
  *
- * A       (device, read)  `dtype` [a_rows][K].
+ * A       (device, read)  `dtype` [a_rows][K]; a_rows >= rows without order.
  * order   (device, read)  int32 [rows] from moe_tables, or NULL.  An entry
  *         outside 0 .. a_rows * k - 1 stands for row 0.
  * starts  (device, read)  int32 [E + 1]; values are taken within 0 .. rows.
@@ -180,7 +180,7 @@ int moe_gemm_describe(int form, int rows, int K, int N, int E, int activation, i
  * Y       (device, read)  `dtype` [rows][N].
  * where   (device, read)  int32 [T][k].   weights (device, read) FP32 [T][k].
  * out     (device, write) `dtype` [T][N].
- * T       >= 0, N >= 0 a multiple of 8 (0 of either: nothing is launched),
+ * T       >= 0, N 0..2^24 a multiple of 8 (0 of either: nothing is launched),
  *         k 1..MOE_MAX_TOP, rows >= 0 (Y may be NULL for 0).
  * Errors: W4A16_ERR_NULL, _SHAPE, _ALIGN (16 bytes; where and weights 4),
  *         _DTYPE, _DEVICE, _LAUNCH.

@@ -80,7 +80,7 @@ def close(got, want, bound, what, name=None):
 # 8-bit products
 # ---------------------------------------------------------------------------
 
-@pytest.mark.parametrize("N,K", [(16, 128), (144, 640), (4096, 1024)])
+@pytest.mark.parametrize("N,K", [(16, 128), (144, 640), (4096, 1024), (16384, 20480)])
 def test_repack(N, K):
     say("repack", N, K)
     q = np.random.default_rng(0).integers(0, 256, (N, K)).astype(np.uint8)

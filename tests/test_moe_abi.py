@@ -159,7 +159,7 @@ def test_experts_refusals(lib):
         _no(f, base, ALIGN, order=A[1] + 2)
         for bad in (dict(rows=-1), dict(rows=(1 << 24) + 1), dict(K=0), dict(K=192), dict(N=-32),
                     dict(N=24), dict(E=0), dict(E=1025), dict(k=0), dict(a_rows=0),
-                    dict(N=1 << 30)):
+                    dict(N=1 << 30), dict(order=None)):  # 8 rows of A for 16
             _no(f, base, SHAPE, **bad)
         _no(f, base, DTYPE, dtype=2)
         _no(f, base, EPILOGUE, activation=2)
@@ -181,7 +181,8 @@ def test_combine_refusals(lib):
     for k in ("Y", "where", "weights", "out"):
         _no(f, COMBINE, NULL, **{k: None})
         _no(f, COMBINE, ALIGN, **{k: COMBINE[k] + 2})
-    for bad in (dict(T=-1), dict(k=0), dict(k=33), dict(N=-8), dict(N=12), dict(rows=-1)):
+    for bad in (dict(T=-1), dict(k=0), dict(k=33), dict(N=-8), dict(N=12),
+                dict(N=(1 << 24) + 8), dict(N=(1 << 31) - 8), dict(rows=-1)):
         _no(f, COMBINE, SHAPE, **bad)
     _no(f, COMBINE, DTYPE, dtype=2)
     _no(f, COMBINE, SHAPE, out=A[0] + 16 * 48 * 2 - 16)
@@ -235,7 +236,11 @@ def test_describe_refusals():
                  lambda: w4.moe_gemm_describe(5, 4, 128, 16, 2, 0, 256),
                  lambda: w4.moe_gemm_describe(8, 4, 128, 16, 2, 1, 256),
                  lambda: w4.moe_gemm_describe(4, 4, 128, 16, 0, 0, 256),
-                 lambda: w4.moe_gemm_describe(4, 4, 128, 16, 2, 3, 256)):
+                 lambda: w4.moe_gemm_describe(4, 4, 128, 16, 2, 3, 256),
+                 # 2^32 threads and more
+                 lambda: w4.moe_gemm_describe(4, 1 << 24, 128, 1 << 22, 4, 1, 256),
+                 lambda: w4.moe_gemm_describe(8, 1 << 24, 128, 1 << 24, 4, 0, 256),
+                 lambda: w4.w8a8_describe(1 << 24, 128, 1 << 24, 256)):
         with pytest.raises(w4.W4A16Error):
             call()
 

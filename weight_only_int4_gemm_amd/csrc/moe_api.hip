@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kW8a8LayoutVersion = 1;
 constexpr int kMaxRows = 1 << 24;        // rows of one call
-constexpr int64_t kMaxGroups = 1 << 24;  // workgroups of one launch dimension
+constexpr int kMaxColumns = 1 << 24;
 constexpr int64_t kMaxStride = 1ll << 32;
 
 bool aligned(const void* p, int to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -45,7 +45,7 @@ bool good_dtype(int dtype) { return dtype == W4A16_DTYPE_F16 || dtype == W4A16_D
 // of one matrix.
 bool good_weights(int K, int64_t W) {
   return K > 0 && K % kBlockK == 0 && K <= (1 << 20) && W > 0 && W % kBlockN == 0 &&
-         W <= (1ll << 36) / K && W <= (1 << 24);
+         W <= (1ll << 36) / K && W <= kMaxColumns;
 }
 
 int done(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_LAUNCH; }
@@ -58,7 +58,8 @@ int check_product(int rows, int K, int N, int E, bool gate, bool f8) {
 }
 
 bool good_plan(const ProductPlan& p) {
-  return (int64_t)p.tiles_m * p.tiles_n <= kMaxGroups;
+  // threads of one launch dimension; the tile counts themselves fit in int
+  return (int64_t)p.tiles_m * p.tiles_n * 64 * p.waves < (1ll << 32);
 }
 
 int describe(int format, int rows, int K, int N, int E, bool gate, int cus, char* buf,
@@ -87,7 +88,7 @@ int check_experts(const void* A, int a_rows, const int32_t* order, int k, const 
   const int rc = check_product(rows, K, N, E, activation == MOE_ACT_SILU_GATE, f8);
   if (rc != W4A16_OK) return rc;
   if (rows == 0 || N == 0) return W4A16_OK;
-  if (k < 1 || a_rows < 1 || a_rows > kMaxRows) return W4A16_ERR_SHAPE;
+  if (k < 1 || a_rows < (order ? 1 : rows) || a_rows > kMaxRows) return W4A16_ERR_SHAPE;
   if (!A || !starts || !Bpacked || !scales || !C) return W4A16_ERR_NULL;
   if (!aligned(A, 16) || !aligned(Bpacked, 16) || !aligned(scales, 16) || !aligned(C, 16) ||
       !aligned(starts, 4) || !aligned(order, 4))
@@ -230,7 +231,7 @@ int w8a8_layout_version(void) { return kW8a8LayoutVersion; }
 size_t w8a8_packed_bytes(int K, int N) { return good_weights(K, N) ? (size_t)K * N : 0; }
 
 int w8a8_repack(const uint8_t* B, uint8_t* Bpacked, int K, int N, void* stream) {
-  if (!good_weights(K, N) || (int64_t)K * N / 4096 > kMaxGroups * 16) return W4A16_ERR_SHAPE;
+  if (!good_weights(K, N)) return W4A16_ERR_SHAPE;
   if (!B || !Bpacked) return W4A16_ERR_NULL;
   if (!aligned(B, 16) || !aligned(Bpacked, 16)) return W4A16_ERR_ALIGN;
   const size_t n = (size_t)K * N;
@@ -458,8 +459,8 @@ int moe_gemm_describe(int form, int rows, int K, int N, int E, int activation, i
 int moe_combine(const uint16_t* Y, int rows, const int32_t* where, const float* weights,
                 uint16_t* out, int T, int k, int N, int dtype, void* stream) {
   if (!good_dtype(dtype)) return W4A16_ERR_DTYPE;
-  if (T < 0 || T > kMaxRows || k < 1 || k > MOE_MAX_TOP || N < 0 || N % 8 || rows < 0 ||
-      rows > kMaxRows)
+  if (T < 0 || T > kMaxRows || k < 1 || k > MOE_MAX_TOP || N < 0 || N % 8 || N > kMaxColumns ||
+      rows < 0 || rows > kMaxRows)
     return W4A16_ERR_SHAPE;
   if (T == 0 || N == 0) return W4A16_OK;
   if ((!Y && rows > 0) || !where || !weights || !out) return W4A16_ERR_NULL;

@@ -14,18 +14,20 @@ hipError_t launch_product_f8(const ProductPlan& plan, const ProductArgs& a, bool
 
 namespace {
 
-// One thread moves 16 codes: 16-byte piece i of the permuted matrix.
+// A thread moves 16 codes at a time: 16-byte piece i of the permuted matrix.
 __global__ __launch_bounds__(256) void w8a8_repack_kernel(const uint8_t* __restrict__ B,
                                                           uint8_t* __restrict__ Bp, int K,
                                                           int64_t pieces) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= pieces) return;
-  const int lane = (int)(i & 63), half = (int)(i >> 6) & 1;
   const int KB = K / kBlockK;
-  const int64_t block = i >> 7;
-  const int64_t n16 = block / KB, kb = block - n16 * KB;
-  const int64_t from = (n16 * 16 + (lane & 15)) * K + kb * kBlockK + half * 64 + (lane >> 4) * 16;
-  reinterpret_cast<uint4*>(Bp)[i] = *reinterpret_cast<const uint4*>(B + from);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces;
+       i += (int64_t)gridDim.x * 256) {
+    const int lane = (int)(i & 63), half = (int)(i >> 6) & 1;
+    const int64_t block = i >> 7;
+    const int64_t n16 = block / KB, kb = block - n16 * KB;
+    const int64_t from =
+        (n16 * 16 + (lane & 15)) * K + kb * kBlockK + half * 64 + (lane >> 4) * 16;
+    reinterpret_cast<uint4*>(Bp)[i] = *reinterpret_cast<const uint4*>(B + from);
+  }
 }
 
 // 16 lanes hold one block of 128 values, eight each.  The largest magnitude
@@ -80,8 +82,9 @@ __global__ __launch_bounds__(256) void w8a8_quantize_kernel(const uint16_t* __re
 
 hipError_t launch_w8a8_repack(const uint8_t* B, uint8_t* Bp, int K, int N, hipStream_t stream) {
   const int64_t pieces = (int64_t)K * N / 16;
-  hipLaunchKernelGGL(w8a8_repack_kernel, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0,
-                     stream, B, Bp, K, pieces);
+  const int64_t groups = (pieces + 255) / 256;
+  hipLaunchKernelGGL(w8a8_repack_kernel, dim3((unsigned)(groups < 65536 ? groups : 65536)),
+                     dim3(256), 0, stream, B, Bp, K, pieces);
   return hipGetLastError();
 }
 
