@@ -173,34 +173,62 @@ ProductPlan plan_matrix(int M, int K, int N, int cus) {
   return best;
 }
 
-// Rows of experts, by the mean number of rows of an expert that can have any.
-// 4 bits, us with 8 experts of 4096 x 22016 (FP16):
-//   mean                     4      8      12     16     48     64     96
-//   streaming kernel         74.6   89.8   91.5   112
-//   tiles of 32 x 128        84.9   83.7   87.1   89.5   129    160    228
-//   64 x 256                                             129    155    169
-//   (64 x 128 between or above: 135, 167, 198; 256 rows: 64 x 256 389,
-//   128 x 128 437, 256 x 256 522; 1024 rows: 1409, 1379, 1393)
-// e4m3, us with 64 experts of 2048 x 2816:
-//   mean                     4      16     32     64     96     128    192    384
-//   streaming kernel         59.7   82.2
-//   tiles of 32 x 128        59.0   65.5   74.3
-//   64 x 128                               69.4   80.5   100    120    162
-//   128 x 256                                            96.3   102    120    184
-//   (128 x 128: 94.8 at 96, 112, 135, 229; 64 x 256: 86.4 at 72, 143 at 192)
+// Rows of experts.  With few rows each, by their mean, the streaming kernel
+// (mean 4: 59.7 us against 59.0 in tiles of 32 rows for 64 experts of
+// 2048 x 2816 in e4m3, 74.6 against 84.9 for 8 of 4096 x 22016 in 4 bits; 8:
+// 89.8 and 83.7).  Beyond, the shape whose predicted time is least, from the
+// sum of tiles (half a tile an expert for unlike loads) as in plan_matrix: with
+// many tiles by the rate of each shape, with few by what one takes alone.
+// Constants measured at the first three of, in us:
+//                                           streaming  32 x 128  64 x *  128 x 256
+//   4 bits, 8 x 4096 x 22016, 16 rows each  112        89.5
+//     48                                               129       129
+//     96                                               228       169
+//   e4m3, 64 x 2048 x 2816, 16 rows each    82.2       65.5
+//     32                                               74.3      69.4
+//     96                                                         100     96.3
+//     192                                                        162     120
+//   e4m3, 16 x 8960 x 256, 36 rows each     25.5       35.3      40.9
+//     4 x 8192 x 256, 1024                  75.9       40.9      42.8    80.8
+//   4 bits, 8 x 8192 x 512, 32 rows each    20.6       35.1      73.0
+//     64 x 4864 x 320, 54 (BF16)            54.0       34.2      60.8
+//     4 x 8192 x 256, 1024                  66.6       50.1      74.6
+// (64 x *: 64 x 128 in e4m3, 64 x 256 in 4 bits.)
 // 4 bits stream four column blocks a workgroup: 16 tokens through 8 experts of
 // 4096 x 22016 93.2 us with two, 74.6 with four; with fewer workgroups than
 // compute units two, and eight waves (one token, 11008 x 4096: 25.6 and 19.4).
-ProductPlan plan_experts(bool f8, int rows, int used, int W, int cus) {
+constexpr Tile kExpertsF8[] = {
+    {2, 2, 0.48f, 0.28f, 1.5f}, {4, 2, 0.56f, 0.37f, 2.f}, {8, 4, 1.20f, 0.90f, 12.f}};
+constexpr Tile kExpertsI4[] = {{2, 2, 0.70f, 0.38f, 1.5f}, {4, 4, 1.20f, 1.10f, 8.f}};
+constexpr Tile kStreamF8 = {1, 2, 0.28f, 0.145f, 4.f}, kStreamI4 = {1, 4, 0.27f, 0.24f, 4.f};
+
+ProductPlan plan_experts(bool f8, int rows, int used, int K, int W, int cus) {
   const int mean = (rows + used - 1) / used;
-  if (f8) {
-    if (mean <= 6) return stream_plan(1, 2, 4, 4);
-    if (mean <= 24) return tile_plan(2, 2);
-    return mean <= 80 ? tile_plan(4, 2) : tile_plan(8, 4);
-  }
-  if (mean <= 7)
+  if (f8 ? mean <= 6 : mean <= 7) {
+    if (f8) return stream_plan(1, 2, 4, 4);
     return (int64_t)used * (W / 64) >= cus ? stream_plan(1, 4, 4, 3) : stream_plan(1, 2, 8, 3);
-  return mean <= 48 ? tile_plan(2, 2) : tile_plan(4, 4);
+  }
+  auto us = [&](const Tile& t, const ProductPlan& p) {
+    const float down = (float)mean / p.tm + 0.5f, across = (float)((W + p.tn - 1) / p.tn);
+    const float each = used * (down > 1.f ? down : 1.f) * across / cus;
+    const float block = each * t.shared > t.alone ? each * t.shared : t.alone;
+    return t.once + K / kBlockK * block;
+  };
+  ProductPlan best = f8 ? stream_plan(1, 2, 4, 4) : stream_plan(1, 4, 4, 3);
+  float least = us(f8 ? kStreamF8 : kStreamI4, best);
+  auto consider = [&](const Tile& t) {
+    const ProductPlan p = tile_plan(t.mb, t.nb);
+    const float time = us(t, p);
+    if (time < least) {
+      least = time;
+      best = p;
+    }
+  };
+  if (f8)
+    for (const Tile& t : kExpertsF8) consider(t);
+  else
+    for (const Tile& t : kExpertsI4) consider(t);
+  return best;
 }
 
 }  // namespace
@@ -209,7 +237,7 @@ ProductPlan make_product_plan(int format, int rows, int K, int N, int E, bool ga
   const int experts = E > 0 ? E : 1;
   const int used = rows < experts ? rows : experts;
   ProductPlan p = E == 0 ? plan_matrix(rows, K, N, cus)
-                         : plan_experts(format == kProdF8, rows, used, gate ? 2 * N : N, cus);
+                         : plan_experts(format == kProdF8, rows, used, K, gate ? 2 * N : N, cus);
   if (gate) p.tn /= 2;
   p.tiles_n = (N + p.tn - 1) / p.tn;
   // the most that the used experts' rows can make: sum of ceil(rows / tm)
