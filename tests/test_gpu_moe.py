@@ -717,6 +717,75 @@ def test_dense_replayed_from_a_graph():
         assert torch.equal(got, c) and got.abs().max() > 0
 
 
+def test_two_graphs_share_a_workspace():
+    """Products of unlike shapes that split K, captured over one workspace and
+    replayed in turn."""
+    torch = _torch()
+    say("dense two graphs")
+    shapes = [(100, 4096, 272), (60, 8192, 528), (33, 6144, 144)]
+    ws = max((w4.alloc_w8a8_workspace(*s) for s in shapes), key=lambda w: w.numel())
+    runs = []
+    for i, (M, K, N) in enumerate(shapes):
+        a, sa, b, sb = (cuda(x) for x in _dense(M, K, N, i))
+        assert w4.w8a8_workspace_bytes(M, K, N) > 0
+        packed = w4.alloc_w8a8_packed(K, N)
+        w4.w8a8_repack(b, packed)
+        c = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+        call = lambda a=a, sa=sa, p=packed, sb=sb, c=c: w4.w8a8_gemm(a, sa, p, sb, c, ws)
+        call()
+        torch.cuda.synchronize()
+        want = c.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, c, want, call))
+    for i in range(9):
+        graph, c, want, call = runs[i * i % 3 if i % 2 else i % 3]
+        c.zero_()
+        graph.replay() if i % 4 else call()
+        torch.cuda.synchronize()
+        assert torch.equal(c, want), i
+
+
+def test_layers_on_two_streams_at_once():
+    torch = _torch()
+    say("two streams")
+    layers = [Layer(8, 70, 2, 6, 384, 256, "bfloat16", 1), Layer(4, 150, 2, 8, 512, 256, "float16", 2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = []
+    for i, layer in enumerate(layers):
+        _fill(layer, np.random.default_rng(i), 0.05)
+        layer.run()
+        want.append(layer.out.clone())
+        layer.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for layer, stream in zip(layers, streams):
+            layer.run(stream=stream)
+    for layer, stream, w in zip(layers, streams, want):
+        stream.synchronize()
+        assert torch.equal(layer.out, w)
+
+
+@pytest.mark.parametrize("T,k", [(700, 3), (9000, 4)])       # one launch, and three
+def test_tables_of_most_experts_in_a_graph(T, k):
+    torch = _torch()
+    say("tables graph", T, k)
+    E = w4.MOE_MAX_EXPERTS
+    ids = torch.zeros((T, k), dtype=torch.int32, device="cuda")
+    starts, order, where = w4.alloc_moe_tables(T, k, E)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w4.moe_tables(ids, starts, order, where)
+    for i in range(3):
+        new = np.random.default_rng(i).integers(-2, E + 2, (T, k)).astype(np.int32)
+        ids.copy_(_torch().from_numpy(new))
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip((starts, order, where), ref.tables(new, E)):
+            assert np.array_equal(got.cpu().numpy(), w), i
+
+
 def test_binding_refusals_on_the_device():
     torch = _torch()
     x = torch.zeros((4, 256), dtype=torch.float16, device="cuda")

@@ -176,7 +176,10 @@ ProductPlan plan_matrix(int M, int K, int N, int cus) {
 // Rows of experts.  With few rows each, by their mean, the streaming kernel
 // (mean 4: 59.7 us against 59.0 in tiles of 32 rows for 64 experts of
 // 2048 x 2816 in e4m3, 74.6 against 84.9 for 8 of 4096 x 22016 in 4 bits; 8:
-// 89.8 and 83.7).  Beyond, the shape whose predicted time is least, from the
+// 89.8 and 83.7), unless K is too short for its waves and the columns are many
+// (5 rows each of 60 experts of K x 17664: 256 105 in e4m3 and 65.2 in 4 bits
+// against 72.7 and 46.7 in tiles; 1024 x 8192 100 and 69.0 against 102 and
+// 68.1).  Beyond, the shape whose predicted time is least, from the
 // sum of tiles (half a tile an expert for unlike loads) as in plan_matrix: with
 // many tiles by the rate of each shape, with few by what one takes alone.
 // Constants measured at the first three of, in us:
@@ -204,7 +207,8 @@ constexpr Tile kStreamF8 = {1, 2, 0.28f, 0.145f, 4.f}, kStreamI4 = {1, 4, 0.27f,
 
 ProductPlan plan_experts(bool f8, int rows, int used, int K, int W, int cus) {
   const int mean = (rows + used - 1) / used;
-  if (f8 ? mean <= 6 : mean <= 7) {
+  if (mean <= (f8 ? 6 : 7)) {
+    if (K < 8 * kBlockK && (int64_t)used * (W / 64) > 4 * (int64_t)cus) return tile_plan(2, 2);
     if (f8) return stream_plan(1, 2, 4, 4);
     return (int64_t)used * (W / 64) >= cus ? stream_plan(1, 4, 4, 3) : stream_plan(1, 2, 8, 3);
   }
