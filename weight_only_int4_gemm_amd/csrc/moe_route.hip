@@ -4,6 +4,7 @@
 
 #include "moe.hpp"
 #include "product.hpp"
+#include "tables_plan.hpp"
 #include "w4a16_moe.h"
 
 namespace w4a16 {
@@ -392,7 +393,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
 // tables
 // ---------------------------------------------------------------------------
 //
-// A stable counting sort.  Up to kOneLaunch choices every workgroup counts all
+// A stable counting sort.  Up to kTablesOneLaunch choices every workgroup counts all
 // choices of each expert, and those before its own chunk, for itself, so that
 // none waits for another, and then places its chunk.  Beyond, counting
 // everything in every workgroup costs more than launches (128 experts: 5.4 us
@@ -400,9 +401,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
 // made by one launch and kept in `order`, the second sums them and writes
 // `where`, the third `order`.
 
-constexpr int kTableThreads = 1024;
 constexpr int kTableWaves = kTableThreads / 64;
-constexpr int kOneLaunch = 16384;
 static_assert(MOE_MAX_EXPERTS <= kTableThreads, "one thread an expert");
 
 // counts[e] of ids[begin .. end), by all threads; `early` those before `border`.
@@ -576,7 +575,7 @@ __global__ __launch_bounds__(256) void moe_order_kernel(TablesArgs a) {
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= a.n) return;
   const int p = a.where[i];
-  if (p >= 0) a.order[p] = i;
+  if ((unsigned)p < (unsigned)a.n) a.order[p] = i;
   if (i >= a.starts[a.E]) a.order[i] = -1;
 }
 
@@ -655,11 +654,9 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_moe_tables(const TablesArgs& a, hipStream_t stream) {
-  const bool one = a.n <= kOneLaunch;
-  // chunks of a multiple of the threads, at most 256 of them
-  int chunk = kTableThreads;
-  while ((int64_t)chunk * 256 < a.n) chunk *= 2;
-  const dim3 groups(a.n > 0 ? (a.n + chunk - 1) / chunk : 1), block(kTableThreads);
+  const bool one = a.n <= kTablesOneLaunch;
+  const int chunk = table_chunk(a.n, a.E);
+  const dim3 groups(table_groups(a.n, chunk)), block(kTableThreads);
   const size_t bytes = (size_t)(2 + kTableWaves) * a.E * sizeof(int);
   if (bytes > 60 * 1024) {
     const hipError_t e = hipFuncSetAttribute(
@@ -672,9 +669,6 @@ hipError_t launch_moe_tables(const TablesArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(moe_tables_kernel, groups, block, bytes, stream, a, chunk);
     return hipGetLastError();
   }
-  // a chunk holds at least as many choices as there are experts, so the counts
-  // fit in `order`
-  static_assert(kTableThreads >= MOE_MAX_EXPERTS, "counts fit");
   hipLaunchKernelGGL(moe_count_kernel, groups, block, a.E * sizeof(int), stream, a, chunk, a.order);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
