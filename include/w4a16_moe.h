@@ -75,8 +75,10 @@ enum moe_activation {
  * weight 0, which every other call here leaves out.
  *
  * Without bias, and without marks of two summed, experts are compared by
- * their logits, whose order is that of the scores; otherwise scores, marks
- * and c are 64-bit numbers.  Weights are FP32.
+ * their logits, whose order is that of the scores; otherwise marks and c are
+ * 64-bit numbers.  So are the scores of a sigmoid, which are 0 for logits
+ * below -709, and with bias or marks of two those of a softmax too; else a
+ * softmax is in FP32.  Weights are FP32.
  *
  * logits  (device, read)  [T] rows of E values of type logits_type (enum
  *         moe_logits), `row` elements apart (at least E where T > 1), aligned
