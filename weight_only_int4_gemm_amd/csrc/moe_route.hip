@@ -413,8 +413,6 @@ constexpr int kTableWaves = kTableThreads / 64;
 static_assert(MOE_MAX_EXPERTS <= kTableThreads, "one thread an expert");
 
 // counts[e] of ids[begin .. end), by all threads; `early` those before `border`.
-// (Lanes of one expert counted before they are added, as in place_ids: 8192
-// choices of 8 experts 10.5 us with the routing, 10.0 so.)
 __device__ __forceinline__ void count_ids(const TablesArgs& a, int begin, int end, int* counts,
                                           int border, int* early) {
   constexpr int U = 4;

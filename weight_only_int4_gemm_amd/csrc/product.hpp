@@ -207,9 +207,11 @@ __device__ __forceinline__ uint16_t round16(float x, bool bf16) {
               : __builtin_bit_cast(uint16_t, (_Float16)x);
 }
 
-// x / (1 + exp(-x)) * u with the hardware exponential and reciprocal (a few
-// FP32 ulps); exp overflows to infinity for x below -88, whose reciprocal
-// gives the signed zero.
+// x / (1 + exp(-x)) * u with the hardware exponential and reciprocal.  The
+// exponent x log2(e) is rounded (the constant and the product), so the result
+// is off by up to (2 |x| + 8) 2^-24 of itself: 2^-17 at x = -60, where half a
+// step of the output is 2^-11 (FP16) or 2^-8.  Below x = -87.3 the reciprocal,
+// under 2^-126, may be 0, and y with it (|y| <= 2^-118 |u|).
 __device__ __forceinline__ float silu_gate(float x, float u) {
   return x * __builtin_amdgcn_rcpf(1.f + __expf(-x)) * u;
 }
