@@ -93,11 +93,25 @@ def _codes(t, what, numel, device):
     return _flat(t, t.dtype, what, numel, device)
 
 
+_INT = 2 ** 31 - 1      # sizes travel as C ints, which would lose their upper bits
+
+
 def _matrix(t, what):
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{what}: expected a matrix, got {tuple(shape)}")
-    return shape
+    try:
+        rows, cols = t.shape
+    except ValueError:
+        raise ValueError(f"{what}: expected a matrix, got {tuple(t.shape)}") from None
+    if rows > _INT or cols > _INT:
+        raise ValueError(f"{what}: no call takes {rows} x {cols}")
+    return rows, cols
+
+
+def _count(starts):
+    """Experts of ``starts`` [E + 1]."""
+    E = starts.numel() - 1
+    if E > _INT:
+        raise ValueError(f"starts: no call takes {E} experts")
+    return E
 
 
 def _strided(t, what, device):
@@ -209,10 +223,11 @@ def moe_tables(ids, starts, order, where, stream=None) -> None:
     dev = _start()
     i32 = _base._torch.int32
     T, k = _matrix(ids, "ids")
+    E = _count(starts)
     _check("moe_tables", _lib().moe_tables(
         _flat(ids, i32, "ids", 0, dev), _flat(starts, i32, "starts", 2, dev),
-        _flat(order, i32, "order", T * k, dev), _flat(where, i32, "where", T * k, dev), T, k,
-        starts.numel() - 1, _raw_stream(stream, dev)))
+        _flat(order, i32, "order", T * k, dev), _flat(where, i32, "where", T * k, dev), T, k, E,
+        _raw_stream(stream, dev)))
 
 
 def _experts(A, order, starts, C, activation, device):
@@ -220,7 +235,7 @@ def _experts(A, order, starts, C, activation, device):
     i32 = _base._torch.int32
     a_rows, K = _matrix(A, "A")
     rows, N = _matrix(C, "C")
-    E = starts.numel() - 1
+    E = _count(starts)
     if order is None and a_rows < rows:
         raise ValueError(f"A: {a_rows} rows for {rows} rows of C")
     return (a_rows, K, rows, N, E, N * (2 if activation == MOE_ACT_SILU_GATE else 1),
